@@ -407,6 +407,150 @@ int bgtq_decode_attn_noalloc(const bgtq_plan* plan, void* stream, const void* q_
                              float softmax_scale, int32_t* dev_status);
 
 /*
+ * ---- Bounded caches: a sliding window with sinks, accumulated attention
+ * weights, eviction.  The paper has no counterpart: its cache grows with the
+ * sequence, and these calls keep what a step reads, or holds, to a budget.
+ * All of them work on the packed records; none dequantises the cache.  Row i
+ * (position i) sees position j under (sinks, window) when
+ *   j <= i  and  (j < sinks  or  j > i - window).
+ * sinks >= 0, window >= 1; a window at least as long as the sequence is plain
+ * causal attention.
+ */
+
+/* Workspace bytes of bgtq_decode_window_attn for `batch` sequences no longer
+ * than max_len (zero-filled once before first use; every call leaves its
+ * counters zero).  Errors: INVALID_ARG. */
+int bgtq_decode_window_workspace(const bgtq_plan* plan, int batch, int64_t max_len, int64_t sinks, int64_t window,
+                                 size_t* bytes);
+
+/*
+ * bgtq_decode_window_attn — bgtq_decode_attn (k_new, v_new, pos_new NULL) or
+ * bgtq_decode_step (all three given) of which the token sees positions
+ * [0, sinks) and [seq_len - window, seq_len) only.
+ *   sinks, window  as above
+ *   out, softmax_scale, cache (contiguous, paged, with a recent-key buffer),
+ *   seq_lens, k_new, v_new, pos_new  as bgtq_decode_step; the new token is
+ *                appended wherever pos_new says, seen or not
+ *   max_len      host bound of seq_lens; a longer sequence is cut to it and
+ *                BGTQ_STATUS_SEQLEN_CAPACITY set
+ *   workspace    16-byte aligned device scratch of bgtq_decode_window_workspace
+ *                bytes; two calls that may overlap on the GPU need two
+ * Only the records of 16-position tiles with a visible position are read: a
+ * page of a paged cache without one may be unmapped (-1) and given away.
+ * An empty sequence yields zeros.  With window >= seq_len the output equals
+ * bgtq_decode_attn's bit for bit.
+ * Errors: INVALID_ARG (pointers, alignment, sinks < 0, window < 1, only some
+ * of the new token's arguments), WORKSPACE, UNSUPPORTED (bK > 3, bV > 4, more
+ * than 65535 sequences), CUDA.
+ */
+int bgtq_decode_window_attn(const bgtq_plan* plan, void* stream, const void* q_fp16, const void* k_new_fp16,
+                            const void* v_new_fp16, const int32_t* pos_new, const bgtq_cache* cache,
+                            const int32_t* seq_lens, int64_t max_len, int batch, int64_t sinks, int64_t window,
+                            void* out, int out_dtype, float softmax_scale, void* workspace, size_t ws_bytes,
+                            int32_t* dev_status);
+
+/* Workspace bytes of bgtq_decode_score_attn: the decode's, and 4 bytes for
+ * every (sequence, query head, position up to max_len).  Zero-filled once
+ * before first use. */
+int bgtq_decode_score_workspace(const bgtq_plan* plan, int batch, int64_t max_len, size_t* bytes);
+
+/*
+ * bgtq_decode_score_attn — bgtq_decode_attn, or with k_new, v_new, pos_new
+ * bgtq_decode_step, that also gives every cached position its attention
+ * weight:
+ *   scores_out[b][h][t] = scores_in[b][h][t] + sum over the G query heads g of
+ *                         KV head h of softmax_t(scale q_g . k_t),  t < seq_len
+ *   scores_in, scores_out  device, [batch][H][capacity] float, 8-byte aligned,
+ *                one array or two that do not overlap (also for a paged
+ *                cache: by position); positions from seq_len on are neither
+ *                read nor written; a new token's position starts from 0
+ *                whatever scores_in holds there
+ * Two launches on `stream`; sums in float32, the query heads in order (the
+ * same bits on every run).  out equals bgtq_decode_attn's bit for bit.
+ * Other arguments and errors as bgtq_decode_window_attn.
+ */
+int bgtq_decode_score_attn(const bgtq_plan* plan, void* stream, const void* q_fp16, const void* k_new_fp16,
+                           const void* v_new_fp16, const int32_t* pos_new, const bgtq_cache* cache,
+                           const int32_t* seq_lens, int64_t max_len, int batch, const float* scores_in,
+                           float* scores_out, void* out, int out_dtype, float softmax_scale, void* workspace,
+                           size_t ws_bytes, int32_t* dev_status);
+
+/*
+ * bgtq_prefill_window_attn — bgtq_prefill_attn under (sinks, window), with the
+ * rows' log-sum-exp.
+ *   lse          device, [batch][H*G][t] float or NULL: natural logarithm of
+ *                the sum of exp(softmax_scale q_i . k_j) over the keys j that
+ *                row i sees
+ * Records, other arguments and errors as bgtq_prefill_attn; also INVALID_ARG
+ * for sinks < 0 or window < 1.  Key tiles that no row of a query block sees
+ * are neither loaded nor multiplied.
+ */
+int bgtq_prefill_window_attn(const bgtq_plan* plan, void* stream, const void* q_fp16, const void* k_fp16,
+                             const void* v_fp16, int batch, int t, int64_t sinks, int64_t window,
+                             const bgtq_cache* cache, void* out, int out_dtype, float softmax_scale, float* lse,
+                             int32_t* dev_status);
+
+/* Workspace bytes of bgtq_prefill_score (may be 0; contents not kept). */
+int bgtq_prefill_score_workspace(const bgtq_plan* plan, int batch, int t, int row0, size_t* bytes);
+
+/*
+ * bgtq_prefill_score — the attention weights that a prompt's rows give to its
+ * positions:
+ *   scores[b][h][j] = sum over the query heads g of KV head h and the rows
+ *                     i >= row0 that see j of exp(scale q_gi . k_j - lse_gi)
+ *   q_fp16, k_fp16  as bgtq_prefill_attn (the prompt's own tokens)
+ *   lse          device, [batch][H*G][t] float as bgtq_prefill_window_attn
+ *                wrote it for the same (sinks, window); rows before row0 are
+ *                not read; a row whose lse is -inf gives nothing
+ *   row0         0 <= row0 <= t: 0 counts every row, t - n the last n
+ *   scores       device, [batch][H][score_stride] float: positions 0 .. t-1
+ *                overwritten, the rest left; score_stride >= t
+ *   workspace    device, 16-byte aligned, bgtq_prefill_score_workspace bytes
+ *                (NULL if 0)
+ * fp16 tensor-core products, float32 sums in a fixed order.
+ * Errors: INVALID_ARG, UNSUPPORTED (sizes past 2^31 rows, t > 8388480, more
+ * than 65535 sequences x KV heads), WORKSPACE, CUDA.
+ */
+int bgtq_prefill_score(const bgtq_plan* plan, void* stream, const void* q_fp16, const void* k_fp16, const float* lse,
+                       int batch, int t, int row0, int64_t sinks, int64_t window, float softmax_scale, float* scores,
+                       int64_t score_stride, void* workspace, size_t ws_bytes, int32_t* dev_status);
+
+/*
+ * bgtq_evict — cut every (sequence, KV head) of a packed cache to `keep`
+ * positions, into another packed cache.
+ * Of a sequence of n > keep positions the first `sinks`, the last `recent`
+ * and, of those between, the keep - sinks - recent of the largest score stay;
+ * equal scores: the lower position (-0 equals +0, NaN is below every number).
+ * The KV heads choose for themselves.  The kept positions' records, norms and
+ * scores move, in position order, to positions 0 .. keep-1 of the
+ * destination, codes bit for bit; n <= keep: all of them.  (Keys keep the
+ * rotation of the position they were cached at.)
+ *   cache        source descriptor, contiguous or paged, without a recent-key
+ *                buffer
+ *   scores       device, [batch][H][capacity] float
+ *   seq_lens     device, [batch] int32
+ *   max_len      host bound of seq_lens; a longer sequence is cut to it and
+ *                BGTQ_STATUS_SEQLEN_CAPACITY set
+ *   keep, sinks, recent  keep >= 1, sinks + recent <= keep
+ *   dst          destination descriptor, without a recent-key buffer, of at
+ *                least min(keep, max_len) positions.  Its buffers must not
+ *                overlap the source's; two paged descriptors of one pool are
+ *                accepted when their page tables share no page (not checked).
+ *                Positions past the kept ones are left as they are, also the
+ *                odd half of a last V pair record.
+ *   dst_scores   device, [batch][H][dst capacity] float
+ *   dst_lens     device, [batch] int32: min(n, keep)
+ *   kept         device, [batch][H][keep] int32: the source positions, -1
+ *                past them
+ * Two launches; every result is the same on every run.
+ * Errors: INVALID_ARG, UNSUPPORTED (a recent-key buffer, more than 65535
+ * sequences), CAPACITY, CUDA.  An unmapped page sets BGTQ_STATUS_PAGE_RANGE.
+ */
+int bgtq_evict(const bgtq_plan* plan, void* stream, const bgtq_cache* cache, const float* scores,
+               const int32_t* seq_lens, int64_t max_len, int batch, int64_t keep, int64_t sinks, int64_t recent,
+               const bgtq_cache* dst, float* dst_scores, int32_t* dst_lens, int32_t* kept, int32_t* dev_status);
+
+/*
  * bgtq_logit_mae — RoPE-logit fidelity diagnostic: for every query head, the
  * mean absolute error of the attention logits computed from the packed keys
  * against the keys as given,

@@ -725,3 +725,56 @@ def chunk_prefill_attention(q_fp16, khat_prefix, vhat_prefix, k_fp16, v_fp16, sc
         p = np.exp(s)
         out[:, r0:r1] = np.einsum("gij,jd->gid", p, vals[:n]) / p.sum(axis=2, keepdims=True)
     return out
+
+
+# =============================================================================
+# Bounded caches (no counterpart in the paper; the packed cache is its
+# substrate).  Reading R23, sliding window with sinks: a row at position i sees
+# position j when j <= i and (j < sinks or j > i - window).  Reading R24,
+# accumulated weights: a position's score is the sum of the softmax weights
+# that rows gave it, over the query heads of its KV head.  Reading R25,
+# eviction: of n > keep positions the first `sinks`, the last `recent` and the
+# best of the others by score (ties: the lower position; NaN below every
+# number, -0 = +0) stay, in position order.
+# =============================================================================
+
+
+def visible(i, j, sinks: int, window: int):
+    return (j <= i) & ((j < sinks) | (j > i - window))
+
+
+def decode_visible(n: int, sinks: int, window: int) -> np.ndarray:
+    """Positions that the token at position n - 1 of a sequence sees."""
+    j = np.arange(n)
+    return j[visible(n - 1, j, sinks, window)]
+
+
+def attention_weights(q_fp16, khat, scale: float = 1.0 / math.sqrt(D)) -> np.ndarray:
+    """softmax_t(scale q_g . k_t), float64 [G][T]."""
+    s = (np.asarray(q_fp16, dtype=np.float16).astype(np.float64) @ np.asarray(khat, dtype=np.float64).T) * scale
+    p = np.exp(s - s.max(axis=1, keepdims=True))
+    return p / p.sum(axis=1, keepdims=True)
+
+
+def prefill_window(q_fp16, k_fp16, v_fp16, sinks: int, window: int, scale: float = 1.0 / math.sqrt(D)):
+    """q [G][T][128], k, v [T][128] -> (out [G][T][128], lse [G][T], weights [G][T][T]), float64."""
+    q = np.asarray(q_fp16, dtype=np.float16).astype(np.float64)
+    k = np.asarray(k_fp16, dtype=np.float16).astype(np.float64)
+    v = np.asarray(v_fp16, dtype=np.float16).astype(np.float64)
+    t = k.shape[0]
+    s = np.einsum("gid,jd->gij", q, k) * scale
+    s = np.where(visible(np.arange(t)[:, None], np.arange(t)[None, :], sinks, window)[None], s, -np.inf)
+    m = s.max(axis=2, keepdims=True)
+    e = np.exp(s - m)
+    l = e.sum(axis=2, keepdims=True)
+    return np.einsum("gij,jd->gid", e, v) / l, (m + np.log(l))[:, :, 0], e / l
+
+
+def evict_positions(scores, n: int, keep: int, sinks: int, recent: int) -> np.ndarray:
+    """Positions of a sequence of n that stay, ascending."""
+    if n <= keep:
+        return np.arange(n)
+    x = np.asarray(scores[:n], dtype=np.float64)
+    mid = [j for j in range(sinks, n - recent)]
+    mid.sort(key=lambda j: (bool(np.isnan(x[j])), -x[j] if not np.isnan(x[j]) else 0.0, j))
+    return np.array(sorted(list(range(sinks)) + mid[: keep - sinks - recent] + list(range(n - recent, n))), dtype=np.int64)

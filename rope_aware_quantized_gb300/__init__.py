@@ -387,6 +387,159 @@ def bgtq_prefill_chunk_attn(plan: Plan, q_fp16, k_fp16, v_fp16, pos_start, cache
                                          scale, _ptr(workspace), workspace.numel(), _ptr(status)))
 
 
+# ----------------------------------------------------------------------------- bounded caches
+
+def _out_dtype(out) -> int:
+    import torch
+    if out.dtype == torch.float32:
+        return 1
+    if out.dtype == torch.float16:
+        return 0
+    raise ValueError("out must be float16 or float32")
+
+
+def _need(x, name: str, dtype, shape):
+    """A contiguous CUDA tensor of this type and shape."""
+    if x.dtype != dtype or tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    if not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+
+
+def _decode_args(plan: Plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new):
+    import torch
+    batch = q_fp16.shape[0]
+    _need(q_fp16, "q", torch.float16, (batch, plan.n_kv_heads * plan.group, HEAD_DIM))
+    _need(out, "out", out.dtype, q_fp16.shape)
+    _need(seq_lens, "seq_lens", torch.int32, (batch,))
+    if cache.batch < batch:
+        raise ValueError("the cache holds fewer sequences than q")
+    if (k_new is None) != (v_new is None) or (k_new is None) != (pos_new is None):
+        raise ValueError("k_new, v_new and pos_new are given together or not at all")
+    if k_new is not None:
+        _need(k_new, "k_new", torch.float16, (batch, plan.n_kv_heads, HEAD_DIM))
+        _need(v_new, "v_new", torch.float16, (batch, plan.n_kv_heads, HEAD_DIM))
+        _need(pos_new, "pos_new", torch.int32, (batch,))
+    return batch
+
+
+def bgtq_decode_window_workspace(plan: Plan, batch: int, max_len: int, sinks: int, window: int) -> int:
+    n = C.c_size_t()
+    _check(lib().bgtq_decode_window_workspace(plan.handle, batch, max_len, sinks, window, C.byref(n)))
+    return n.value
+
+
+def bgtq_decode_window_attn(plan: Plan, q_fp16, cache: Cache, seq_lens, max_len: int, sinks: int, window: int, out,
+                            workspace, k_new=None, v_new=None, pos_new=None, softmax_scale: float | None = None,
+                            status=None, stream=None):
+    """Decode attention over positions [0, sinks) and [seq_len - window, seq_len) of the packed cache
+    (q: [B][H*G][128] float16; out: same shape, float16 or float32; workspace: a zeroed uint8 CUDA
+    tensor of bgtq_decode_window_workspace bytes).  With k_new, v_new ([B][H][128] float16) and
+    pos_new ([B] int32) the new token is quantize-appended first, in the same launch."""
+    batch = _decode_args(plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new)
+    scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
+    _check(lib().bgtq_decode_window_attn(plan.handle, _stream(stream), _ptr(q_fp16), _ptr(k_new), _ptr(v_new), _ptr(pos_new),
+                                         C.byref(cache.desc), _ptr(seq_lens), max_len, batch, sinks, window, _ptr(out),
+                                         _out_dtype(out), scale, _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(), _ptr(status)))
+
+
+def bgtq_decode_score_workspace(plan: Plan, batch: int, max_len: int) -> int:
+    n = C.c_size_t()
+    _check(lib().bgtq_decode_score_workspace(plan.handle, batch, max_len, C.byref(n)))
+    return n.value
+
+
+def bgtq_decode_score_attn(plan: Plan, q_fp16, cache: Cache, seq_lens, max_len: int, scores_in, scores_out, out, workspace,
+                           k_new=None, v_new=None, pos_new=None, softmax_scale: float | None = None, status=None,
+                           stream=None):
+    """Decode attention over the packed cache that also gives every cached position its attention
+    weight: scores_out[b][h][t] = scores_in[b][h][t] + the weights of position t summed over the
+    query heads of KV head h, t < seq_len ([B][H][capacity] float32 each; scores_out may be
+    scores_in; positions from seq_len on are left as they are).  Other arguments as
+    bgtq_decode_window_attn; a new token's position starts from a score of 0."""
+    import torch
+    batch = _decode_args(plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new)
+    for x, name in ((scores_in, "scores_in"), (scores_out, "scores_out")):
+        _need(x, name, torch.float32, (batch, plan.n_kv_heads, cache.capacity))
+    scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
+    _check(lib().bgtq_decode_score_attn(plan.handle, _stream(stream), _ptr(q_fp16), _ptr(k_new), _ptr(v_new), _ptr(pos_new),
+                                        C.byref(cache.desc), _ptr(seq_lens), max_len, batch, _ptr(scores_in),
+                                        _ptr(scores_out), _ptr(out), _out_dtype(out), scale, _ptr(workspace),
+                                        workspace.numel() * workspace.element_size(), _ptr(status)))
+
+
+def bgtq_prefill_window_attn(plan: Plan, q_fp16, k_fp16, v_fp16, cache: Cache, sinks: int, window: int, out, lse=None,
+                             softmax_scale: float | None = None, status=None, stream=None):
+    """bgtq_prefill_attn under a sliding window with sinks: row i attends the keys j <= i with
+    j < sinks or j > i - window (window >= T: plain causal attention).  lse: an optional
+    [B][H*G][T] float32 tensor that receives every row's log-sum-exp of its visible logits."""
+    import torch
+    b, hq, t, d = q_fp16.shape
+    _need(q_fp16, "q", torch.float16, (b, plan.n_kv_heads * plan.group, t, HEAD_DIM))
+    _need(k_fp16, "k", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM))
+    _need(v_fp16, "v", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM))
+    _need(out, "out", out.dtype, q_fp16.shape)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, (b, hq, t))
+    if cache.batch < b:
+        raise ValueError("the cache holds fewer sequences than q")
+    scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
+    _check(lib().bgtq_prefill_window_attn(plan.handle, _stream(stream), _ptr(q_fp16), _ptr(k_fp16), _ptr(v_fp16), b, t, sinks,
+                                          window, C.byref(cache.desc), _ptr(out), _out_dtype(out), scale, _ptr(lse),
+                                          _ptr(status)))
+
+
+def bgtq_prefill_score_workspace(plan: Plan, batch: int, t: int, row0: int = 0) -> int:
+    n = C.c_size_t()
+    _check(lib().bgtq_prefill_score_workspace(plan.handle, batch, t, row0, C.byref(n)))
+    return n.value
+
+
+def bgtq_prefill_score(plan: Plan, q_fp16, k_fp16, lse, scores, workspace=None, row0: int = 0, sinks: int = 0,
+                       window: int | None = None, softmax_scale: float | None = None, status=None, stream=None):
+    """Attention weights that the prompt's rows row0 .. T-1 give to every position, from their
+    log-sum-exp: scores[b][h][j] = sum over the query heads of KV head h and the rows i that see j
+    of exp(scale q_i . k_j - lse_i), j < T, overwritten (q: [B][H*G][T][128], k: [B][H][T][128]
+    float16; lse: [B][H*G][T] float32; scores: [B][H][>= T] float32, for instance a cache's
+    [B][H][capacity]).  sinks, window as bgtq_prefill_window_attn (window None: no window);
+    workspace: a uint8 CUDA tensor of bgtq_prefill_score_workspace bytes (None if that is 0)."""
+    import torch
+    b, hq, t, d = q_fp16.shape
+    _need(q_fp16, "q", torch.float16, (b, plan.n_kv_heads * plan.group, t, HEAD_DIM))
+    _need(k_fp16, "k", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM))
+    _need(lse, "lse", torch.float32, (b, hq, t))
+    _need(scores, "scores", torch.float32, (b, plan.n_kv_heads, scores.shape[-1]))
+    scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
+    _check(lib().bgtq_prefill_score(plan.handle, _stream(stream), _ptr(q_fp16), _ptr(k_fp16), _ptr(lse), b, t, row0, sinks,
+                                    max(t, 1) if window is None else window, scale, _ptr(scores), scores.shape[-1],
+                                    _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                    _ptr(status)))
+
+
+def bgtq_evict(plan: Plan, cache: Cache, scores, seq_lens, max_len: int, keep: int, sinks: int, recent: int, dst: Cache,
+               dst_scores, dst_lens, kept, status=None, stream=None):
+    """Cut every (sequence, KV head) of a packed cache to `keep` positions: the first `sinks`, the
+    last `recent` and, of those between, the ones of the largest score (ties: the lower position),
+    in position order into `dst`, another cache of at least min(keep, max_len) positions; a shorter
+    sequence is kept whole.  scores [B][H][capacity], dst_scores [B][H][dst capacity] float32;
+    seq_lens, dst_lens [B] int32; kept [B][H][keep] int32: the source positions, -1 past them."""
+    import torch
+    batch = seq_lens.shape[0]
+    _need(seq_lens, "seq_lens", torch.int32, (batch,))
+    _need(scores, "scores", torch.float32, (batch, plan.n_kv_heads, cache.capacity))
+    _need(dst_scores, "dst_scores", torch.float32, (batch, plan.n_kv_heads, dst.capacity))
+    _need(dst_lens, "dst_lens", torch.int32, (batch,))
+    _need(kept, "kept", torch.int32, (batch, plan.n_kv_heads, keep))
+    if cache.batch < batch or dst.batch < batch:
+        raise ValueError("a cache holds fewer sequences than seq_lens")
+    _check(lib().bgtq_evict(plan.handle, _stream(stream), C.byref(cache.desc), _ptr(scores), _ptr(seq_lens), max_len, batch,
+                            keep, sinks, recent, C.byref(dst.desc), _ptr(dst_scores), _ptr(dst_lens), _ptr(kept),
+                            _ptr(status)))
+
+
 def bgtq_dequant_debug(plan: Plan, cache: Cache, b: int, head: int, t0: int, t1: int, k_out=None, v_out=None,
                        codec_domain: bool = False, stream=None):
     _check(lib().bgtq_dequant_debug(plan.handle, _stream(stream), C.byref(cache.desc), cache.batch, b, head, t0, t1,
@@ -397,5 +550,7 @@ __all__ = [
     "BgtqError", "Plan", "Cache", "CacheView", "bgtq_alloc_bits", "bgtq_plan_create", "bgtq_cache_bytes",
     "bgtq_quantize_append", "bgtq_decode_attn_workspace", "bgtq_decode_attn", "bgtq_decode_step",
     "bgtq_decode_attn_noalloc", "bgtq_logit_mae", "bgtq_prefill_attn", "bgtq_prefill_chunk_workspace", "bgtq_prefill_chunk_attn",
-    "bgtq_plan_save", "bgtq_plan_load", "bgtq_dequant_debug",
+    "bgtq_plan_save", "bgtq_plan_load", "bgtq_dequant_debug", "bgtq_decode_window_workspace", "bgtq_decode_window_attn",
+    "bgtq_decode_score_workspace", "bgtq_decode_score_attn", "bgtq_prefill_window_attn", "bgtq_prefill_score_workspace",
+    "bgtq_prefill_score", "bgtq_evict",
 ]

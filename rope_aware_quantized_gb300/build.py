@@ -31,6 +31,12 @@ SOURCES = [
     ("decode_attn.cu", []),
     ("decode_attn_paged.cu", []),
     ("decode_attn_noalloc.cu", []),
+    ("decode_window.cu", []),
+    ("decode_window_paged.cu", []),
+    ("decode_score.cu", []),
+    ("decode_score_paged.cu", []),
+    ("evict.cu", []),
+    ("prefill_score.cu", []),
     ("fidelity.cu", []),
     ("prefill_attn.cu", []),
     ("prefill_chunk.cu", []),

@@ -973,6 +973,256 @@ int bgtq_prefill_chunk_attn(const bgtq_plan* p, void* stream, const void* q, con
     return BGTQ_OK;
 }
 
+// ---- bounded caches: sliding window and sinks, accumulated weights, eviction
+
+}  // extern "C"
+
+namespace {
+
+// Arguments that the windowed and the scoring decode share.
+int check_decode_call(const bgtq_plan* p, const void* q, const void* k_new, const void* v_new, const int32_t* pos_new,
+                      const bgtq_cache* c, const int32_t* seq_lens, int64_t max_len, int batch, const void* out,
+                      int out_dtype, float scale, const void* ws) {
+    if (!p) return set_error(BGTQ_ERR_INVALID_ARG, "plan is NULL");
+    const int rc = check_cache(p, c);
+    if (rc) return rc;
+    if (batch < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and max_len must be >= 0");
+    if (batch > 65535) return set_error(BGTQ_ERR_UNSUPPORTED, "at most 65535 sequences per call");
+    if (batch == 0) return BGTQ_OK;
+    if (!q || !seq_lens || !out || !ws) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
+    if ((!k_new || !v_new || !pos_new) && (k_new || v_new || pos_new))
+        return set_error(BGTQ_ERR_INVALID_ARG, "k_new, v_new and pos_new are given together or not at all");
+    if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 7)
+        return set_error(BGTQ_ERR_INVALID_ARG, "k_new and v_new must be 8-byte aligned");
+    if (reinterpret_cast<uintptr_t>(q) & 3) return set_error(BGTQ_ERR_INVALID_ARG, "q must be 4-byte aligned");
+    if (reinterpret_cast<uintptr_t>(ws) & 15) return set_error(BGTQ_ERR_INVALID_ARG, "workspace must be 16-byte aligned");
+    if (out_dtype != 0 && out_dtype != 1) return set_error(BGTQ_ERR_INVALID_ARG, "out_dtype must be 0 (half) or 1 (float)");
+    if (reinterpret_cast<uintptr_t>(out) & (out_dtype ? 3 : 1))
+        return set_error(BGTQ_ERR_INVALID_ARG, "out must be aligned to its type");
+    if (p->bk > 3) return set_error(BGTQ_ERR_UNSUPPORTED, "decode supports bits_per_key <= 384");
+    if (p->bv > 4) return set_error(BGTQ_ERR_UNSUPPORTED, "decode supports v_bits <= 4");
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return set_error(BGTQ_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+    return BGTQ_OK;
+}
+
+int check_window(int64_t sinks, int64_t window) {
+    if (sinks < 0) return set_error(BGTQ_ERR_INVALID_ARG, "sinks must be >= 0");
+    if (window < 1) return set_error(BGTQ_ERR_INVALID_ARG, "window must be >= 1");
+    return BGTQ_OK;
+}
+
+// The parts of a scoring decode's workspace: the decode's own, then every
+// query head's softmax statistics, then the logits (whole tiles).
+struct ScoreWorkspace {
+    size_t stat, logit, bytes;
+    int64_t stride;
+};
+ScoreWorkspace score_workspace(const bgtq_plan& p, int batch, int64_t max_len, const SplitPlan& sp) {
+    auto up = [](size_t n) { return (n + 255) / 256 * 256; };
+    const size_t rows = (size_t)batch * p.H * p.G;
+    ScoreWorkspace w;
+    w.stride = (max_len + 15) / 16 * 16;
+    w.stat = up(decode_workspace_bytes(p, batch, sp));
+    w.logit = w.stat + up(rows * sizeof(float2));
+    w.bytes = w.logit + up(rows * (size_t)w.stride * sizeof(float));
+    return w;
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bgtq_decode_window_workspace(const bgtq_plan* p, int batch, int64_t max_len, int64_t sinks, int64_t window,
+                                 size_t* bytes) {
+    if (!p || !bytes) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
+    if (batch < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and max_len must be >= 0");
+    const int rc = check_window(sinks, window);
+    if (rc) return rc;
+    *bytes = decode_workspace_bytes(*p, batch, decode_split(*p, batch, decode_window_positions(max_len, sinks, window)));
+    return BGTQ_OK;
+}
+
+int bgtq_decode_window_attn(const bgtq_plan* p, void* stream, const void* q, const void* k_new, const void* v_new,
+                            const int32_t* pos_new, const bgtq_cache* c, const int32_t* seq_lens, int64_t max_len,
+                            int batch, int64_t sinks, int64_t window, void* out, int out_dtype, float scale, void* ws,
+                            size_t ws_bytes, int32_t* status) {
+    int rc = check_decode_call(p, q, k_new, v_new, pos_new, c, seq_lens, max_len, batch, out, out_dtype, scale, ws);
+    if (rc) return rc;
+    if ((rc = check_window(sinks, window))) return rc;
+    if (batch == 0) return BGTQ_OK;
+    if ((rc = check_plan(p))) return rc;
+    max_len = std::min(max_len, c->capacity);
+    const SplitPlan sp = decode_split(*p, batch, decode_window_positions(max_len, sinks, window));
+    const size_t need = decode_workspace_bytes(*p, batch, sp);
+    if (ws_bytes < need) return set_error(BGTQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+    DecodeExtra x;
+    x.max_len = max_len;
+    x.window = true;
+    x.sinks = (int)std::min(sinks, max_len);
+    x.span = (int)std::max<int64_t>(std::min(window, max_len), 1);
+    const cudaError_t e = launch_decode(*p, (cudaStream_t)stream, q, *c, seq_lens, batch, sp, out, out_dtype, scale, ws,
+                                        status, k_new, v_new, pos_new, x);
+    if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "decode_window_attn launch: %s", cudaGetErrorString(e));
+    return BGTQ_OK;
+}
+
+int bgtq_decode_score_workspace(const bgtq_plan* p, int batch, int64_t max_len, size_t* bytes) {
+    if (!p || !bytes) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
+    if (batch < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and max_len must be >= 0");
+    *bytes = score_workspace(*p, batch, max_len, decode_split(*p, batch, max_len)).bytes;
+    return BGTQ_OK;
+}
+
+int bgtq_decode_score_attn(const bgtq_plan* p, void* stream, const void* q, const void* k_new, const void* v_new,
+                           const int32_t* pos_new, const bgtq_cache* c, const int32_t* seq_lens, int64_t max_len,
+                           int batch, const float* scores_in, float* scores_out, void* out, int out_dtype, float scale,
+                           void* ws, size_t ws_bytes, int32_t* status) {
+    int rc = check_decode_call(p, q, k_new, v_new, pos_new, c, seq_lens, max_len, batch, out, out_dtype, scale, ws);
+    if (rc) return rc;
+    if (batch == 0) return BGTQ_OK;
+    if (!scores_in || !scores_out) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
+    if ((reinterpret_cast<uintptr_t>(scores_in) | reinterpret_cast<uintptr_t>(scores_out)) & 7)
+        return set_error(BGTQ_ERR_INVALID_ARG, "scores must be 8-byte aligned");
+    const size_t nb = (size_t)batch * p->H * (size_t)c->capacity * sizeof(float);
+    if (scores_in != scores_out && overlap(scores_in, nb, scores_out, nb))
+        return set_error(BGTQ_ERR_INVALID_ARG, "scores_in and scores_out are one array or do not overlap");
+    if ((rc = check_plan(p))) return rc;
+    max_len = std::min(max_len, c->capacity);
+    const SplitPlan sp = decode_split(*p, batch, max_len);
+    const ScoreWorkspace w = score_workspace(*p, batch, max_len, sp);
+    if (ws_bytes < w.bytes) return set_error(BGTQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, w.bytes);
+    DecodeExtra x;
+    x.max_len = max_len;
+    x.stat = reinterpret_cast<float2*>(static_cast<char*>(ws) + w.stat);
+    x.logit = reinterpret_cast<float*>(static_cast<char*>(ws) + w.logit);
+    x.logit_stride = w.stride;
+    cudaError_t e = launch_decode(*p, (cudaStream_t)stream, q, *c, seq_lens, batch, sp, out, out_dtype, scale, ws, status,
+                                  k_new, v_new, pos_new, x);
+    if (e == cudaSuccess)
+        e = launch_score_add(*p, (cudaStream_t)stream, *c, seq_lens, max_len, batch, x, pos_new, scores_in, scores_out);
+    if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "decode_score_attn launch: %s", cudaGetErrorString(e));
+    return BGTQ_OK;
+}
+
+int bgtq_prefill_window_attn(const bgtq_plan* p, void* stream, const void* q, const void* k, const void* v, int batch,
+                             int t, int64_t sinks, int64_t window, const bgtq_cache* c, void* out, int out_dtype,
+                             float scale, float* lse, int32_t* status) {
+    if (!p) return set_error(BGTQ_ERR_INVALID_ARG, "plan is NULL");
+    int rc = check_cache(p, c);
+    if (rc) return rc;
+    if ((rc = check_window(sinks, window))) return rc;
+    if (batch < 0 || t < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and t must be >= 0");
+    if (t > c->capacity) return set_error(BGTQ_ERR_CAPACITY, "t = %d exceeds the cache capacity", t);
+    if (batch == 0 || t == 0) return BGTQ_OK;
+    if (!q || !k || !v || !out) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15)
+        return set_error(BGTQ_ERR_INVALID_ARG, "q, k and v must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(out) & 15) return set_error(BGTQ_ERR_INVALID_ARG, "out must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(lse) & 3) return set_error(BGTQ_ERR_INVALID_ARG, "lse must be 4-byte aligned");
+    if (out_dtype != 0 && out_dtype != 1) return set_error(BGTQ_ERR_INVALID_ARG, "out_dtype must be 0 (half) or 1 (float)");
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return set_error(BGTQ_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+    if (batch > 65535) return set_error(BGTQ_ERR_UNSUPPORTED, "at most 65535 sequences per call");
+    if ((uint64_t)batch * p->H * p->G * (uint64_t)t + 128 >= (1ull << 31))
+        return set_error(BGTQ_ERR_UNSUPPORTED, "batch * query heads * t must stay below 2^31 - 128");
+    if ((rc = check_plan(p))) return rc;
+    const PrefillWindow w = {(int)std::min<int64_t>(sinks, t), (int)std::min<int64_t>(window, t), lse};
+    const cudaError_t e =
+        launch_prefill(*p, (cudaStream_t)stream, q, k, v, batch, t, *c, out, out_dtype, scale, status, &w);
+    if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "prefill_window_attn launch: %s", cudaGetErrorString(e));
+    return BGTQ_OK;
+}
+
+int bgtq_prefill_score_workspace(const bgtq_plan* p, int batch, int t, int row0, size_t* bytes) {
+    if (!p || !bytes) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
+    if (batch < 0 || t < 0 || row0 < 0 || row0 > t)
+        return set_error(BGTQ_ERR_INVALID_ARG, "batch and t must be >= 0 and row0 in [0, t]");
+    *bytes = prefill_score_workspace_bytes(*p, batch, t, row0);
+    return BGTQ_OK;
+}
+
+int bgtq_prefill_score(const bgtq_plan* p, void* stream, const void* q, const void* k, const float* lse, int batch, int t,
+                       int row0, int64_t sinks, int64_t window, float scale, float* scores, int64_t score_stride,
+                       void* ws, size_t ws_bytes, int32_t* status) {
+    if (!p) return set_error(BGTQ_ERR_INVALID_ARG, "plan is NULL");
+    int rc = check_window(sinks, window);
+    if (rc) return rc;
+    if (batch < 0 || t < 0 || row0 < 0 || row0 > t)
+        return set_error(BGTQ_ERR_INVALID_ARG, "batch and t must be >= 0 and row0 in [0, t]");
+    if (batch == 0 || t == 0) return BGTQ_OK;
+    if (!q || !k || !lse || !scores) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
+    if ((reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(k)) & 15)
+        return set_error(BGTQ_ERR_INVALID_ARG, "q and k must be 16-byte aligned");
+    if ((reinterpret_cast<uintptr_t>(lse) | reinterpret_cast<uintptr_t>(scores)) & 3)
+        return set_error(BGTQ_ERR_INVALID_ARG, "lse and scores must be 4-byte aligned");
+    if (score_stride < t) return set_error(BGTQ_ERR_INVALID_ARG, "score_stride must be at least t");
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return set_error(BGTQ_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+    if ((uint64_t)batch * p->H * p->G * (uint64_t)t + 128 >= (1ull << 31) || t > 65535 * 128 ||
+        (int64_t)batch * p->H > 65535)
+        return set_error(BGTQ_ERR_UNSUPPORTED,
+                         "batch * query heads * t must stay below 2^31 - 128, t at most 8388480, batch * KV heads at most 65535");
+    const size_t need = prefill_score_workspace_bytes(*p, batch, t, row0);
+    if (ws_bytes < need) return set_error(BGTQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+    if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15)))
+        return set_error(BGTQ_ERR_INVALID_ARG, "workspace must be a 16-byte aligned device buffer");
+    if ((rc = check_plan(p))) return rc;
+    const cudaError_t e = launch_prefill_score(*p, (cudaStream_t)stream, q, k, lse, batch, t, row0, (int)std::min<int64_t>(sinks, t),
+                                               (int)std::min<int64_t>(window, t), scale, scores, score_stride, ws, status);
+    if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "prefill_score launch: %s", cudaGetErrorString(e));
+    return BGTQ_OK;
+}
+
+int bgtq_evict(const bgtq_plan* p, void* stream, const bgtq_cache* c, const float* scores, const int32_t* seq_lens,
+               int64_t max_len, int batch, int64_t keep, int64_t sinks, int64_t recent, const bgtq_cache* dst,
+               float* dst_scores, int32_t* dst_lens, int32_t* kept, int32_t* status) {
+    if (!p) return set_error(BGTQ_ERR_INVALID_ARG, "plan is NULL");
+    int rc = check_cache(p, c);
+    if (rc || (rc = check_cache(p, dst))) return rc;
+    if (batch < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and max_len must be >= 0");
+    if (keep < 1 || keep > INT32_MAX) return set_error(BGTQ_ERR_INVALID_ARG, "keep must be in [1, 2^31)");
+    if (sinks < 0 || recent < 0 || sinks > keep || recent > keep - sinks)
+        return set_error(BGTQ_ERR_INVALID_ARG, "sinks and recent must be >= 0 and sinks + recent at most keep");
+    if (c->recent > 0 || dst->recent > 0)
+        return set_error(BGTQ_ERR_UNSUPPORTED, "eviction of a cache with a recent-key buffer is not supported");
+    if (batch > 65535) return set_error(BGTQ_ERR_UNSUPPORTED, "at most 65535 sequences per call");
+    if (batch == 0) return BGTQ_OK;
+    if (!scores || !seq_lens || !dst_scores || !dst_lens || !kept) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
+    if ((reinterpret_cast<uintptr_t>(scores) | reinterpret_cast<uintptr_t>(dst_scores) | reinterpret_cast<uintptr_t>(seq_lens) |
+         reinterpret_cast<uintptr_t>(dst_lens) | reinterpret_cast<uintptr_t>(kept)) & 3)
+        return set_error(BGTQ_ERR_INVALID_ARG, "scores, lengths and kept must be 4-byte aligned");
+    max_len = std::min(max_len, c->capacity);
+    if (std::min(keep, max_len) > dst->capacity)
+        return set_error(BGTQ_ERR_CAPACITY, "the destination holds %lld positions, %lld may be kept", (long long)dst->capacity,
+                         (long long)std::min(keep, max_len));
+    // the move is out of place: no buffer of the destination may reach into
+    // one of the source (pools that both page tables map are the caller's
+    // word: the destination's pages are then not the source's)
+    const size_t units = (size_t)batch * p->H;
+    auto records = [&](const bgtq_cache* x) {
+        return x->page_table ? (size_t)x->n_pages * p->H * (size_t)x->page_tokens : units * (size_t)x->capacity;
+    };
+    const size_t ns = records(c), nd = records(dst);
+    const bool one_pool = c->page_table && dst->page_table && c->k_codes == dst->k_codes && c->v_codes == dst->v_codes &&
+                          c->k_norm == dst->k_norm && c->v_norm == dst->v_norm && c->n_pages == dst->n_pages &&
+                          c->page_tokens == dst->page_tokens && c->page_table != dst->page_table;
+    if (!one_pool && (overlap(c->k_codes, ns * 16 * p->bk, dst->k_codes, nd * 16 * p->bk) ||
+                      overlap(c->v_codes, ns * 16 * p->bv, dst->v_codes, nd * 16 * p->bv) ||
+                      overlap(c->k_norm, ns * 4, dst->k_norm, nd * 4) || overlap(c->v_norm, ns * 4, dst->v_norm, nd * 4)))
+        return set_error(BGTQ_ERR_INVALID_ARG, "the destination's records overlap the source's");
+    if (overlap(scores, units * (size_t)c->capacity * 4, dst_scores, units * (size_t)dst->capacity * 4) ||
+        overlap(seq_lens, (size_t)batch * 4, dst_lens, (size_t)batch * 4))
+        return set_error(BGTQ_ERR_INVALID_ARG, "dst_scores or dst_lens overlaps scores or seq_lens");
+    if ((rc = check_plan(p))) return rc;
+    const cudaError_t e = launch_evict(*p, (cudaStream_t)stream, *c, scores, seq_lens, max_len, batch, (int)keep, (int)sinks,
+                                       (int)recent, *dst, dst_scores, dst_lens, kept, status);
+    if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "evict launch: %s", cudaGetErrorString(e));
+    return BGTQ_OK;
+}
+
 int bgtq_logit_mae(const bgtq_plan* p, void* stream, const void* q, const void* k, const bgtq_cache* c, int64_t t,
                    int batch, float scale, float* mae) {
     int rc = check_plan(p);

@@ -140,13 +140,25 @@ struct CacheMap {
 #endif
 };
 
+// A windowed prefill: row i attends keys j <= i with j < sinks or j > i - span.
+struct PrefillWindow {
+    int sinks, span;
+    float* lse;  // [B][H*G][T] or nullptr
+};
 cudaError_t launch_prefill(const bgtq_plan& pl, cudaStream_t s, const void* q, const void* k, const void* v,
                            int batch, int t, const bgtq_cache& c, void* out, int out_dtype, float scale,
-                           int32_t* status);
+                           int32_t* status, const PrefillWindow* win = nullptr);
 size_t prefill_chunk_workspace_bytes(const bgtq_plan& pl, int batch, int64_t max_prefix);
 cudaError_t launch_prefill_chunk(const bgtq_plan& pl, cudaStream_t s, const void* q, const void* k, const void* v,
                                  int batch, int c, const int32_t* pos_start, int64_t max_prefix, const bgtq_cache& cache,
                                  void* out, int out_dtype, float scale, void* ws, int32_t* status);
+
+// Column sums of a prompt's attention weights (prefill_score.cu); ws holds
+// prefill_score_workspace_bytes (0: none is needed).
+size_t prefill_score_workspace_bytes(const bgtq_plan& pl, int batch, int t, int row0);
+cudaError_t launch_prefill_score(const bgtq_plan& pl, cudaStream_t s, const void* q, const void* k, const float* lse,
+                                 int batch, int t, int row0, int sinks, int window, float scale, float* scores,
+                                 int64_t stride, void* ws, int32_t* status);
 
 // Host checks of a cache descriptor (buffers, alignment, capacity, the
 // recent-key buffer, paging); sets the thread's error message.
@@ -212,11 +224,32 @@ size_t decode_workspace_bytes(const bgtq_plan& p, int batch, const SplitPlan& sp
 // bytes of per-(sequence, KV head, query head) arrival counters at the front
 // of the decode workspace (they must be zero before a call; calls leave them zero)
 size_t decode_counter_bytes(const bgtq_plan& p, int batch);
+// What a decode launch does besides plain attention.
+struct DecodeExtra {
+    int64_t max_len = 0;     // windowed and scoring launches: longest sequence (at most the capacity)
+    bool window = false;     // attend positions [0, sinks) and [seq - window, seq)
+    int sinks = 0, span = 0;  // span: the window's length
+    float* logit = nullptr;  // non-null: leave logits and softmax statistics for launch_score_add
+    int64_t logit_stride = 0;
+    float2* stat = nullptr;
+};
 // k_new/v_new/pos_new non-null: the fused step (append one token per
 // sequence, then attend); null: attention only.
 cudaError_t launch_decode(const bgtq_plan& p, cudaStream_t s, const void* q, const bgtq_cache& c,
                           const int32_t* seq_lens, int batch, const SplitPlan& sp, void* out, int out_dtype,
                           float scale, void* ws, int32_t* status, const void* k_new = nullptr,
-                          const void* v_new = nullptr, const int32_t* pos_new = nullptr);
+                          const void* v_new = nullptr, const int32_t* pos_new = nullptr,
+                          const DecodeExtra& extra = DecodeExtra());
+// Positions of a windowed decode's compact sequence, at most (whole tiles).
+int64_t decode_window_positions(int64_t max_len, int64_t sinks, int64_t window);
+// scores_out[b][h][t] = scores_in[b][h][t] (0 at a fused step's new position)
+// + the attention weights of position t summed over the KV head's query
+// heads, t < seq_lens[b] <= max_len, from what a scoring decode left.
+cudaError_t launch_score_add(const bgtq_plan& p, cudaStream_t s, const bgtq_cache& c, const int32_t* seq_lens,
+                             int64_t max_len, int batch, const DecodeExtra& extra, const int32_t* pos_new,
+                             const float* scores_in, float* scores_out);
+cudaError_t launch_evict(const bgtq_plan& p, cudaStream_t s, const bgtq_cache& src, const float* scores,
+                         const int32_t* seq_lens, int64_t max_len, int batch, int keep, int sinks, int recent,
+                         const bgtq_cache& dst, float* dst_scores, int32_t* dst_lens, int32_t* kept, int32_t* status);
 
 }  // namespace bgtq

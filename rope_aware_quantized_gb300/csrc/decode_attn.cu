@@ -29,14 +29,14 @@ int resident_ctas(int ws) {
     cudaLaunchConfig_t cfg = launch_config<BK, BV>(dim3(kCluster, 1, 1), nullptr, ws, attr);
     cfg.numAttrs = 1;  // occupancy: the cluster shape only
     int clusters = 0;
-    if (cudaOccupancyMaxActiveClusters(&clusters, decode_kernel<BK, BV, 2, false>, &cfg) != cudaSuccess || clusters <= 0) {
+    if (cudaOccupancyMaxActiveClusters(&clusters, decode_kernel<BK, BV, 2, false, kDecodePlain>, &cfg) != cudaSuccess || clusters <= 0) {
         cudaGetLastError();
         return 0;
     }
     // never more than the SMs hold block by block (registers, shared memory)
     int per_sm = 0, dev = 0, sms = 0;
     cudaGetDevice(&dev);
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_kernel<BK, BV, 2, false>, kWarps * 32,
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, decode_kernel<BK, BV, 2, false, kDecodePlain>, kWarps * 32,
                                                       cfg.dynamicSmemBytes) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         cudaGetLastError();
@@ -142,7 +142,7 @@ size_t decode_workspace_bytes(const bgtq_plan& p, int batch, const SplitPlan& sp
 cudaError_t launch_decode(const bgtq_plan& pl, cudaStream_t s, const void* q, const bgtq_cache& c,
                           const int32_t* seq_lens, int batch, const SplitPlan& sp, void* out, int out_dtype,
                           float scale, void* ws, int32_t* status, const void* k_new, const void* v_new,
-                          const int32_t* pos_new) {
+                          const int32_t* pos_new, const DecodeExtra& extra) {
     DecodeParams p;
     p.q = static_cast<const __half*>(q);
     p.kc = static_cast<uint8_t*>(c.k_codes);
@@ -177,6 +177,12 @@ cudaError_t launch_decode(const bgtq_plan& pl, cudaStream_t s, const void* q, co
     p.thr = pl.dev.thr;
     p.k_recent = static_cast<__half*>(c.k_recent);
     p.recent = c.recent;
+    p.max_seq = extra.max_len;
+    p.sinks = extra.sinks;
+    p.window = extra.span;
+    p.logit = extra.logit;
+    p.logit_stride = extra.logit_stride;
+    p.stat = extra.stat;
     dim3 grid((unsigned)sp.n_split, (unsigned)pl.H, (unsigned)batch);
     // the fast instances decode codes of width >= 4 only in each lane's
     // kFastWide widest slots; the general instance in any slot, and it takes
@@ -184,23 +190,22 @@ cudaError_t launch_decode(const bgtq_plan& pl, cudaStream_t s, const void* q, co
     bool any_wide = false;
     for (const HeadTab& ht : pl.heads) any_wide |= ht.n_wide > kFastWide;
     const int kind = any_wide ? 2 : (c.recent > 0 ? (c.recent <= kWinPre ? 1 : 2) : 0);
-    if (c.page_table) return launch_decode_paged(p, grid, s, kind, pl.bk, pl.bv);
-    const int key = pl.bk * 10 + pl.bv;
-    switch (key) {
-        case 11: return launch_t<1, 1, false>(p, grid, s, kind);
-        case 12: return launch_t<1, 2, false>(p, grid, s, kind);
-        case 13: return launch_t<1, 3, false>(p, grid, s, kind);
-        case 14: return launch_t<1, 4, false>(p, grid, s, kind);
-        case 21: return launch_t<2, 1, false>(p, grid, s, kind);
-        case 22: return launch_t<2, 2, false>(p, grid, s, kind);
-        case 23: return launch_t<2, 3, false>(p, grid, s, kind);
-        case 24: return launch_t<2, 4, false>(p, grid, s, kind);
-        case 31: return launch_t<3, 1, false>(p, grid, s, kind);
-        case 32: return launch_t<3, 2, false>(p, grid, s, kind);
-        case 33: return launch_t<3, 3, false>(p, grid, s, kind);
-        case 34: return launch_t<3, 4, false>(p, grid, s, kind);
-        default: return cudaErrorInvalidValue;
+    if (extra.window || extra.logit) {
+        const int mkind = kind ? 2 : 0;
+        if (extra.window)
+            return c.page_table ? launch_decode_window_paged(p, grid, s, mkind, pl.bk, pl.bv)
+                                : launch_decode_window(p, grid, s, mkind, pl.bk, pl.bv);
+        return c.page_table ? launch_decode_score_paged(p, grid, s, mkind, pl.bk, pl.bv)
+                            : launch_decode_score(p, grid, s, mkind, pl.bk, pl.bv);
     }
+    if (c.page_table) return launch_decode_paged(p, grid, s, kind, pl.bk, pl.bv);
+    return launch_widths<false, kDecodePlain>(p, grid, s, kind, pl.bk, pl.bv);
+}
+
+int64_t decode_window_positions(int64_t max_len, int64_t sinks, int64_t window) {
+    // the sinks' tiles, and a window that starts anywhere inside a tile
+    const int64_t s = (std::min(sinks, max_len) + kTile - 1) / kTile * kTile;
+    return std::min(max_len, s + std::min(window, max_len) + kTile - 1);
 }
 
 }  // namespace bgtq

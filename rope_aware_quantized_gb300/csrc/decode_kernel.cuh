@@ -82,11 +82,26 @@ struct DecodeParams {
     // positions [seq - recent, seq); written by the fused step's append
     __half* k_recent;
     int64_t recent;
+    // windowed and scoring instances: sequences longer than the call allows
+    // are cut to it and flagged (their workspace is sized by it)
+    int64_t max_seq;
+    // windowed instances: positions [0, sinks) and [seq - window, seq) are attended
+    int sinks, window;
+    // scoring instances: every attended position's logit (log2 domain)
+    // [B][H][G][logit_stride] and each query head's softmax (maximum, sum)
+    float* logit;
+    int64_t logit_stride;
+    float2* stat;
 };
 
 // Launches the paged-cache instances (defined in their own translation unit,
 // so that the contiguous instances carry no paging code).
 cudaError_t launch_decode_paged(const DecodeParams& p, dim3 grid, cudaStream_t s, int kind, int bk, int bv);
+// The windowed and the scoring instances, likewise.
+cudaError_t launch_decode_window(const DecodeParams& p, dim3 grid, cudaStream_t s, int kind, int bk, int bv);
+cudaError_t launch_decode_window_paged(const DecodeParams& p, dim3 grid, cudaStream_t s, int kind, int bk, int bv);
+cudaError_t launch_decode_score(const DecodeParams& p, dim3 grid, cudaStream_t s, int kind, int bk, int bv);
+cudaError_t launch_decode_score_paged(const DecodeParams& p, dim3 grid, cudaStream_t s, int kind, int bk, int bv);
 
 namespace {
 
@@ -442,13 +457,24 @@ struct BoolTag {
     static constexpr bool value = B;
 };
 
+// what a decode instance computes (decode_kernel's kMode)
+constexpr int kDecodePlain = 0, kDecodeWindow = 1, kDecodeScore = 2;
+
 // Instances (kKind): 0 = fast (slots 0 and 8 alone may hold codes wider
 // than the pair tables; no recent-key buffer), 1 = fast with an fp16
 // recent-key buffer of at most kWinPre keys (their exact logits computed
 // ahead of the main loop), 2 = general (any slot wide, any buffer); kPaged:
 // the cache is paged.  The buffer and paging paths are separate instances
 // so that the instances without them carry none of their code.
-template <int BK, int BV, int kKind, bool kPaged>
+// kMode: kDecodePlain; kDecodeWindow attends the first p.sinks and the last
+// p.window positions only, in compact positions: the 16-token tiles with a
+// visible token, numbered without the gap between the sinks' tiles and the
+// window's, take the place of the sequence (its split, its staging and its
+// merge are the plain ones), a tile's records are found through real_pos and
+// the invisible tokens of the two border tiles are masked, so a page that
+// holds no visible token is never read and may be unmapped; kDecodeScore also
+// leaves the logits and the softmax statistics for score_add_kernel.
+template <int BK, int BV, int kKind, bool kPaged, int kMode>
 __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) {
     constexpr int NW = kKind == 2 ? 16 : kFastWide;  // leading slots that may hold codes of width >= 4
     constexpr bool kWinPath = kKind >= 1;  // fp16 recent-key buffer supported
@@ -481,14 +507,34 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
     const int G = p.G;
     const size_t unit = (size_t)b * p.H + h;
     int seq = p.seq_lens[b];
-    if (seq < 0 || (int64_t)seq > p.cap) {
+    const int64_t seq_cap = kMode == kDecodePlain ? p.cap : p.max_seq;
+    if (seq < 0 || (int64_t)seq > seq_cap) {
         pdl_wait();
         if (tid == 0 && split == 0 && h == 0 && p.status) {
             atomicOr(p.status, BGTQ_STATUS_SEQLEN_CAPACITY);
             debug_in_range(false, p.status);  // records past the capacity
         }
-        seq = seq < 0 ? 0 : (int)p.cap;
+        seq = seq < 0 ? 0 : (int)seq_cap;
     }
+    // Windowed instances: from here on `seq` and every token position are
+    // compact ones; positions [0, s_end) are the sinks' tiles, those from
+    // s_end on lie `gap` further in the cache.
+    int win_lo = 0, s_end = 0, gap = 0;
+    if constexpr (kMode == kDecodeWindow) {
+        win_lo = max(0, seq - p.window);
+        s_end = (min(p.sinks, win_lo) + kTile - 1) / kTile * kTile;
+        gap = max(0, win_lo / kTile * kTile - s_end);
+        seq -= gap;
+    }
+    auto real_pos = [&](int v) -> int {
+        if constexpr (kMode == kDecodeWindow) return v < s_end ? v : v + gap;
+        return v;
+    };
+    // the compact position of a real one; -1 inside the gap
+    auto compact_pos = [&](int r) -> int {
+        if constexpr (kMode == kDecodeWindow) return r < s_end ? r : r < s_end + gap ? -1 : r - gap;
+        return r;
+    };
     // Token ranges, newest first: split 0 attends [a0, seq) with a0 the
     // multiple of 16 at or above seq - (tps - slack), split s >= 1 the tps
     // tokens [a0 - s tps, a0 - (s - 1) tps) (the oldest one clipped at 0).
@@ -508,7 +554,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
     if (p.k_new) {
         pos = p.pos_new[b];
         pos_bad = pos < 0 || (int64_t)pos + 1 > p.cap;
-        owner = !pos_bad && split == (pos < seq && pos < a0 ? 1 + (a0 - 1 - pos) / p.tps : 0);
+        const int cpos = compact_pos(pos);
+        owner = !pos_bad && split == (cpos >= 0 && cpos < seq && cpos < a0 ? 1 + (a0 - 1 - cpos) / p.tps : 0);
         if (owner) {
             stage_thresholds(s_thr, p.thr, tid, kWarps * 32);
             if (warp < 2) enc_lane_load(el, p.heads + h, warp == 0, BV, p.v_inv_sqrt, lane);
@@ -544,7 +591,12 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
     const HeadTab* ht = p.heads + h;
     const int t_begin = !active ? seq : split == 0 ? a0 : max(0, a0 - split * p.tps);
     const int t_end = !active ? seq : split == 0 ? seq : a0 - (split - 1) * p.tps;
-    const int wstart = p.recent > 0 ? max(0, seq - (int)p.recent) : seq;  // first position of the fp16 keys
+    // first position of the fp16 keys (windowed: a first one inside the gap is
+    // the window's first tile)
+    int wstart = p.recent > 0 ? max(0, seq + gap - (int)p.recent) : seq;
+    if constexpr (kMode == kDecodeWindow) {
+        if (p.recent > 0) wstart = compact_pos(wstart) >= 0 ? compact_pos(wstart) : s_end;
+    }
     const int wlo = max(t_begin, wstart);  // the range's first window token (instance 1: s_wlog column 0)
     // record bases: the (sequence, head) row of a contiguous cache (token
     // slot = position), the pools of a paged one (token slot per tile)
@@ -559,9 +611,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
     // (no branch on the page index: the prologue flags bad ones, so the
     // page-table load can be issued a tile ahead of its use)
     auto tile_slot = [&](int T0) -> int64_t {
-        if constexpr (!kPaged) return T0;
-        const int64_t sl = p.map.slot(b, h, T0);
-        return sl >= 0 ? sl : ((int64_t)h << p.map.lp) + (T0 & ((1 << p.map.lp) - 1));
+        if constexpr (!kPaged) return real_pos(T0);
+        const int64_t sl = p.map.slot(b, h, real_pos(T0));
+        if (kMode == kDecodeWindow && sl < 0 && p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
+        return sl >= 0 ? sl : ((int64_t)h << p.map.lp) + (real_pos(T0) & ((1 << p.map.lp) - 1));
     };
     // warp w takes tiles T0 = t_begin + 16 w + kStep k; kStages - 1 of them are
     // being copied while one is processed
@@ -593,7 +646,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
     uint32_t slot_pairs[4];
     // (no L2 prefetch of the token range before the wait: under programmatic
     // dependent launch it competes with the previous kernel's own reads)
-    if (kPaged && active) {
+    if (kPaged && kMode != kDecodeWindow && active) {  // (windowed: each tile's lookup checked its own page)
         // paged: thread i checks the page-table entry of page i of the range
         // (the page table is read before the wait, like seq_lens); the main
         // loop reads page 0 in place of a bad one
@@ -836,7 +889,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
         auto load_kb = [&]() {
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt) {
-                const int tk = min(max(T0 + 8 * nt + g, wstart), seq - 1);
+                const int tk = real_pos(min(max(T0 + 8 * nt + g, wstart), seq - 1));
                 const uint32_t* kr = reinterpret_cast<const uint32_t*>(
                     p.k_recent + (unit * (size_t)p.recent + (size_t)(tk % p.recent)) * kD + 2 * t);
 #pragma unroll
@@ -895,6 +948,29 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
                     const int tok = T0 + 8 * nt + 2 * t + e;
                     if (tok >= wstart && tok < t_end) lg[nt][e] = s16[nt][e] * p.scale_log2;
                 }
+        }
+        if constexpr (kMode == kDecodeWindow) {
+            // positions between the sinks and the window: the rest of the
+            // sinks' last tile and the start of the window's first
+            const int r0 = real_pos(T0);
+            if (r0 < win_lo && r0 + kTile > p.sinks) {
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = r0 + 8 * nt + 2 * t + e;
+                        if (r >= p.sinks && r < win_lo) lg[nt][e] = -INFINITY;
+                    }
+            }
+        }
+        if constexpr (kMode == kDecodeScore) {
+            // 8-byte stores, 32 bytes a head and 8-token group (the row is
+            // padded to whole tiles; past the sequence they are -inf)
+            if (g < G) {
+                float* dst = p.logit + (unit * G + g) * (size_t)p.logit_stride + T0 + 2 * t;
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) *reinterpret_cast<float2*>(dst + 8 * nt) = make_float2(lg[nt][0], lg[nt][1]);
+            }
         }
         float mx = -INFINITY;
 #pragma unroll
@@ -1121,6 +1197,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
 #pragma unroll
         for (int i = 0; i < 4; ++i) sw[2 + lane + 32 * i] = O[i];
         __syncthreads();
+        float Mt_all = -INFINITY;  // the query head's softmax reference (scoring instances)
         if (warp == 0) {
             float mw[kWarps];
             float Mt = -INFINITY;
@@ -1129,6 +1206,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
                 mw[w] = s_wp[w][0][0];
                 Mt = fmaxf(Mt, mw[w]);
             }
+            Mt_all = Mt;
             L = 0.0f;
             O[0] = O[1] = O[2] = O[3] = 0.0f;
 #pragma unroll
@@ -1169,7 +1247,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
             if (p.out_dtype) static_cast<float*>(p.out)[o] = val;
             else static_cast<__half*>(p.out)[o] = __float2half_rn(val);
         }
-        if (lane == 0) p.count[unit * G + r] = 0;
+        if (lane == 0) {
+            if constexpr (kMode == kDecodeScore) p.stat[unit * G + r] = make_float2(Mt_all, L);
+            p.count[unit * G + r] = 0;
+        }
     }
     cluster_wait();  // no CTA leaves while another may still read its partials
 }
@@ -1177,7 +1258,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
 // The dynamic shared memory of the three instances of decode_kernel<BK, BV>
 // of one paging mode is raised above the 48 KB default once per device, to
 // the size with the largest lookup tables.
-template <int BK, int BV, bool kPaged>
+template <int BK, int BV, bool kPaged, int kMode = kDecodePlain>
 cudaError_t ensure_smem_attr() {
     static std::mutex mu;
     static bool done[64] = {false};
@@ -1187,11 +1268,13 @@ cudaError_t ensure_smem_attr() {
     std::lock_guard<std::mutex> lock(mu);
     if (done[dev]) return cudaSuccess;
     const int bytes = decode_smem_bytes<BK, BV>(kWMax);
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<BK, BV, 0, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<BK, BV, 0, kPaged, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if constexpr (kMode == kDecodePlain) {
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(decode_kernel<BK, BV, 1, kPaged, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    }
     if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel<BK, BV, 1, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess)
-        e = cudaFuncSetAttribute(decode_kernel<BK, BV, 2, kPaged>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        e = cudaFuncSetAttribute(decode_kernel<BK, BV, 2, kPaged, kMode>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e == cudaSuccess) done[dev] = true;
     return e;
 }
@@ -1214,17 +1297,39 @@ cudaLaunchConfig_t launch_config(dim3 grid, cudaStream_t s, int ws, cudaLaunchAt
     return cfg;
 }
 
-template <int BK, int BV, bool kPaged>
+template <int BK, int BV, bool kPaged, int kMode = kDecodePlain>
 cudaError_t launch_t(DecodeParams p, dim3 grid, cudaStream_t s, int kind) {
-    cudaError_t e = ensure_smem_attr<BK, BV, kPaged>();
+    cudaError_t e = ensure_smem_attr<BK, BV, kPaged, kMode>();
     if (e != cudaSuccess) return e;
     const int ws = p.img_ws;
     p.img_bytes = decode_table_bytes(ws);
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = launch_config<BK, BV>(grid, s, ws, attr);
-    if (kind == 2) return cudaLaunchKernelEx(&cfg, decode_kernel<BK, BV, 2, kPaged>, p);
-    if (kind == 1) return cudaLaunchKernelEx(&cfg, decode_kernel<BK, BV, 1, kPaged>, p);
-    return cudaLaunchKernelEx(&cfg, decode_kernel<BK, BV, 0, kPaged>, p);
+    if (kind == 2) return cudaLaunchKernelEx(&cfg, decode_kernel<BK, BV, 2, kPaged, kMode>, p);
+    if constexpr (kMode == kDecodePlain) {  // (the other modes take their recent keys in the general instance)
+        if (kind == 1) return cudaLaunchKernelEx(&cfg, decode_kernel<BK, BV, 1, kPaged, kMode>, p);
+    }
+    return cudaLaunchKernelEx(&cfg, decode_kernel<BK, BV, 0, kPaged, kMode>, p);
+}
+
+// The launch of the instance of (bk, bv).
+template <bool kPaged, int kMode>
+cudaError_t launch_widths(const DecodeParams& p, dim3 grid, cudaStream_t s, int kind, int bk, int bv) {
+    switch (bk * 10 + bv) {
+        case 11: return launch_t<1, 1, kPaged, kMode>(p, grid, s, kind);
+        case 12: return launch_t<1, 2, kPaged, kMode>(p, grid, s, kind);
+        case 13: return launch_t<1, 3, kPaged, kMode>(p, grid, s, kind);
+        case 14: return launch_t<1, 4, kPaged, kMode>(p, grid, s, kind);
+        case 21: return launch_t<2, 1, kPaged, kMode>(p, grid, s, kind);
+        case 22: return launch_t<2, 2, kPaged, kMode>(p, grid, s, kind);
+        case 23: return launch_t<2, 3, kPaged, kMode>(p, grid, s, kind);
+        case 24: return launch_t<2, 4, kPaged, kMode>(p, grid, s, kind);
+        case 31: return launch_t<3, 1, kPaged, kMode>(p, grid, s, kind);
+        case 32: return launch_t<3, 2, kPaged, kMode>(p, grid, s, kind);
+        case 33: return launch_t<3, 3, kPaged, kMode>(p, grid, s, kind);
+        case 34: return launch_t<3, 4, kPaged, kMode>(p, grid, s, kind);
+        default: return cudaErrorInvalidValue;
+    }
 }
 
 }  // namespace

@@ -32,6 +32,12 @@
 // The records of a block's 128 positions are encoded, with the warp encoder
 // steps of the append kernel (bit-identical to an append of the same tokens),
 // by the encoder warps of the KV head's CTAs of that block, an even share each.
+// The windowed instance (bgtq_prefill_window_attn: row i attends the keys
+// j <= i with j < sinks or j > i - window) runs the same pipeline over the key
+// tiles that its 128 rows can see, the diagonal one first: every row sees its
+// own key there, so the running maximum is finite before a tile that a row
+// sees nothing of.  Only the diagonal tile, those at the window's low edge and
+// those at the sinks' end are masked.  It also gives each row's log-sum-exp.
 // Every wait is bounded: after kWaitNs it sets BGTQ_STATUS_TIMEOUT, the CTA
 // skips the rest of its work, lets its copies and MMAs land and frees its
 // tensor memory.
@@ -96,10 +102,34 @@ bool descriptors_valid() {
     return true;
 }
 
+// The key tiles of a query block, in the order they are attended: 0 .. qb, or
+// (windowed) the window's from the diagonal down, then the sinks' from the
+// last one down.
+template <bool kWin>
+struct KeyTiles {
+    int n;        // tiles
+    int diag;     // the tile that holds the rows themselves (query block qb)
+    int n_win;    // windowed: tiles of the window, diag - n_win + 1 .. diag
+    int n_sink;   // windowed: tiles of the sinks below them
+    __device__ __forceinline__ KeyTiles(int qb, int q0, int sinks, int window) : n(qb + 1), diag(qb), n_win(0), n_sink(0) {
+        if constexpr (kWin) {
+            const int first = max(0, q0 - window + 1) / kTcKeys;
+            n_win = qb - first + 1;
+            n_sink = min((min(sinks, first * kTcKeys) + kTcKeys - 1) / kTcKeys, first);
+            n = n_win + n_sink;
+        }
+    }
+    __device__ __forceinline__ int tile(int j) const {
+        if constexpr (kWin) return j < n_win ? diag - j : n_sink - 1 - (j - n_win);
+        return j;
+    }
+};
+
 // Softmax warpgroup g: the online softmax of row r of query head hq0 + g
-// over key tiles 0 .. nkt-1, then the normalised output row.
-__device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, int g, int b, int hq, int q0, int nkt,
-                                             uint32_t bar_s, uint32_t bar_p, uint32_t bar_o, volatile int* abort_flag,
+// over the block's key tiles, then the normalised output row.
+template <bool kWin>
+__device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, int g, int b, int hq, int q0,
+                                             const KeyTiles<kWin>& kt, uint32_t bar_s, uint32_t bar_p, uint32_t bar_o, volatile int* abort_flag,
                                              int warp, int lane) {
     const int r = 32 * (warp & 3) + lane;  // row of the block = tensor-memory lane
     const int row = q0 + r;
@@ -108,6 +138,7 @@ __device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, i
     const float c = p.scale_log2;
     float m = 0.0f, l = 0.0f;
     bool ok = true;
+    const int nkt = kt.n;
     for (int j = 0; j < nkt; ++j) {
         if (!__all_sync(0xffffffffu, mbar_wait(bar_s, j & 1, abort_flag, p.status))) {
             ok = false;
@@ -119,7 +150,17 @@ __device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, i
         for (int q = 0; q < kTcKeys / 32; ++q) tmem_ld32(tS + 32 * q, s + 32 * q);
 #pragma unroll
         for (int q = 0; q < kTcKeys / 32; ++q) tmem_wait_ld32(s + 32 * q);
-        if (j == nkt - 1) {  // the diagonal tile: keys after the row, and past the prompt
+        if constexpr (kWin) {
+            const int k0 = kt.tile(j) * kTcKeys;
+            // the diagonal tile, and tiles with a key that the block's last
+            // row is past the window of, unless all of them are sinks
+            if (j == 0 || (k0 <= q0 + kTcRows - 1 - p.window && k0 + kTcKeys > p.sinks)) {
+                const int lim = min(row, p.T - 1) - k0, low = row - p.window - k0, sk = p.sinks - k0;
+#pragma unroll
+                for (int k = 0; k < kTcKeys; ++k)
+                    if (k > lim || (k <= low && k >= sk)) s[k] = -INFINITY;
+            }
+        } else if (j == nkt - 1) {  // the diagonal tile: keys after the row, and past the prompt
             const int lim = min(row, p.T - 1) - j * kTcKeys;
 #pragma unroll
             for (int k = 0; k < kTcKeys; ++k)
@@ -135,7 +176,7 @@ __device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, i
         float f = 1.0f;
         bool raise = false;
         if (j == 0) {
-            m = mt;  // key 0 is before every row: finite
+            m = mt;  // key 0 is before every row (windowed: the row's own key): finite
         } else if (mt > m + kHeadroom) {
             f = ex2(m - mt);
             m = mt;
@@ -175,6 +216,10 @@ __device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, i
     if (!ok || !__all_sync(0xffffffffu, mbar_wait(bar_o, 0, abort_flag, p.status))) return;
     tc_fence_after();
     const float inv = 1.0f / l;
+    if constexpr (kWin) {
+        if (p.lse && row < p.T)
+            p.lse[((size_t)b * p.H * p.G + hq) * p.T + row] = (m + log2f(l)) * 0.6931471805599453f;
+    }
     const size_t o0 = ((size_t)((size_t)b * p.H * p.G + hq) * p.T + row) * kD;
 #pragma unroll 1
     for (int q = 0; q < kD / 32; ++q) {
@@ -198,6 +243,7 @@ __device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, i
     }
 }
 
+template <bool kWin>
 __global__ void __launch_bounds__(kTcThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, PfParams p) {
@@ -219,7 +265,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int q0 = qb * kTcRows;
     const int hq0 = h * p.G + 2 * pair;
     const int ng = 2 * pair + 1 < p.G ? 2 : 1;  // query heads of this CTA
-    const int nkt = qb + 1;                     // key tiles; tile qb holds the diagonal
+    const KeyTiles<kWin> kt(qb, q0, p.sinks, p.window);
+    const int nkt = kt.n;
     const uint32_t bar0 = smem_u32(&s_bar[0]);
     volatile int* abort_flag = &s_abort;
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
@@ -255,14 +302,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (j >= 2 && !mbar_wait(BAR(kBarKEmpty + s), par, abort_flag, p.status)) break;
                 mbar_expect_tx(BAR(kBarKFull + s), kTcTile);
                 for (int x = 0; x < 2; ++x)
-                    tma_load_2d(sbase + kOffK + s * kTcTile + x * kTcBox, &tk, 64 * x, krow + j * kTcKeys, BAR(kBarKFull + s));
+                    tma_load_2d(sbase + kOffK + s * kTcTile + x * kTcBox, &tk, 64 * x, krow + kt.tile(j) * kTcKeys, BAR(kBarKFull + s));
                 if (j >= 2 && !mbar_wait(BAR(kBarVEmpty + s), par, abort_flag, p.status)) {
                     used[s] = 2 * j + 1;  // K of tile j in flight, V not
                     break;
                 }
                 mbar_expect_tx(BAR(kBarVFull + s), kTcTile);
                 for (int x = 0; x < 2; ++x)
-                    tma_load_2d(sbase + kOffV + s * kTcTile + x * kTcBox, &tv, 64 * x, krow + j * kTcKeys, BAR(kBarVFull + s));
+                    tma_load_2d(sbase + kOffV + s * kTcTile + x * kTcBox, &tv, 64 * x, krow + kt.tile(j) * kTcKeys, BAR(kBarVFull + s));
                 used[s] = 2 * j + 2;
             }
             // every copy issued has landed before the CTA ends (normally at
@@ -351,7 +398,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // ---- softmax warpgroups
         const int g = warp >> 2;
         if (g < ng)
-            softmax_rows(p, tmem, g, b, hq0 + g, q0, nkt, BAR(kBarS + g), BAR(kBarP + g), BAR(kBarO + g), abort_flag, warp,
+            softmax_rows<kWin>(p, tmem, g, b, hq0 + g, q0, kt, BAR(kBarS + g), BAR(kBarP + g), BAR(kBarO + g), abort_flag, warp,
                          lane);
     }
 #undef BAR
@@ -367,7 +414,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 cudaError_t launch_prefill(const bgtq_plan& pl, cudaStream_t s, const void* q, const void* k, const void* v,
                            int batch, int t, const bgtq_cache& c, void* out, int out_dtype, float scale,
-                           int32_t* status) {
+                           int32_t* status, const PrefillWindow* win) {
     static std::mutex mu;
     static bool done[64] = {false};
     static const bool desc_ok = descriptors_valid();
@@ -383,8 +430,10 @@ cudaError_t launch_prefill(const bgtq_plan& pl, cudaStream_t s, const void* q, c
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!done[dev]) {
-            const cudaError_t e =
-                cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
+            cudaError_t e =
+                cudaFuncSetAttribute(prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
             if (e != cudaSuccess) return e;
             done[dev] = true;
         }
@@ -416,8 +465,14 @@ cudaError_t launch_prefill(const bgtq_plan& pl, cudaStream_t s, const void* q, c
     p.k_recent = static_cast<__half*>(c.k_recent);
     p.recent = c.recent;
     p.status = status;
+    p.sinks = win ? win->sinks : 0;
+    p.window = win ? win->span : 0;
+    p.lse = win ? win->lse : nullptr;
     const dim3 grid((unsigned)units, (unsigned)nqb, 1);
-    prefill_kernel<<<grid, kTcThreads, kTcSmem, s>>>(tq, tk, tv, p);
+    if (win)
+        prefill_kernel<true><<<grid, kTcThreads, kTcSmem, s>>>(tq, tk, tv, p);
+    else
+        prefill_kernel<false><<<grid, kTcThreads, kTcSmem, s>>>(tq, tk, tv, p);
     return cudaGetLastError();
 }
 

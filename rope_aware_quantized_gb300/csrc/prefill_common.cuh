@@ -30,6 +30,10 @@ struct PfParams {
     __half* k_recent;
     int64_t recent;
     int32_t* status;
+    // windowed prefill: visible keys of row i are j <= i with j < sinks or
+    // j > i - window; lse [B][H*G][T] natural log-sum-exp of a row's logits
+    int sinks, window;
+    float* lse;
 };
 
 // Encode the keys and values of cache positions [p0, p0 + n) of (b, h),
