@@ -437,8 +437,7 @@ int bgtq_decode_window_workspace(const bgtq_plan* plan, int batch, int64_t max_l
  *                bytes; two calls that may overlap on the GPU need two
  * Only the records of 16-position tiles with a visible position are read: a
  * page of a paged cache without one may be unmapped (-1) and given away.
- * An empty sequence yields zeros.  With window >= seq_len the output equals
- * bgtq_decode_attn's bit for bit.
+ * An empty sequence yields zeros.
  * Errors: INVALID_ARG (pointers, alignment, sinks < 0, window < 1, only some
  * of the new token's arguments), WORKSPACE, UNSUPPORTED (bK > 3, bV > 4, more
  * than 65535 sequences), CUDA.
@@ -466,7 +465,7 @@ int bgtq_decode_score_workspace(const bgtq_plan* plan, int batch, int64_t max_le
  *                read nor written; a new token's position starts from 0
  *                whatever scores_in holds there
  * Two launches on `stream`; sums in float32, the query heads in order (the
- * same bits on every run).  out equals bgtq_decode_attn's bit for bit.
+ * same bits on every run).
  * Other arguments and errors as bgtq_decode_window_attn.
  */
 int bgtq_decode_score_attn(const bgtq_plan* plan, void* stream, const void* q_fp16, const void* k_new_fp16,

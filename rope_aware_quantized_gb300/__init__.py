@@ -47,7 +47,8 @@ def _ptr(x) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # (the handle alone: building a Stream object costs a small call as much again)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -400,6 +401,8 @@ def _out_dtype(out) -> int:
 
 def _need(x, name: str, dtype, shape):
     """A contiguous CUDA tensor of this type and shape."""
+    if x.dtype == dtype and x.shape == shape and x.is_contiguous() and x.is_cuda:
+        return
     if x.dtype != dtype or tuple(x.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
     if not x.is_contiguous():

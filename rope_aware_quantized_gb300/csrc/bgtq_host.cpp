@@ -1043,7 +1043,8 @@ int bgtq_decode_window_workspace(const bgtq_plan* p, int batch, int64_t max_len,
     if (batch < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and max_len must be >= 0");
     const int rc = check_window(sinks, window);
     if (rc) return rc;
-    *bytes = decode_workspace_bytes(*p, batch, decode_split(*p, batch, decode_window_positions(max_len, sinks, window)));
+    *bytes = decode_workspace_bytes(*p, batch,
+                                    decode_split_bounded(*p, batch, decode_window_positions(max_len, sinks, window)));
     return BGTQ_OK;
 }
 
@@ -1057,7 +1058,7 @@ int bgtq_decode_window_attn(const bgtq_plan* p, void* stream, const void* q, con
     if (batch == 0) return BGTQ_OK;
     if ((rc = check_plan(p))) return rc;
     max_len = std::min(max_len, c->capacity);
-    const SplitPlan sp = decode_split(*p, batch, decode_window_positions(max_len, sinks, window));
+    const SplitPlan sp = decode_split_bounded(*p, batch, decode_window_positions(max_len, sinks, window));
     const size_t need = decode_workspace_bytes(*p, batch, sp);
     if (ws_bytes < need) return set_error(BGTQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
     DecodeExtra x;
@@ -1074,7 +1075,7 @@ int bgtq_decode_window_attn(const bgtq_plan* p, void* stream, const void* q, con
 int bgtq_decode_score_workspace(const bgtq_plan* p, int batch, int64_t max_len, size_t* bytes) {
     if (!p || !bytes) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
     if (batch < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and max_len must be >= 0");
-    *bytes = score_workspace(*p, batch, max_len, decode_split(*p, batch, max_len)).bytes;
+    *bytes = score_workspace(*p, batch, max_len, decode_split_bounded(*p, batch, max_len)).bytes;
     return BGTQ_OK;
 }
 
@@ -1093,7 +1094,7 @@ int bgtq_decode_score_attn(const bgtq_plan* p, void* stream, const void* q, cons
         return set_error(BGTQ_ERR_INVALID_ARG, "scores_in and scores_out are one array or do not overlap");
     if ((rc = check_plan(p))) return rc;
     max_len = std::min(max_len, c->capacity);
-    const SplitPlan sp = decode_split(*p, batch, max_len);
+    const SplitPlan sp = decode_split_bounded(*p, batch, max_len);
     const ScoreWorkspace w = score_workspace(*p, batch, max_len, sp);
     if (ws_bytes < w.bytes) return set_error(BGTQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, w.bytes);
     DecodeExtra x;

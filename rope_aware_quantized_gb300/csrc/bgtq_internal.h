@@ -218,8 +218,12 @@ struct SplitPlan {
     int n_split = 1;
     int tokens_per_split = 64;
     int slack = 0;  // the newest range (split 0) holds about this many tokens fewer
+    int cluster = 8;  // splits whose partials one thread-block cluster merges
 };
 SplitPlan decode_split(const bgtq_plan& p, int batch, int64_t max_len);
+// The split of the windowed and the scoring decode: as decode_split, or, when
+// its clusters would not fit the GPU at once, splits without clusters.
+SplitPlan decode_split_bounded(const bgtq_plan& p, int batch, int64_t max_len);
 size_t decode_workspace_bytes(const bgtq_plan& p, int batch, const SplitPlan& sp);
 // bytes of per-(sequence, KV head, query head) arrival counters at the front
 // of the decode workspace (they must be zero before a call; calls leave them zero)

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(128) quantize_append_kernel(QParams p) {
     enc_lane_load(el, ht, is_k, p.bv, p.v_inv_sqrt, lane);
     __syncthreads();
     // pos_start is read before the wait: no kernel of this library writes it
-    const int ps = p.pos_start[b];
+    const int ps = p.pos_start ? p.pos_start[b] : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (ps < 0 || (int64_t)ps + p.t_new > p.cap) {
         if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0 && p.status) {

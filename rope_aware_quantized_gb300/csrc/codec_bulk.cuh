@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkMinBlocks) quantize_append_
     const int h = blockIdx.y, b = (int)blockIdx.z - (is_v ? nbz : 0);
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // pos_start is read before the wait: no kernel of this library writes it
-    const int ps = p.pos_start[b];
+    const int ps = p.pos_start ? p.pos_start[b] : 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (ps < 0 || (int64_t)ps + p.t_new > p.cap) {
         if (blockIdx.x == 0 && h == 0 && tid == 0 && p.status) {

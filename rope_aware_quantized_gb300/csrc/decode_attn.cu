@@ -129,6 +129,37 @@ SplitPlan decode_split(const bgtq_plan& p, int batch, int64_t max_len) {
     return sp;
 }
 
+SplitPlan decode_split_bounded(const bgtq_plan& p, int batch, int64_t max_len) {
+    const int64_t units = std::max<int64_t>(1, (int64_t)batch * p.H);
+    const int64_t len = std::max<int64_t>(max_len, 1);
+    int64_t slots = (p.bk >= 1 && p.bk <= 3 && p.bv >= 1 && p.bv <= 4)
+                        ? resident_ctas_for(p.bk, p.bv, p.img_ws) : 0;
+    if (slots <= 0) slots = 2 * std::max(1, p.num_sms);
+    if (units * kCluster <= slots) return decode_split(p, batch, max_len);
+    // A large batch: clusters of kCluster splits would take several waves of
+    // CTAs, each with its set-up (about kFixed tokens' worth of time: 5 us
+    // against 13 ns a token), so a unit is cut into as few splits as fill the
+    // GPU evenly: the split count of the shortest waves x (kFixed + tokens).
+    constexpr int64_t kFixed = 400;
+    SplitPlan best;
+    int64_t best_cost = INT64_MAX;
+    for (int64_t ns = (len + kMaxSplitTokens - 1) / kMaxSplitTokens; ns <= kMaxClusters; ++ns) {
+        const int64_t slack = ns > 1 ? std::min<int64_t>(256, (len + ns - 1) / ns / 4) / kTile * kTile : 0;
+        int64_t tps = (len + slack + ns - 1) / ns;
+        tps = std::max<int64_t>((tps + kTile - 1) / kTile * kTile, (int64_t)kWarps * kTile);
+        if (tps > kMaxSplitTokens) continue;
+        const int64_t cost = (units * ns + slots - 1) / slots * (kFixed + tps);
+        if (cost >= best_cost) continue;
+        best_cost = cost;
+        const int64_t a0 = std::max<int64_t>(0, (len - tps + slack + kTile - 1) / kTile * kTile);
+        best.tokens_per_split = (int)tps;
+        best.slack = (int)slack;
+        best.n_split = (int)(1 + (a0 + tps - 1) / tps);
+        best.cluster = 1;
+    }
+    return best_cost == INT64_MAX ? decode_split(p, batch, max_len) : best;
+}
+
 size_t decode_counter_bytes(const bgtq_plan& p, int batch) {
     return (((size_t)batch * p.H * p.G * sizeof(uint32_t)) + 255) / 256 * 256;
 }
@@ -136,7 +167,7 @@ size_t decode_counter_bytes(const bgtq_plan& p, int batch) {
 size_t decode_workspace_bytes(const bgtq_plan& p, int batch, const SplitPlan& sp) {
     const size_t units = (size_t)batch * p.H;
     const size_t counters = decode_counter_bytes(p, batch);
-    return counters + units * (size_t)(sp.n_split / kCluster) * p.G * kPartStride * sizeof(float);
+    return counters + units * (size_t)(sp.n_split / sp.cluster) * p.G * kPartStride * sizeof(float);
 }
 
 cudaError_t launch_decode(const bgtq_plan& pl, cudaStream_t s, const void* q, const bgtq_cache& c,
@@ -178,6 +209,7 @@ cudaError_t launch_decode(const bgtq_plan& pl, cudaStream_t s, const void* q, co
     p.k_recent = static_cast<__half*>(c.k_recent);
     p.recent = c.recent;
     p.max_seq = extra.max_len;
+    p.cluster = sp.cluster;
     p.sinks = extra.sinks;
     p.window = extra.span;
     p.logit = extra.logit;

@@ -85,6 +85,7 @@ struct DecodeParams {
     // windowed and scoring instances: sequences longer than the call allows
     // are cut to it and flagged (their workspace is sized by it)
     int64_t max_seq;
+    int cluster;  // CTAs per thread-block cluster: kCluster, or 1 (windowed and scoring instances)
     // windowed instances: positions [0, sinks) and [seq - window, seq) are attended
     int sinks, window;
     // scoring instances: every attended position's logit (log2 domain)
@@ -543,8 +544,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
     // by about `slack` tokens to make up for the append.
     const int a0 = max(0, (seq - p.tps + p.slack + 15) & ~15);
     const int n_active = 1 + (a0 + p.tps - 1) / p.tps;
-    const int n_clusters = (n_active + kCluster - 1) / kCluster;
-    const int cid = split / kCluster;
+    const int csize = kMode == kDecodePlain ? kCluster : p.cluster;
+    const int n_clusters = (n_active + csize - 1) / csize;
+    const int cid = split / csize;
     // Fused step: the CTA whose token range holds the new position appends
     // the new token before attending (split 0 when the position is not
     // attended).  pos_new is read before the wait, like seq_lens.
@@ -1101,59 +1103,47 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
     constexpr int kHeadsPerCta = (8 + kCluster - 1) / kCluster;
     static_assert(kCluster <= 32 && kWarps * 32 >= kD, "cluster merge layout");
     cluster.sync();
-    const size_t max_clusters = (size_t)p.n_split / kCluster;
+    const size_t max_clusters = (size_t)p.n_split / csize;
     float* cpart_base = p.part + unit * max_clusters * (size_t)G * kPartStride;
-    float Mc[kHeadsPerCta], Lc[kHeadsPerCta], Oc[kHeadsPerCta];
-#pragma unroll
-    for (int j = 0; j < kHeadsPerCta; ++j) {
-        const int hh = crank + j * kCluster;
-        Mc[j] = -INFINITY;
-        Lc[j] = 0.0f;
-        Oc[j] = 0.0f;
-        if (hh >= G) continue;
+    auto reduce_head = [&](int hh, float& M, float& L, float& O) {
         float mi = -INFINITY, li = 0.0f;
-        if (lane < kCluster) {
+        if (lane < csize) {
             const float* src = cluster.map_shared_rank(&s_cp[hh][0], lane);
             mi = src[0];
             li = src[1];
         }
-        float M = mi;
+        M = mi;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         const float fi = mi == -INFINITY ? 0.0f : exp2f(mi - M);
-        float L = li * fi;
+        L = li * fi;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        float O = 0.0f;
+        O = 0.0f;
         if (tid < kD) {
             float x[kCluster];
 #pragma unroll
-            for (int c = 0; c < kCluster; ++c) x[c] = *cluster.map_shared_rank(&s_cp[hh][2 + tid], c);
+            for (int c = 0; c < kCluster; ++c) x[c] = c < csize ? *cluster.map_shared_rank(&s_cp[hh][2 + tid], c) : 0.0f;
 #pragma unroll
             for (int c = 0; c < kCluster; ++c) O += __shfl_sync(0xffffffffu, fi, c) * x[c];
         }
-        Mc[j] = M;
-        Lc[j] = L;
-        Oc[j] = O;
-    }
-    cluster_arrive();  // this CTA has finished reading the other CTAs' partials
-#pragma unroll
-    for (int j = 0; j < kHeadsPerCta; ++j) {
-        const int r = crank + j * kCluster;
-        if (r >= G) continue;
+    };
+    auto store_head = [&](int r, float M, float L, float O) {
         float* dst = cpart_base + ((size_t)cid * G + r) * kPartStride;
-        if (tid < kD) dst[2 + tid] = Oc[j];
+        if (tid < kD) dst[2 + tid] = O;
         if (tid == 0) {
-            dst[0] = Mc[j];
-            dst[1] = Lc[j];
+            dst[0] = M;
+            dst[1] = L;
         }
+    };
+    auto finish_head = [&](int r) {
         __syncthreads();  // the partial is written before thread 0 releases it
         if (tid == 0) {
             const unsigned prev = ticket_acq_rel(p.count + unit * G + r);
             s_last = (prev == (unsigned)(n_clusters - 1)) ? 1 : 0;
         }
         __syncthreads();  // thread 0's acquire is ordered before the loads below
-        if (!s_last) continue;
+        if (!s_last) return;
         // ---- last cluster partial of query head r: warp w merges the
         // partials of clusters w, w + kWarps, ... (one batch of independent
         // loads; lane holds dims lane + 32 i) into the free per-warp region,
@@ -1218,7 +1208,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
             }
         }
         __syncthreads();  // the per-warp region is read before a next head reuses it
-        if (warp != 0) continue;
+        if (warp != 0) return;
         // inverse value rotation (Hadamard-128, 1/sqrt(128), signs): stages
         // 1..16 by shuffles, 32 and 64 between the lane's four dims
         float v[4];
@@ -1251,6 +1241,34 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
             if constexpr (kMode == kDecodeScore) p.stat[unit * G + r] = make_float2(Mt_all, L);
             p.count[unit * G + r] = 0;
         }
+    };
+    if constexpr (kMode == kDecodePlain) {
+        float Mc[kHeadsPerCta], Lc[kHeadsPerCta], Oc[kHeadsPerCta];
+#pragma unroll
+        for (int j = 0; j < kHeadsPerCta; ++j) {
+            Mc[j] = -INFINITY;
+            Lc[j] = 0.0f;
+            Oc[j] = 0.0f;
+            if (crank + j * kCluster < G) reduce_head(crank + j * kCluster, Mc[j], Lc[j], Oc[j]);
+        }
+        cluster_arrive();  // this CTA has finished reading the other CTAs' partials
+#pragma unroll
+        for (int j = 0; j < kHeadsPerCta; ++j) {
+            const int r = crank + j * kCluster;
+            if (r >= G) continue;
+            store_head(r, Mc[j], Lc[j], Oc[j]);
+            finish_head(r);
+        }
+    } else {  // a CTA without a cluster has all the heads
+#pragma unroll 1
+        for (int r = crank; r < G; r += csize) {
+            float M, L, O;
+            reduce_head(r, M, L, O);
+            store_head(r, M, L, O);
+        }
+        cluster_arrive();
+#pragma unroll 1
+        for (int r = crank; r < G; r += csize) finish_head(r);
     }
     cluster_wait();  // no CTA leaves while another may still read its partials
 }
@@ -1280,14 +1298,15 @@ cudaError_t ensure_smem_attr() {
 }
 
 template <int BK, int BV>
-cudaLaunchConfig_t launch_config(dim3 grid, cudaStream_t s, int ws, cudaLaunchAttribute* attr /*[2]*/) {
+cudaLaunchConfig_t launch_config(dim3 grid, cudaStream_t s, int ws, cudaLaunchAttribute* attr /*[2]*/,
+                                 int cluster = kCluster) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(kWarps * 32, 1, 1);
     cfg.dynamicSmemBytes = decode_smem_bytes<BK, BV>(ws);
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kCluster;
+    attr[0].val.clusterDim.x = (unsigned)cluster;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1304,7 +1323,7 @@ cudaError_t launch_t(DecodeParams p, dim3 grid, cudaStream_t s, int kind) {
     const int ws = p.img_ws;
     p.img_bytes = decode_table_bytes(ws);
     cudaLaunchAttribute attr[2];
-    cudaLaunchConfig_t cfg = launch_config<BK, BV>(grid, s, ws, attr);
+    cudaLaunchConfig_t cfg = launch_config<BK, BV>(grid, s, ws, attr, p.cluster);
     if (kind == 2) return cudaLaunchKernelEx(&cfg, decode_kernel<BK, BV, 2, kPaged, kMode>, p);
     if constexpr (kMode == kDecodePlain) {  // (the other modes take their recent keys in the general instance)
         if (kind == 1) return cudaLaunchKernelEx(&cfg, decode_kernel<BK, BV, 1, kPaged, kMode>, p);

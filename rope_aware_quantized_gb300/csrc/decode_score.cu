@@ -39,14 +39,23 @@ __global__ void __launch_bounds__(kScoreThreads) score_add_kernel(ScoreParams p)
     const int fresh = p.pos_new ? p.pos_new[b] : -1;  // a new position has no weight yet
     pdl_wait();  // the logits, and the scores a previous kernel may be writing
     if (t0 >= seq) return;
-    float w0 = 0.0f, w1 = 0.0f;
+    // every head's statistics and logits in flight at once, then the sums in
+    // the heads' order
     const float* lg = p.logit + unit * p.G * (size_t)p.stride + t0;
-    for (int g = 0; g < p.G; ++g) {
-        const float2 st = p.stat[unit * p.G + g];
-        const float2 l = __ldcs(reinterpret_cast<const float2*>(lg + g * (size_t)p.stride));
-        const float inv = 1.0f / st.y;
-        w0 += fast_exp2(l.x - st.x) * inv;
-        w1 += fast_exp2(l.y - st.x) * inv;
+    float2 st[8], l[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+        if (g >= p.G) break;
+        st[g] = p.stat[unit * p.G + g];
+        l[g] = __ldcs(reinterpret_cast<const float2*>(lg + g * (size_t)p.stride));
+    }
+    float w0 = 0.0f, w1 = 0.0f;
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+        if (g >= p.G) break;
+        const float inv = 1.0f / st[g].y;
+        w0 += fast_exp2(l[g].x - st[g].x) * inv;
+        w1 += fast_exp2(l[g].y - st[g].x) * inv;
     }
     const size_t at = unit * (size_t)p.cap + t0;
     if (t0 + 1 < seq) {

@@ -21,7 +21,7 @@ struct QParams {
     const __half* k;
     const __half* v;
     int t_new, H;
-    const int32_t* pos_start;
+    const int32_t* pos_start;  // [B]; nullptr: position 0 of every sequence
     uint8_t* kc;
     float* kn;
     uint8_t* vc;

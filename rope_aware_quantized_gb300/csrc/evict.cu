@@ -4,19 +4,22 @@
 // all, and their records moved in position order into another packed cache.
 //
 // Two launches.  evict_select_kernel: one thread-block cluster per (sequence,
-// KV head), each CTA with a contiguous segment of the positions, its scores
-// in shared memory as integers of the same order.  The threshold (the score
-// that the last kept position has) is found by an exact radix selection: three
-// histograms of 11, 11 and 10 bits from the top, each summed over the cluster
-// through distributed shared memory, one cluster barrier apiece.  Equal
-// scores at the threshold are taken from the lowest position.  Every CTA then
-// counts its share, and its warps write their positions at the index that the
-// counts before them give: no atomics on global memory, the same result on
-// every run.  evict_move_kernel: 128 destination tokens per block; K records
-// and norms are copies; a V record holds two tokens' codes in alternating
-// bit fields, so each of its words is the even fields of one source word
-// (shifted down by one field if the token sat in the odd half) joined with
-// the odd fields of another.
+// KV head), each CTA with a contiguous segment of the positions, each warp
+// with a contiguous part of it, the scores in registers as integers of the
+// same order.  The threshold (the score that the last kept position has) is
+// found by an exact radix selection: three histograms of 11, 11 and 10 bits
+// from the top, each summed over the cluster through distributed shared
+// memory, one cluster barrier apiece.  Equal scores at the threshold are
+// taken from the lowest position.  Every CTA then counts its share, and its
+// warps write their positions at the index that the counts before them give:
+// no atomics on global memory, the same result on every run.  The kernel is
+// latency-bound (a few round trips per histogram), so a long sequence is
+// spread over up to 16 CTAs and every loop over a thread's keys is unrolled.
+// evict_move_kernel: 128 destination tokens per block; K records and norms
+// are copies; a V record holds two tokens' codes in alternating bit fields,
+// so each of its words is the even fields of one source word (shifted down by
+// one field if the token sat in the odd half) joined with the odd fields of
+// another.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -29,12 +32,10 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
-constexpr int kSelKeys = 32768;      // scores of a segment kept in shared memory (128 KB); longer ones are read again
-constexpr int kSelMaxCluster = 8;
-constexpr int kSelPerCta = 4096;     // positions a CTA takes before the cluster grows
+constexpr int kSelMaxCluster = 16;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveTok = 128;        // destination tokens of a block (even)
 
@@ -81,16 +82,19 @@ __device__ __forceinline__ uint32_t score_key(float f) {
     return (u >> 31) ? ~u : (u | 0x80000000u);
 }
 
-struct SelShared {
+struct __align__(16) SelShared {
     uint32_t hist[3][kSelBins];
+    uint32_t total[kSelBins];  // the cluster's histogram
     uint32_t warp_sum[kSelWarps];
     uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
     uint32_t cta_gt, cta_eq;
     uint32_t bin, above;
 };
 
-__global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictParams p, int keys_in_smem) {
-    extern __shared__ uint32_t s_key[];
+// KPT: keys per thread (8, 16 or 32; 32 KPT positions per warp), or 0: any
+// number, read from global memory on every pass.
+template <int KPT>
+__global__ void __launch_bounds__(kSelThreads, KPT > 16 ? 1 : 2) evict_select_kernel(EvictParams p) {
     __shared__ SelShared s;
     cg::cluster_group cluster = cg::this_cluster();
     const int crank = (int)cluster.block_rank(), csize = (int)cluster.num_blocks();
@@ -98,7 +102,7 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictParam
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const size_t unit = (size_t)b * p.H + h;
     evict_pdl_trigger();
-    for (int i = tid; i < 3 * kSelBins; i += kSelThreads) (&s.hist[0][0])[i] = 0;
+    for (int i = tid; i < 3 * kSelBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(&s.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
     evict_pdl_wait();
     const int n = evict_len(p, b, h == 0 && crank == 0 && tid == 0);
     const int m = min(n, p.keep);
@@ -112,44 +116,81 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictParam
     // candidates [c0, c1); the positions outside always stay
     const int c0 = p.sinks, c1 = n - p.recent;  // n > keep >= sinks + recent
     uint32_t need = (uint32_t)(p.keep - p.sinks - p.recent);
-    const int seg = ((n + csize - 1) / csize + 31) & ~31;
-    const int a0 = min(n, crank * seg), a1 = min(n, a0 + seg);
+    const bool none = need == 0;  // the sinks and the recent positions fill the budget
+    // the warp's positions: groups of 32 from w0
+    const int wn = KPT > 0 ? 32 * KPT : ((n + csize * kSelWarps - 1) / (csize * kSelWarps) + 31) & ~31;
+    const int w0 = (int)min((int64_t)n, ((int64_t)crank * kSelWarps + warp) * wn), w1 = (int)min((int64_t)n, (int64_t)w0 + wn);
     const float* row = p.scores + unit * (size_t)p.cap;
-    const bool in_smem = seg <= keys_in_smem;
-    if (in_smem) {
-        for (int i = a0 + tid; i < a1; i += kSelThreads) s_key[i - a0] = score_key(row[i]);
+    // keys of the lane's positions, and which of them are candidates (bit j)
+    uint32_t key[KPT > 0 ? KPT : 1], cand = 0;
+    if constexpr (KPT > 0) {
+        float x[KPT];
+#pragma unroll
+        for (int j = 0; j < KPT; ++j) {
+            const int i = w0 + 32 * j + lane;
+            x[j] = i < w1 ? __ldg(row + i) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < KPT; ++j) {
+            const int i = w0 + 32 * j + lane;
+            key[j] = score_key(x[j]);
+            cand |= (i < w1 && i >= c0 && i < c1 ? 1u : 0u) << j;
+        }
     }
-    __syncthreads();
-    auto key_at = [&](int i) -> uint32_t { return in_smem ? s_key[i - a0] : score_key(__ldg(row + i)); };
+    // f(position, key, whether it is a candidate) for every group of 32
+    // positions of the warp, in order
+    auto groups = [&](auto&& f) {
+        if constexpr (KPT > 0) {
+#pragma unroll
+            for (int j = 0; j < KPT; ++j) f(w0 + 32 * j + lane, key[j], ((cand >> j) & 1u) != 0);
+        } else {
+            for (int i0 = w0; i0 < w1; i0 += 32) {
+                const int i = i0 + lane;
+                f(i, i < w1 ? score_key(__ldg(row + i)) : 0u, i < w1 && i >= c0 && i < c1);
+            }
+        }
+    };
+    __syncthreads();  // the histograms are zero
 
     uint32_t prefix = 0;  // the threshold's bits found so far
-    for (int pass = 0; pass < 3 && need > 0; ++pass) {
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        if (none) break;
         const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
         const uint32_t mask = pass == 2 ? 1023u : 2047u;
-        const int lo = max(a0, c0), hi = min(a1, c1);
-        for (int i0 = lo; i0 < hi; i0 += kSelThreads) {
-            const int i = i0 + tid;
-            uint32_t digit = 0xFFFFFFFFu;
-            if (i < hi) {
-                const uint32_t k = key_at(i);
-                const bool mine = pass == 0 || (pass == 1 ? (k >> 21) == prefix : (k >> 10) == prefix);
-                if (mine) digit = (k >> shift) & mask;
+        uint32_t* hist = s.hist[pass];
+        groups([&](int, uint32_t k, bool in) {
+            if (in && (pass == 0 || (pass == 1 ? (k >> 21) == prefix : (k >> 10) == prefix)))
+                atomicAdd(hist + ((k >> shift) & mask), 1u);
+        });
+        // the cluster's histogram: CTA r sums a share of the bins over the
+        // cluster and writes it to every CTA (all bins read by every CTA
+        // would be csize times the traffic between the SMs)
+        const uint32_t* total = hist;
+        if (csize > 1) {
+            cluster.sync();
+            total = s.total;
+            const int share = kSelBins / csize, b0 = crank * share;  // (csize: a power of two)
+            for (int q = tid; q < share; q += kSelThreads) {
+                uint32_t r[kSelMaxCluster], sum = 0;
+#pragma unroll
+                for (int c = 0; c < kSelMaxCluster; ++c)
+                    r[c] = c < csize ? *cluster.map_shared_rank(hist + b0 + q, c) : 0u;
+#pragma unroll
+                for (int c = 0; c < kSelMaxCluster; ++c) sum += r[c];
+#pragma unroll
+                for (int c = 0; c < kSelMaxCluster; ++c)
+                    if (c < csize) *cluster.map_shared_rank(s.total + b0 + q, c) = sum;
             }
-            // lanes with the same digit add once (equal scores would
-            // serialise otherwise)
-            const uint32_t peers = __match_any_sync(0xFFFFFFFFu, digit);
-            if (digit != 0xFFFFFFFFu && lane == __ffs(peers) - 1) atomicAdd(&s.hist[pass][digit], (uint32_t)__popc(peers));
+            cluster.sync();
+        } else {
+            __syncthreads();
         }
-        cluster.sync();
-        // the cluster's histogram, two bins a thread from the top
-        const int hb = kSelBins - 2 - 2 * tid;
-        uint32_t v1 = 0, v0 = 0;  // bins hb + 1, hb
-        for (int c = 0; c < csize; ++c) {
-            const uint2 r = *reinterpret_cast<const uint2*>(cluster.map_shared_rank(&s.hist[pass][hb], c));
-            v0 += r.x;
-            v1 += r.y;
-        }
-        uint32_t inc = v0 + v1;
+        // four bins a thread, from the top
+        static_assert(kSelBins == 4 * kSelThreads, "16-byte reads of four bins");
+        const int hb = kSelBins - 4 * (tid + 1);
+        const uint4 v = *reinterpret_cast<const uint4*>(total + hb);
+        uint32_t inc = (v.x + v.y) + (v.z + v.w);
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
@@ -157,76 +198,69 @@ __global__ void __launch_bounds__(kSelThreads, 1) evict_select_kernel(EvictParam
         }
         if (lane == 31) s.warp_sum[warp] = inc;
         __syncthreads();
-        uint32_t before = 0;
-        for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
-        const uint32_t above1 = before + inc - v0 - v1, above0 = above1 + v1;
-        if (above1 < need && need <= above0) {
-            s.bin = (uint32_t)hb + 1;
-            s.above = above1;
-        } else if (above0 < need && need <= above0 + v0) {
-            s.bin = (uint32_t)hb;
-            s.above = above0;
+        const uint32_t before = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? s.warp_sum[lane] : 0u);
+        // candidates above bin hb + 3, hb + 2, hb + 1, hb; the bin that the
+        // need-th falls into
+        const uint32_t a3 = before + inc - ((v.x + v.y) + (v.z + v.w)), a2 = a3 + v.w, a1 = a2 + v.z, a0 = a1 + v.y;
+        if (a3 < need && need <= a0 + v.x) {
+            s.bin = (uint32_t)hb + (need <= a2 ? 3u : need <= a1 ? 2u : need <= a0 ? 1u : 0u);
+            s.above = need <= a2 ? a3 : need <= a1 ? a2 : need <= a0 ? a1 : a0;
         }
         __syncthreads();
         prefix = pass == 2 ? (prefix << 10) | s.bin : (prefix << 11) | s.bin;
         need -= s.above;
-        __syncthreads();  // warp_sum, bin and above are written again
+        // (warp_sum, bin, above and total are written again only after the
+        // next pass's first barrier)
     }
-    // threshold: candidates above `prefix` and the first `need` equal to it
-    // stay (none if the sinks and the recent positions fill the budget)
-    const bool none = p.keep == p.sinks + p.recent;
-    const int wseg = ((seg + kSelWarps - 1) / kSelWarps + 31) & ~31;
-    const int w0 = min(a1, a0 + warp * wseg), w1 = min(a1, w0 + wseg);
+    // threshold: candidates above `prefix` and the first `need` equal to it stay
     uint32_t gt = 0, eq = 0;
-    if (!none) {
-        for (int i0 = w0; i0 < w1; i0 += 32) {
-            const int i = i0 + lane;
-            const bool cand = i < w1 && i >= c0 && i < c1;
-            const uint32_t k = cand ? key_at(i) : 0u;
-            gt += (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, cand && k > prefix));
-            eq += (uint32_t)__popc(__ballot_sync(0xFFFFFFFFu, cand && k == prefix));
-        }
-    }
+    groups([&](int, uint32_t k, bool in) {
+        gt += in && !none && k > prefix ? 1u : 0u;
+        eq += in && !none && k == prefix ? 1u : 0u;
+    });
+    gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+    eq = __reduce_add_sync(0xFFFFFFFFu, eq);
     if (lane == 0) {
         s.warp_gt[warp] = gt;
         s.warp_eq[warp] = eq;
     }
     __syncthreads();
-    if (tid == 0) {
-        uint32_t g = 0, e = 0;
-        for (int w = 0; w < kSelWarps; ++w) {
-            const uint32_t wg = s.warp_gt[w], we = s.warp_eq[w];
-            s.warp_gt[w] = g;
-            s.warp_eq[w] = e;
-            g += wg;
-            e += we;
+    // candidates before the warp's positions: of its CTA's earlier warps, and
+    // of the cluster's earlier CTAs
+    uint32_t gb = lane < kSelWarps ? s.warp_gt[lane] : 0u, eb = lane < kSelWarps ? s.warp_eq[lane] : 0u;
+    if (warp == 0) {
+        const uint32_t g = __reduce_add_sync(0xFFFFFFFFu, gb), e = __reduce_add_sync(0xFFFFFFFFu, eb);
+        if (lane == 0) {
+            s.cta_gt = g;
+            s.cta_eq = e;
         }
-        s.cta_gt = g;
-        s.cta_eq = e;
     }
     cluster.sync();
-    uint32_t gb = s.warp_gt[warp], eb = s.warp_eq[warp];  // candidates before the warp's positions
-    for (int c = 0; c < crank; ++c) {
-        gb += *cluster.map_shared_rank(&s.cta_gt, c);
-        eb += *cluster.map_shared_rank(&s.cta_eq, c);
+    if (lane >= warp) gb = eb = 0u;
+    if (lane < crank) {
+        gb += *cluster.map_shared_rank(&s.cta_gt, lane);
+        eb += *cluster.map_shared_rank(&s.cta_eq, lane);
     }
-    for (int i0 = w0; i0 < w1; i0 += 32) {
-        const int i = i0 + lane;
-        const bool cand = i < w1 && i >= c0 && i < c1;
-        const uint32_t k = cand && !none ? key_at(i) : 0u;
-        const bool isg = cand && !none && k > prefix, ise = cand && !none && k == prefix;
-        const uint32_t bg = __ballot_sync(0xFFFFFFFFu, isg), be = __ballot_sync(0xFFFFFFFFu, ise);
-        const uint32_t lt = (1u << lane) - 1u;
-        const uint32_t g = gb + (uint32_t)__popc(bg & lt), e = eb + (uint32_t)__popc(be & lt);
-        const bool stays = i < w1 && (!cand || isg || (ise && e < need));
-        if (stays) {
-            const uint32_t always = (uint32_t)(min(i, c0) + max(0, i - c1));
-            kept[always + g + min(e, need)] = i;
+    gb = __reduce_add_sync(0xFFFFFFFFu, gb);
+    eb = __reduce_add_sync(0xFFFFFFFFu, eb);
+    // (no CTA leaves while another may read its counts)
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    // kept positions before the warp's: the ones that always stay among the
+    // w0 first positions, the candidates above the threshold, the equal ones
+    uint32_t at = (uint32_t)(min(w0, c0) + max(0, w0 - c1)) + gb + min(eb, need);
+    const uint32_t lt = (1u << lane) - 1u;
+    groups([&](int i, uint32_t k, bool in) {
+        bool stays = i < w1 && (!in || (!none && k > prefix));
+        const uint32_t be = __ballot_sync(0xFFFFFFFFu, in && !none && k == prefix);
+        if (be != 0) {
+            if (in && !none && k == prefix) stays = eb + (uint32_t)__popc(be & lt) < need;
+            eb += (uint32_t)__popc(be);
         }
-        gb += (uint32_t)__popc(bg);
-        eb += (uint32_t)__popc(be);
-    }
-    cluster.sync();  // no CTA leaves while another may read its counts
+        const uint32_t bs = __ballot_sync(0xFFFFFFFFu, stays);
+        if (stays) kept[at + (uint32_t)__popc(bs & lt)] = i;
+        at += (uint32_t)__popc(bs);
+    });
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Bits of the even tokens' fields in word w of a V record: bit i belongs to
@@ -244,7 +278,8 @@ template <int BV>
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p) {
     __shared__ int64_t s_src[kMoveTok];  // source record slot of each token
     __shared__ int64_t s_dst[kMoveTok];  // destination record slot (-1: not written)
-    __shared__ uint32_t s_even[8 * BV];
+    __shared__ int s_pos[kMoveTok];
+    __shared__ __align__(16) uint32_t s_even[8 * BV];
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const size_t unit = (size_t)b * p.H + h;
     evict_pdl_trigger();
@@ -262,45 +297,59 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
         if (src < 0) src = (int64_t)h << p.map.lp | (pos & ((1 << p.map.lp) - 1));  // an unmapped page: page 0 is read
         s_src[i] = src;
         s_dst[i] = dst;
-        p.dst_scores[unit * (size_t)p.dst_cap + d0 + i] = p.scores[unit * (size_t)p.cap + pos];
-        if (dst >= 0) {
-            p.dkn[dst] = p.kn[src];
-            p.dvn[dst] = p.vn[src];
-        }
+        s_pos[i] = pos;
     }
     __syncthreads();
-    // K records, 16 bytes a step
+    for (int i = tid; i < nt; i += kMoveThreads) {
+        p.dst_scores[unit * (size_t)p.dst_cap + d0 + i] = p.scores[unit * (size_t)p.cap + s_pos[i]];
+        if (s_dst[i] >= 0) {
+            p.dkn[s_dst[i]] = p.kn[s_src[i]];
+            p.dvn[s_dst[i]] = p.vn[s_src[i]];
+        }
+    }
+    // 16 bytes a step: the K records' pieces, then the V records'.  A V piece
+    // joins the even fields of one source with the odd ones of the other (of a
+    // single last token: the record's own odd fields stay).
     const uint4* ksrc = reinterpret_cast<const uint4*>(p.kc);
     uint4* kdst = reinterpret_cast<uint4*>(p.dkc);
-    for (int i = tid; i < nt * p.bk; i += kMoveThreads) {
-        const int t = i / p.bk, c = i - t * p.bk;
-        if (s_dst[t] >= 0) kdst[s_dst[t] * p.bk + c] = ksrc[s_src[t] * p.bk + c];
-    }
-    // V records, a word a step: the even fields of one source, the odd ones of
-    // the other (of a single last token: the record's own odd fields stay)
     const uint32_t* vsrc = reinterpret_cast<const uint32_t*>(p.vc);
     uint32_t* vdst = reinterpret_cast<uint32_t*>(p.dvc);
-    constexpr int kW = 8 * BV;
-    for (int i = tid; i < (nt + 1) / 2 * kW; i += kMoveThreads) {
-        const int pr = i / kW, w = i - pr * kW;
-        const int64_t dst = s_dst[2 * pr];
+    constexpr int kW = 8 * BV, kPieces = 2 * BV;
+    const int nk = nt * p.bk, n = nk + (nt + 1) / 2 * kPieces;
+#pragma unroll 3
+    for (int i = tid; i < n; i += kMoveThreads) {
+        if (i < nk) {
+            const int t = i / p.bk, c = i - t * p.bk;
+            const uint4 x = __ldcs(ksrc + s_src[t] * p.bk + c);
+            if (s_dst[t] >= 0) kdst[s_dst[t] * p.bk + c] = x;
+            continue;
+        }
+        const int pr = (i - nk) / kPieces, w = 4 * (i - nk - pr * kPieces);
+        const int64_t dst = s_dst[2 * pr], sa = s_src[2 * pr];
         if (dst < 0) continue;
-        const uint32_t even = s_even[w];
-        const int64_t sa = s_src[2 * pr];
-        const uint32_t* ra = vsrc + (sa >> 1) * kW;
-        uint32_t x = ra[w];
-        if (sa & 1) x = __funnelshift_r(x, w + 1 < kW ? ra[w + 1] : 0u, BV);
+        const uint32_t* ra = vsrc + (sa >> 1) * kW + w;
         uint32_t* out = vdst + (dst >> 1) * kW + w;
-        uint32_t y;
+        uint4 x = *reinterpret_cast<const uint4*>(ra), y;
+        if (sa & 1) {  // an odd token's fields move down to the even ones
+            const uint32_t up = w + 4 < kW ? ra[4] : 0u;
+            x = make_uint4(__funnelshift_r(x.x, x.y, BV), __funnelshift_r(x.y, x.z, BV), __funnelshift_r(x.z, x.w, BV),
+                           __funnelshift_r(x.w, up, BV));
+        }
         if (2 * pr + 1 < nt) {
             const int64_t sb = s_src[2 * pr + 1];
-            const uint32_t* rb = vsrc + (sb >> 1) * kW;
-            y = rb[w];
-            if (!(sb & 1)) y = __funnelshift_l(w > 0 ? rb[w - 1] : 0u, y, BV);
+            const uint32_t* rb = vsrc + (sb >> 1) * kW + w;
+            y = *reinterpret_cast<const uint4*>(rb);
+            if (!(sb & 1)) {  // an even token's fields move up
+                const uint32_t down = w > 0 ? rb[-1] : 0u;
+                y = make_uint4(__funnelshift_l(down, y.x, BV), __funnelshift_l(y.x, y.y, BV), __funnelshift_l(y.y, y.z, BV),
+                               __funnelshift_l(y.z, y.w, BV));
+            }
         } else {
-            y = *out;
+            y = *reinterpret_cast<const uint4*>(out);
         }
-        *out = (x & even) | (y & ~even);
+        const uint4 e = *reinterpret_cast<const uint4*>(s_even + w);
+        *reinterpret_cast<uint4*>(out) = make_uint4((x.x & e.x) | (y.x & ~e.x), (x.y & e.y) | (y.y & ~e.y),
+                                                    (x.z & e.z) | (y.z & ~e.z), (x.w & e.w) | (y.w & ~e.w));
     }
 }
 
@@ -316,9 +365,12 @@ cudaError_t launch_evict(const bgtq_plan& pl, cudaStream_t s, const bgtq_cache& 
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     {
         std::lock_guard<std::mutex> lock(mu);
-        if (!done[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       kSelKeys * (int)sizeof(uint32_t));
+        if (!done[dev]) {  // clusters of 16 CTAs
+            constexpr cudaFuncAttribute kAttr = cudaFuncAttributeNonPortableClusterSizeAllowed;
+            cudaError_t e = cudaFuncSetAttribute(evict_select_kernel<0>, kAttr, 1);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel<8>, kAttr, 1);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel<16>, kAttr, 1);
+            if (e == cudaSuccess) e = cudaFuncSetAttribute(evict_select_kernel<32>, kAttr, 1);
             if (e != cudaSuccess) return e;
             done[dev] = true;
         }
@@ -348,11 +400,13 @@ cudaError_t launch_evict(const bgtq_plan& pl, cudaStream_t s, const bgtq_cache& 
     p.H = pl.H;
     p.bk = pl.bk;
     p.status = status;
-    // a CTA for every kSelPerCta positions, up to a portable cluster
+    // CTAs per unit: as many as hold its keys in registers, 16 a thread, and
+    // more while they leave SMs idle and a thread has over 8 keys
     int csize = 1;
-    while (csize < kSelMaxCluster && (int64_t)csize * kSelPerCta < max_len) csize *= 2;
-    const int64_t seg = ((max_len + csize - 1) / csize + 31) / 32 * 32;
-    const int keys = seg <= kSelKeys ? (int)seg : 0;
+    const int64_t units = (int64_t)batch * pl.H, two_waves = 2 * (int64_t)std::max(1, pl.num_sms);
+    auto keys = [&] { return (max_len + (int64_t)csize * kSelThreads - 1) / ((int64_t)csize * kSelThreads); };
+    while (csize < kSelMaxCluster && (keys() > 16 || (units * csize * 2 <= two_waves && keys() > 8))) csize *= 2;
+    const int64_t kpt = keys();
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -363,11 +417,13 @@ cudaError_t launch_evict(const bgtq_plan& pl, cudaStream_t s, const bgtq_cache& 
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)csize, (unsigned)pl.H, (unsigned)batch);
     cfg.blockDim = dim3(kSelThreads, 1, 1);
-    cfg.dynamicSmemBytes = (size_t)keys * sizeof(uint32_t);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, p, keys);
+    cudaError_t e = kpt <= 8    ? cudaLaunchKernelEx(&cfg, evict_select_kernel<8>, p)
+                    : kpt <= 16 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<16>, p)
+                    : kpt <= 32 ? cudaLaunchKernelEx(&cfg, evict_select_kernel<32>, p)
+                                : cudaLaunchKernelEx(&cfg, evict_select_kernel<0>, p);
     if (e != cudaSuccess) return e;
     const int64_t most = std::min<int64_t>(keep, max_len);
     if (most == 0) return cudaSuccess;

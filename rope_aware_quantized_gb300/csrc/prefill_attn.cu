@@ -59,6 +59,7 @@ constexpr int kTcKeys = 128;                      // keys per tile
 constexpr int kTcThreads = 384;                   // two softmax warpgroups, the MMA warp, the TMA warp, 2 encoder warps
 constexpr int kEncWarps = 2;                      // warps that encode records alongside the attention
 constexpr int kEncWarp0 = 10;
+constexpr int kWinThreads = kEncWarp0 * 32;       // the windowed instance has no encoder warps
 constexpr uint32_t kTcTile = kTcRows * kD * 2;    // one 128 x 128 fp16 tile: 32 KB
 constexpr uint32_t kTcBox = kTcTile / 2;          // one 64-column box of it (128 rows x 128 B)
 constexpr uint32_t kOffQ = 0;                     // Q_g at + g kTcTile
@@ -244,7 +245,7 @@ __device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, i
 }
 
 template <bool kWin>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(kWin ? kWinThreads : kTcThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, PfParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -285,6 +286,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
+    // (windowed: a dependent launch of the append; nothing an earlier kernel
+    // may still read or write is touched before this)
+    if constexpr (kWin) asm volatile("griddepcontrol.wait;" ::: "memory");
 
     if (warp == 9) {
         // ---- TMA: Q of the CTA's heads, then K and V tiles through two stages
@@ -330,9 +334,60 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         __syncwarp();
     } else if (warp == 8) {
         // ---- MMA issue
-        if (lane == 0) {
-            constexpr uint32_t idS = instr_desc(kTcRows, kTcKeys, 0);
-            constexpr uint32_t idO = instr_desc(kTcRows, kD, 1);
+        constexpr uint32_t idS = instr_desc(kTcRows, kTcKeys, 0);
+        constexpr uint32_t idO = instr_desc(kTcRows, kD, 1);
+        if constexpr (kWin) {
+            // the whole warp runs the loop, an elected lane issues
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+            auto wait = [&](int bar, uint32_t parity) -> bool {
+                return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity & 1u, abort_flag, p.status));
+            };
+            auto issue_s = [&](int g, int j) {
+                const uint32_t qa = sbase + kOffQ + g * kTcTile, ka = sbase + kOffK + (j & 1) * kTcTile;
+#pragma unroll
+                for (int k = 0; k < kD / 16; ++k) {
+                    const uint32_t off = (uint32_t)(k >> 2) * kTcBox + (uint32_t)(k & 3) * 32;
+                    mma_ss_warp(tm + 128u * g, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), idS, k > 0);
+                }
+                mma_commit_warp(BAR(kBarS + g));
+            };
+            auto issue_pv = [&](int g, int j) {
+                const uint32_t va = sbase + kOffV + (j & 1) * kTcTile;
+#pragma unroll
+                for (int k = 0; k < kTcKeys / 16; ++k)
+                    mma_ts_warp(tm + 256u + 128u * g, tm + 128u * g + 8u * k, smem_desc(va + 2048u * k, kTcBox, 1024), idO,
+                                (j > 0 || k > 0) ? 1u : 0u);
+            };
+            bool ok = wait(kBarQ, 0) && wait(kBarKFull, 0);
+            if (ok) {
+                tc_fence_after();
+                for (int g = 0; g < ng; ++g) issue_s(g, 0);
+                mma_commit_warp(BAR(kBarKEmpty));
+            }
+            for (int j = 0; ok && j < nkt; ++j) {
+                const int s = j & 1;
+                const bool next = j + 1 < nkt;
+                if (!wait(kBarVFull + s, (uint32_t)(j >> 1))) break;
+                for (int g = 0; g < ng && ok; ++g) {
+                    ok = wait(kBarP + g, (uint32_t)j);
+                    if (ok && next && g == 0) ok = wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_pv(g, j);
+                    if (next) {
+                        issue_s(g, j + 1);
+                    } else {
+                        mma_commit_warp(BAR(kBarO + g));
+                    }
+                }
+                if (!ok) break;
+                mma_commit_warp(BAR(kBarVEmpty + s));
+                if (next) mma_commit_warp(BAR(kBarKEmpty + (s ^ 1)));
+            }
+            // every MMA issued has completed before the CTA ends
+            mma_commit_warp(BAR(kBarDrain));
+            mbar_wait(BAR(kBarDrain), 0, abort_flag, p.status, false);
+        } else if (lane == 0) {
             auto issue_s = [&](int g, int j) {
                 const uint32_t qa = sbase + kOffQ + g * kTcTile, ka = sbase + kOffK + (j & 1) * kTcTile;
 #pragma unroll
@@ -381,7 +436,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             mbar_wait(BAR(kBarDrain), 0, abort_flag, p.status, false);
         }
         __syncwarp();
-    } else if (warp >= kEncWarp0) {
+    } else if (!kWin && warp >= kEncWarp0) {
         // ---- record encoder: the block's 128 positions are shared out over
         // the CTAs of the KV head's query-head pairs (an even share each, so a
         // V pair record is never split); encoded while the others attend
@@ -469,10 +524,22 @@ cudaError_t launch_prefill(const bgtq_plan& pl, cudaStream_t s, const void* q, c
     p.window = win ? win->span : 0;
     p.lse = win ? win->lse : nullptr;
     const dim3 grid((unsigned)units, (unsigned)nqb, 1);
-    if (win)
-        prefill_kernel<true><<<grid, kTcThreads, kTcSmem, s>>>(tq, tk, tv, p);
-    else
-        prefill_kernel<false><<<grid, kTcThreads, kTcSmem, s>>>(tq, tk, tv, p);
+    if (win) {
+        const cudaError_t e = launch_quantize_append(pl, s, k, v, batch, t, nullptr, c, status);
+        if (e != cudaSuccess) return e;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr.val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = grid;
+        cfg.blockDim = dim3(kWinThreads, 1, 1);
+        cfg.dynamicSmemBytes = kTcSmem;
+        cfg.stream = s;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, prefill_kernel<true>, tq, tk, tv, p);
+    }
+    prefill_kernel<false><<<grid, kTcThreads, kTcSmem, s>>>(tq, tk, tv, p);
     return cudaGetLastError();
 }
 
