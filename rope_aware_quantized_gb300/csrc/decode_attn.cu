@@ -143,11 +143,11 @@ SplitPlan decode_split_bounded(const bgtq_plan& p, int batch, int64_t max_len) {
     constexpr int64_t kFixed = 400;
     SplitPlan best;
     int64_t best_cost = INT64_MAX;
-    for (int64_t ns = (len + kMaxSplitTokens - 1) / kMaxSplitTokens; ns <= kMaxClusters; ++ns) {
+    for (int64_t ns = (len + kMaxSplitTokensBounded - 1) / kMaxSplitTokensBounded; ns <= kMaxClusters; ++ns) {
         const int64_t slack = ns > 1 ? std::min<int64_t>(256, (len + ns - 1) / ns / 4) / kTile * kTile : 0;
         int64_t tps = (len + slack + ns - 1) / ns;
         tps = std::max<int64_t>((tps + kTile - 1) / kTile * kTile, (int64_t)kWarps * kTile);
-        if (tps > kMaxSplitTokens) continue;
+        if (tps > kMaxSplitTokensBounded) continue;
         const int64_t cost = (units * ns + slots - 1) / slots * (kFixed + tps);
         if (cost >= best_cost) continue;
         best_cost = cost;

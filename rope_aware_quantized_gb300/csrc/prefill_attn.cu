@@ -155,11 +155,23 @@ __device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, i
             const int k0 = kt.tile(j) * kTcKeys;
             // the diagonal tile, and tiles with a key that the block's last
             // row is past the window of, unless all of them are sinks
-            if (j == 0 || (k0 <= q0 + kTcRows - 1 - p.window && k0 + kTcKeys > p.sinks)) {
-                const int lim = min(row, p.T - 1) - k0, low = row - p.window - k0, sk = p.sinks - k0;
+            const int low = row - p.window - k0, sk = p.sinks - k0;
+            if (j == 0) {
+                const int lim = min(row, p.T - 1) - k0;
 #pragma unroll
                 for (int k = 0; k < kTcKeys; ++k)
-                    if (k > lim || (k <= low && k >= sk)) s[k] = -INFINITY;
+                    if (k > lim) s[k] = -INFINITY;
+            }
+            if (k0 <= q0 + kTcRows - 1 - p.window && sk < kTcKeys) {
+                if (sk <= 0) {
+#pragma unroll
+                    for (int k = 0; k < kTcKeys; ++k)
+                        if (k <= low) s[k] = -INFINITY;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kTcKeys; ++k)
+                        if (k <= low && k >= sk) s[k] = -INFINITY;
+                }
             }
         } else if (j == nkt - 1) {  // the diagonal tile: keys after the row, and past the prompt
             const int lim = min(row, p.T - 1) - j * kTcKeys;
@@ -200,6 +212,22 @@ __device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, i
         }
         uint32_t pk[kTcKeys / 2];
         float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if constexpr (kWin) {
+            const uint64_t c2 = pack2(c, c), m2 = pack2(-m, -m);
+            uint64_t l2[4];
+#pragma unroll
+            for (int i = 0; i < kTcKeys / 2; ++i) {
+                const uint64_t e = exp2_pair(fma2(pack2(s[2 * i], s[2 * i + 1]), c2, m2));
+                l2[i & 3] = i < 4 ? e : add2(l2[i & 3], e);
+                const float2 w = unpack2(e);
+                pk[i] = pack_h2(w.x, w.y);
+            }
+            const float2 a = unpack2(add2(l2[0], l2[1])), b2 = unpack2(add2(l2[2], l2[3]));
+            ls[0] = a.x;
+            ls[1] = a.y;
+            ls[2] = b2.x;
+            ls[3] = b2.y;
+        } else
 #pragma unroll
         for (int i = 0; i < kTcKeys / 2; ++i) {
             const float p0 = ex2(fmaf(s[2 * i], c, -m)), p1 = ex2(fmaf(s[2 * i + 1], c, -m));
@@ -367,10 +395,10 @@ __global__ void __launch_bounds__(kWin ? kWinThreads : kTcThreads, 1)
             for (int j = 0; ok && j < nkt; ++j) {
                 const int s = j & 1;
                 const bool next = j + 1 < nkt;
-                if (!wait(kBarVFull + s, (uint32_t)(j >> 1))) break;
+                // (the tiles first: their waits pass while the softmax runs)
+                ok = wait(kBarVFull + s, (uint32_t)(j >> 1)) && (!next || wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)));
                 for (int g = 0; g < ng && ok; ++g) {
                     ok = wait(kBarP + g, (uint32_t)j);
-                    if (ok && next && g == 0) ok = wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1));
                     if (!ok) break;
                     tc_fence_after();
                     issue_pv(g, j);

@@ -90,35 +90,6 @@ struct PsParams {
     int32_t* status;
 };
 
-// ---- weights 2^x of pairs of values
-
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-// 2^x of both.  (A polynomial on the FMA pipe for a share of the pairs was
-// slower: 134, 142 and 159 us with 1, 2 and 3 of 8 against 125 for 8191 rows x
-// 16 query heads; the special-function unit is not what bounds the kernels.)
-__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
-    const float2 v = unpack2(x);
-    return pack2(ex2(v.x), ex2(v.y));
-}
 // A row's log-sum-exp; -inf for a row that does not count.
 __device__ __forceinline__ float row_lse(const PsParams& p, const float* lse_row, int row, bool counts) {
     return counts && row < p.T ? __ldg(lse_row + row) : -INFINITY;
