@@ -538,7 +538,8 @@ int bgtq_prefill_score(const bgtq_plan* plan, void* stream, const void* q_fp16, 
  *                Positions past the kept ones are left as they are, also the
  *                odd half of a last V pair record.
  *   dst_scores   device, [batch][H][dst capacity] float
- *   dst_lens     device, [batch] int32: min(n, keep)
+ *   dst_lens     device, [batch] int32: min(n, keep); may be the seq_lens of the
+ *                next call on the stream
  *   kept         device, [batch][H][keep] int32: the source positions, -1
  *                past them
  * Two launches; every result is the same on every run.

@@ -411,10 +411,18 @@ def _need(x, name: str, dtype, shape):
         raise ValueError(f"{name} must be a CUDA tensor")
 
 
+def _here(x):
+    """The tensor is on the current device (the kernels launch there)."""
+    import torch
+    if x.get_device() != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 def _decode_args(plan: Plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new):
     import torch
     batch = q_fp16.shape[0]
     _need(q_fp16, "q", torch.float16, (batch, plan.n_kv_heads * plan.group, HEAD_DIM))
+    _here(q_fp16)
     _need(out, "out", out.dtype, q_fp16.shape)
     _need(seq_lens, "seq_lens", torch.int32, (batch,))
     if cache.batch < batch:
@@ -482,6 +490,7 @@ def bgtq_prefill_window_attn(plan: Plan, q_fp16, k_fp16, v_fp16, cache: Cache, s
     import torch
     b, hq, t, d = q_fp16.shape
     _need(q_fp16, "q", torch.float16, (b, plan.n_kv_heads * plan.group, t, HEAD_DIM))
+    _here(q_fp16)
     _need(k_fp16, "k", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM))
     _need(v_fp16, "v", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM))
     _need(out, "out", out.dtype, q_fp16.shape)
@@ -512,6 +521,7 @@ def bgtq_prefill_score(plan: Plan, q_fp16, k_fp16, lse, scores, workspace=None, 
     import torch
     b, hq, t, d = q_fp16.shape
     _need(q_fp16, "q", torch.float16, (b, plan.n_kv_heads * plan.group, t, HEAD_DIM))
+    _here(q_fp16)
     _need(k_fp16, "k", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM))
     _need(lse, "lse", torch.float32, (b, hq, t))
     _need(scores, "scores", torch.float32, (b, plan.n_kv_heads, scores.shape[-1]))
@@ -532,6 +542,7 @@ def bgtq_evict(plan: Plan, cache: Cache, scores, seq_lens, max_len: int, keep: i
     import torch
     batch = seq_lens.shape[0]
     _need(seq_lens, "seq_lens", torch.int32, (batch,))
+    _here(seq_lens)
     _need(scores, "scores", torch.float32, (batch, plan.n_kv_heads, cache.capacity))
     _need(dst_scores, "dst_scores", torch.float32, (batch, plan.n_kv_heads, dst.capacity))
     _need(dst_lens, "dst_lens", torch.int32, (batch,))

@@ -979,6 +979,16 @@ int bgtq_prefill_chunk_attn(const bgtq_plan* p, void* stream, const void* q, con
 
 namespace {
 
+// The plan's device tables, on the current device.
+int check_plan_here(const bgtq_plan* p) {
+    const int rc = check_plan(p);
+    if (rc) return rc;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev != p->device)
+        return set_error(BGTQ_ERR_INVALID_ARG, "the plan was built on device %d, the current device is %d", p->device, dev);
+    return BGTQ_OK;
+}
+
 // Arguments that the windowed and the scoring decode share.
 int check_decode_call(const bgtq_plan* p, const void* q, const void* k_new, const void* v_new, const int32_t* pos_new,
                       const bgtq_cache* c, const int32_t* seq_lens, int64_t max_len, int batch, const void* out,
@@ -1056,7 +1066,7 @@ int bgtq_decode_window_attn(const bgtq_plan* p, void* stream, const void* q, con
     if (rc) return rc;
     if ((rc = check_window(sinks, window))) return rc;
     if (batch == 0) return BGTQ_OK;
-    if ((rc = check_plan(p))) return rc;
+    if ((rc = check_plan_here(p))) return rc;
     max_len = std::min(max_len, c->capacity);
     const SplitPlan sp = decode_split_bounded(*p, batch, decode_window_positions(max_len, sinks, window));
     const size_t need = decode_workspace_bytes(*p, batch, sp);
@@ -1092,7 +1102,7 @@ int bgtq_decode_score_attn(const bgtq_plan* p, void* stream, const void* q, cons
     const size_t nb = (size_t)batch * p->H * (size_t)c->capacity * sizeof(float);
     if (scores_in != scores_out && overlap(scores_in, nb, scores_out, nb))
         return set_error(BGTQ_ERR_INVALID_ARG, "scores_in and scores_out are one array or do not overlap");
-    if ((rc = check_plan(p))) return rc;
+    if ((rc = check_plan_here(p))) return rc;
     max_len = std::min(max_len, c->capacity);
     const SplitPlan sp = decode_split_bounded(*p, batch, max_len);
     const ScoreWorkspace w = score_workspace(*p, batch, max_len, sp);
@@ -1130,7 +1140,7 @@ int bgtq_prefill_window_attn(const bgtq_plan* p, void* stream, const void* q, co
     if (batch > 65535) return set_error(BGTQ_ERR_UNSUPPORTED, "at most 65535 sequences per call");
     if ((uint64_t)batch * p->H * p->G * (uint64_t)t + 128 >= (1ull << 31))
         return set_error(BGTQ_ERR_UNSUPPORTED, "batch * query heads * t must stay below 2^31 - 128");
-    if ((rc = check_plan(p))) return rc;
+    if ((rc = check_plan_here(p))) return rc;
     const PrefillWindow w = {(int)std::min<int64_t>(sinks, t), (int)std::min<int64_t>(window, t), lse};
     const cudaError_t e =
         launch_prefill(*p, (cudaStream_t)stream, q, k, v, batch, t, *c, out, out_dtype, scale, status, &w);
@@ -1170,7 +1180,7 @@ int bgtq_prefill_score(const bgtq_plan* p, void* stream, const void* q, const vo
     if (ws_bytes < need) return set_error(BGTQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
     if (need > 0 && (!ws || (reinterpret_cast<uintptr_t>(ws) & 15)))
         return set_error(BGTQ_ERR_INVALID_ARG, "workspace must be a 16-byte aligned device buffer");
-    if ((rc = check_plan(p))) return rc;
+    if ((rc = check_plan_here(p))) return rc;
     const cudaError_t e = launch_prefill_score(*p, (cudaStream_t)stream, q, k, lse, batch, t, row0, (int)std::min<int64_t>(sinks, t),
                                                (int)std::min<int64_t>(window, t), scale, scores, score_stride, ws, status);
     if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "prefill_score launch: %s", cudaGetErrorString(e));
@@ -1185,6 +1195,8 @@ int bgtq_evict(const bgtq_plan* p, void* stream, const bgtq_cache* c, const floa
     if (rc || (rc = check_cache(p, dst))) return rc;
     if (batch < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and max_len must be >= 0");
     if (keep < 1 || keep > INT32_MAX) return set_error(BGTQ_ERR_INVALID_ARG, "keep must be in [1, 2^31)");
+    if (std::min(max_len, c->capacity) > INT32_MAX - (1 << 20))
+        return set_error(BGTQ_ERR_UNSUPPORTED, "sequences of at most 2^31 - 2^20 positions");
     if (sinks < 0 || recent < 0 || sinks > keep || recent > keep - sinks)
         return set_error(BGTQ_ERR_INVALID_ARG, "sinks and recent must be >= 0 and sinks + recent at most keep");
     if (c->recent > 0 || dst->recent > 0)
@@ -1217,7 +1229,7 @@ int bgtq_evict(const bgtq_plan* p, void* stream, const bgtq_cache* c, const floa
     if (overlap(scores, units * (size_t)c->capacity * 4, dst_scores, units * (size_t)dst->capacity * 4) ||
         overlap(seq_lens, (size_t)batch * 4, dst_lens, (size_t)batch * 4))
         return set_error(BGTQ_ERR_INVALID_ARG, "dst_scores or dst_lens overlaps scores or seq_lens");
-    if ((rc = check_plan(p))) return rc;
+    if ((rc = check_plan_here(p))) return rc;
     const cudaError_t e = launch_evict(*p, (cudaStream_t)stream, *c, scores, seq_lens, max_len, batch, (int)keep, (int)sinks,
                                        (int)recent, *dst, dst_scores, dst_lens, kept, status);
     if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "evict launch: %s", cudaGetErrorString(e));

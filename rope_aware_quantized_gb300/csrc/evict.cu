@@ -101,14 +101,16 @@ __global__ void __launch_bounds__(kSelThreads, KPT > 16 ? 1 : 2) evict_select_ke
     const int h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const size_t unit = (size_t)b * p.H + h;
-    evict_pdl_trigger();
+    // (with nothing to move no kernel of this call follows, and the lengths
+    // written here may be what the next one reads before it waits)
+    if (p.max_len > 0) evict_pdl_trigger();
     for (int i = tid; i < 3 * kSelBins / 4; i += kSelThreads) reinterpret_cast<uint4*>(&s.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
     evict_pdl_wait();
     const int n = evict_len(p, b, h == 0 && crank == 0 && tid == 0);
     const int m = min(n, p.keep);
     int32_t* kept = p.kept + unit * (size_t)p.keep;
     if (h == 0 && crank == 0 && tid == 0) p.dst_lens[b] = m;
-    for (int i = m + crank * kSelThreads + tid; i < p.keep; i += csize * kSelThreads) kept[i] = -1;
+    for (int64_t i = (int64_t)m + crank * kSelThreads + tid; i < p.keep; i += csize * kSelThreads) kept[i] = -1;
     if (n <= p.keep) {  // everything stays (the whole cluster leaves here)
         for (int i = crank * kSelThreads + tid; i < n; i += csize * kSelThreads) kept[i] = i;
         return;
@@ -280,9 +282,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
     __shared__ int64_t s_dst[kMoveTok];  // destination record slot (-1: not written)
     __shared__ int s_pos[kMoveTok];
     __shared__ __align__(16) uint32_t s_even[8 * BV];
+    // No early start of the next kernel from here: it may be a decode, which
+    // reads its lengths before it waits, and those may be dst_lens.
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const size_t unit = (size_t)b * p.H + h;
-    evict_pdl_trigger();
     if (tid < 8 * BV) s_even[tid] = even_fields<BV>(tid);
     const int m = min(evict_len(p, b, false), p.keep);
     const int d0 = blockIdx.x * kMoveTok;

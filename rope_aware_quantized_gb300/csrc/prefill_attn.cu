@@ -328,20 +328,26 @@ __global__ void __launch_bounds__(kWin ? kWinThreads : kTcThreads, 1)
                 for (int x = 0; x < 2; ++x)
                     tma_load_2d(sbase + kOffQ + g * kTcTile + x * kTcBox, &tq, 64 * x, qrow + g * p.T, BAR(kBarQ));
             const int krow = (b * p.H + h) * p.T;
+            auto load_tile = [&](uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
+                if constexpr (kWin)
+                    tma_load_3d(dst, map, x, row, b * p.H + h, bar);
+                else
+                    tma_load_2d(dst, map, x, krow + row, bar);
+            };
             for (int j = 0; j < nkt; ++j) {
                 const int s = j & 1;
                 const uint32_t par = (uint32_t)((j >> 1) - 1) & 1u;
                 if (j >= 2 && !mbar_wait(BAR(kBarKEmpty + s), par, abort_flag, p.status)) break;
                 mbar_expect_tx(BAR(kBarKFull + s), kTcTile);
                 for (int x = 0; x < 2; ++x)
-                    tma_load_2d(sbase + kOffK + s * kTcTile + x * kTcBox, &tk, 64 * x, krow + kt.tile(j) * kTcKeys, BAR(kBarKFull + s));
+                    load_tile(sbase + kOffK + s * kTcTile + x * kTcBox, &tk, 64 * x, kt.tile(j) * kTcKeys, BAR(kBarKFull + s));
                 if (j >= 2 && !mbar_wait(BAR(kBarVEmpty + s), par, abort_flag, p.status)) {
                     used[s] = 2 * j + 1;  // K of tile j in flight, V not
                     break;
                 }
                 mbar_expect_tx(BAR(kBarVFull + s), kTcTile);
                 for (int x = 0; x < 2; ++x)
-                    tma_load_2d(sbase + kOffV + s * kTcTile + x * kTcBox, &tv, 64 * x, krow + kt.tile(j) * kTcKeys, BAR(kBarVFull + s));
+                    load_tile(sbase + kOffV + s * kTcTile + x * kTcBox, &tv, 64 * x, kt.tile(j) * kTcKeys, BAR(kBarVFull + s));
                 used[s] = 2 * j + 2;
             }
             // every copy issued has landed before the CTA ends (normally at
@@ -522,8 +528,10 @@ cudaError_t launch_prefill(const bgtq_plan& pl, cudaStream_t s, const void* q, c
         }
     }
     alignas(64) CUtensorMap tq, tk, tv;
-    if (!rows_map(&tq, q, q_rows, kTcRows) || !rows_map(&tk, k, (uint64_t)batch * pl.H * t, kTcKeys) ||
-        !rows_map(&tv, v, (uint64_t)batch * pl.H * t, kTcKeys))
+    const uint64_t kv = (uint64_t)batch * pl.H;
+    if (!rows_map(&tq, q, q_rows, kTcRows) ||
+        !(win ? heads_map(&tk, k, kv, t, kTcKeys) && heads_map(&tv, v, kv, t, kTcKeys)
+              : rows_map(&tk, k, kv * t, kTcKeys) && rows_map(&tv, v, kv * t, kTcKeys)))
         return cudaErrorInvalidValue;
     PfParams p;
     p.q = static_cast<const __half*>(q);

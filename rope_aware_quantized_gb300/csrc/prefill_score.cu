@@ -134,7 +134,7 @@ __device__ __forceinline__ void load_row_tile(const CUtensorMap* tq, uint32_t ds
         const int g = g_first + min(head_tile * (cols / p.box) + u, n_heads - 1);
         for (int r = 0; r < p.box; r += step)
             for (int x = 0; x < 2; ++x)
-                tma_load_2d(dst + x * box_bytes + (uint32_t)(u * p.box + r) * 128u, tq, 64 * x, (bh * p.G + g) * p.T + row + r, bar);
+                tma_load_3d(dst + x * box_bytes + (uint32_t)(u * p.box + r) * 128u, tq, 64 * x, row + r, bh * p.G + g, bar);
     }
 }
 
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                 if (m >= 1 && !mbar_wait(BAR(kPsBarKEmpty), (uint32_t)(m - 1) & 1u, abort_flag, p.status)) break;
                 mbar_expect_tx(BAR(kPsBarK), 2 * kPsTile);
                 for (int x = 0; x < 4; ++x)
-                    tma_load_2d(sbase + x * kPsBox, &tk, 64 * (x & 1), it.bh * p.T + it.k0 + kPsKeys * (x >> 1), BAR(kPsBarK));
+                    tma_load_3d(sbase + x * kPsBox, &tk, 64 * (x & 1), it.k0 + kPsKeys * (x >> 1), it.bh, BAR(kPsBarK));
                 ++m;
                 int ht = 0, q = 0;  // head group and row tile
                 for (int i = 0; i < rt.n; ++i, ++t) {
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                 if (n >= kPrStages && !mbar_wait(BAR(kPrBarEmpty + s), (uint32_t)(n / kPrStages - 1) & 1u, abort_flag, p.status)) break;
                 mbar_expect_tx(BAR(kPrBarFull + s), kPsTile);
                 for (int x = 0; x < 2; ++x)
-                    tma_load_2d(skey + s * kPsTile + x * kPsBox, &tk, 64 * x, bh * p.T + kt * kPsKeys, BAR(kPrBarFull + s));
+                    tma_load_3d(skey + s * kPsTile + x * kPsBox, &tk, 64 * x, kt * kPsKeys, bh, BAR(kPrBarFull + s));
                 ++n;
             }
             // every copy issued has landed before the CTA ends
@@ -627,8 +627,8 @@ cudaError_t launch_prefill_score(const bgtq_plan& pl, cudaStream_t s, const void
     }
     const PsPlan sp = ps_plan(pl, batch, t, row0);
     alignas(64) CUtensorMap tq, tk;
-    if (!rows_map(&tq, q, (uint64_t)batch * pl.H * pl.G * t, (uint32_t)std::min(sp.box, 128)) ||
-        !rows_map(&tk, k, (uint64_t)batch * pl.H * t, kPsKeys))
+    if (!heads_map(&tq, q, (uint64_t)batch * pl.H * pl.G, t, (uint32_t)std::min(sp.box, 128)) ||
+        !heads_map(&tk, k, (uint64_t)batch * pl.H, t, kPsKeys))
         return cudaErrorInvalidValue;
     PsParams p;
     p.lse = lse;

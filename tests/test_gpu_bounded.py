@@ -638,3 +638,59 @@ def test_bounded_run_captured_and_on_another_stream():
         g.replay()
         torch.cuda.synchronize()
         check(i)
+
+
+@pytest.mark.parametrize("T", [100, 129])
+def test_prompt_calls_keep_what_is_not_finite_to_its_own_head(T):
+    """A head of NaN and infinities: the heads before it, whose last tiles end inside it, are as without it."""
+    L = Layer(31, 2, 2, 384, 3, [T, T])
+    q, k, v = prompt(L)
+    res = []
+    for bad in (False, True):
+        if bad:
+            q[1], k[1], v[1] = np.nan, np.inf, np.nan
+            q[1, 0], k[1, 0], v[1, 0] = np.inf, np.nan, -np.inf
+        out = torch.zeros(q.shape, dtype=torch.float32, device="cuda")
+        lse = torch.zeros(q.shape[:3], device="cuda")
+        bg.bgtq_prefill_window_attn(L.plan, dev(q), dev(k), dev(v), L.cache(T + T % 2), 3, 40, out, lse=lse)
+        got = [out[0].clone(), lse[0].clone()]
+        for row0 in (0, T - 9):
+            scores = torch.zeros((2, 2, T), device="cuda")
+            n = bg.bgtq_prefill_score_workspace(L.plan, 2, T, row0)
+            bg.bgtq_prefill_score(L.plan, dev(q), dev(k), lse, scores, zeros_ws(n), row0=row0, sinks=3, window=40)
+            got.append(scores[0].clone())
+        res.append(got)
+    torch.cuda.synchronize()
+    for a, b in zip(*res):
+        assert torch.isfinite(b).all() and torch.equal(a, b)
+
+
+def test_evicted_lengths_go_straight_into_decode():
+    """dst_lens as the next call's seq_lens, with nothing in between: a decode reads its lengths before it waits."""
+    L = Layer(32, 2, 4, 384, 3, [900, 700, 60])
+    cap = 900
+    cache = L.cache(cap)
+    L.fill(cache)
+    scores = dev(score_kinds("spread", (3, 2, cap), 3))
+    q = dev(L.q)
+    for keep in (300, 40, 64, 500, 33):
+        dst = L.cache(keep + keep % 2)
+        ds = torch.zeros((3, 2, dst.capacity), device="cuda")
+        kept = torch.zeros((3, 2, keep), dtype=torch.int32, device="cuda")
+        lens = lens32([0, 0, 0])
+        ws = zeros_ws(bg.bgtq_decode_window_workspace(L.plan, 3, keep, 2, 20))
+        ws2 = zeros_ws(bg.bgtq_decode_score_workspace(L.plan, 3, keep))
+        out = [torch.zeros((3, 8, 128), device="cuda") for _ in range(4)]
+        src_lens = lens32(L.lens)
+        torch.cuda.synchronize()
+        bg.bgtq_evict(L.plan, cache, scores, src_lens, cap, keep, 2, 5, dst, ds, lens, kept)
+        bg.bgtq_decode_window_attn(L.plan, q, dst, lens, keep, 2, 20, out[0], ws)
+        bg.bgtq_evict(L.plan, cache, scores, src_lens, cap, keep, 2, 5, dst, ds, lens, kept)
+        bg.bgtq_decode_score_attn(L.plan, q, dst, lens, keep, ds, ds, out[1], ws2)
+        torch.cuda.synchronize()
+        assert lens.tolist() == [min(n, keep) for n in L.lens]
+        bg.bgtq_decode_window_attn(L.plan, q, dst, lens, keep, 2, 20, out[2], ws)
+        torch.cuda.synchronize()
+        bg.bgtq_decode_score_attn(L.plan, q, dst, lens, keep, ds, ds, out[3], ws2)
+        torch.cuda.synchronize()
+        assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
