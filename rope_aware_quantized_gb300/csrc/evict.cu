@@ -38,6 +38,7 @@ constexpr int kSelBins = 2048;
 constexpr int kSelMaxCluster = 16;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveTok = 128;        // destination tokens of a block (even)
+constexpr int kMoveBatch = 2;        // record pieces of a thread in flight (1: 19.1 us for 128K -> 32K, 2: 18.7, 3: 18.4; for 32 x 8 units 63, 64, 72 us)
 
 __device__ __forceinline__ void evict_pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void evict_pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
@@ -303,56 +304,72 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
         s_pos[i] = pos;
     }
     __syncthreads();
+    // (all of a step's loads before its stores: the compiler may not move a
+    // load over a store that could overlap it)
     for (int i = tid; i < nt; i += kMoveThreads) {
-        p.dst_scores[unit * (size_t)p.dst_cap + d0 + i] = p.scores[unit * (size_t)p.cap + s_pos[i]];
+        const float sc = __ldg(p.scores + unit * (size_t)p.cap + s_pos[i]), kn = __ldg(p.kn + s_src[i]), vn = __ldg(p.vn + s_src[i]);
+        p.dst_scores[unit * (size_t)p.dst_cap + d0 + i] = sc;
         if (s_dst[i] >= 0) {
-            p.dkn[s_dst[i]] = p.kn[s_src[i]];
-            p.dvn[s_dst[i]] = p.vn[s_src[i]];
+            p.dkn[s_dst[i]] = kn;
+            p.dvn[s_dst[i]] = vn;
         }
     }
-    // 16 bytes a step: the K records' pieces, then the V records'.  A V piece
-    // joins the even fields of one source with the odd ones of the other (of a
-    // single last token: the record's own odd fields stay).
+    // 16-byte pieces, kMoveBatch a thread at a time: the K records' pieces,
+    // then the V records'.  A V piece joins the even fields of one source with
+    // the odd ones of the other (of a single last token: the record's own odd
+    // fields stay).
     const uint4* ksrc = reinterpret_cast<const uint4*>(p.kc);
     uint4* kdst = reinterpret_cast<uint4*>(p.dkc);
     const uint32_t* vsrc = reinterpret_cast<const uint32_t*>(p.vc);
     uint32_t* vdst = reinterpret_cast<uint32_t*>(p.dvc);
     constexpr int kW = 8 * BV, kPieces = 2 * BV;
     const int nk = nt * p.bk, n = nk + (nt + 1) / 2 * kPieces;
-#pragma unroll 3
-    for (int i = tid; i < n; i += kMoveThreads) {
-        if (i < nk) {
-            const int t = i / p.bk, c = i - t * p.bk;
-            const uint4 x = __ldcs(ksrc + s_src[t] * p.bk + c);
-            if (s_dst[t] >= 0) kdst[s_dst[t] * p.bk + c] = x;
-            continue;
-        }
-        const int pr = (i - nk) / kPieces, w = 4 * (i - nk - pr * kPieces);
-        const int64_t dst = s_dst[2 * pr], sa = s_src[2 * pr];
-        if (dst < 0) continue;
-        const uint32_t* ra = vsrc + (sa >> 1) * kW + w;
-        uint32_t* out = vdst + (dst >> 1) * kW + w;
-        uint4 x = *reinterpret_cast<const uint4*>(ra), y;
-        if (sa & 1) {  // an odd token's fields move down to the even ones
-            const uint32_t up = w + 4 < kW ? ra[4] : 0u;
-            x = make_uint4(__funnelshift_r(x.x, x.y, BV), __funnelshift_r(x.y, x.z, BV), __funnelshift_r(x.z, x.w, BV),
-                           __funnelshift_r(x.w, up, BV));
-        }
-        if (2 * pr + 1 < nt) {
-            const int64_t sb = s_src[2 * pr + 1];
-            const uint32_t* rb = vsrc + (sb >> 1) * kW + w;
-            y = *reinterpret_cast<const uint4*>(rb);
-            if (!(sb & 1)) {  // an even token's fields move up
-                const uint32_t down = w > 0 ? rb[-1] : 0u;
-                y = make_uint4(__funnelshift_l(down, y.x, BV), __funnelshift_l(y.x, y.y, BV), __funnelshift_l(y.y, y.z, BV),
-                               __funnelshift_l(y.z, y.w, BV));
+    for (int i0 = tid; i0 < n; i0 += kMoveBatch * kMoveThreads) {
+        uint4 x[kMoveBatch], y[kMoveBatch];
+        uint32_t up[kMoveBatch], down[kMoveBatch];
+#pragma unroll
+        for (int u = 0; u < kMoveBatch; ++u) {
+            const int i = i0 + u * kMoveThreads;
+            if (i < nk) {
+                const int t = i / p.bk;
+                x[u] = __ldg(ksrc + s_src[t] * p.bk + (i - t * p.bk));
+            } else if (i < n) {
+                const int pr = (i - nk) / kPieces, w = 4 * (i - nk - pr * kPieces);
+                const uint32_t* ra = vsrc + (s_src[2 * pr] >> 1) * kW + w;
+                x[u] = __ldg(reinterpret_cast<const uint4*>(ra));
+                up[u] = w + 4 < kW ? __ldg(ra + 4) : 0u;
+                if (2 * pr + 1 < nt) {
+                    const uint32_t* rb = vsrc + (s_src[2 * pr + 1] >> 1) * kW + w;
+                    y[u] = __ldg(reinterpret_cast<const uint4*>(rb));
+                    down[u] = w > 0 ? __ldg(rb - 1) : 0u;
+                } else if (s_dst[2 * pr] >= 0) {
+                    y[u] = *reinterpret_cast<const uint4*>(vdst + (s_dst[2 * pr] >> 1) * kW + w);
+                }
             }
-        } else {
-            y = *reinterpret_cast<const uint4*>(out);
         }
-        const uint4 e = *reinterpret_cast<const uint4*>(s_even + w);
-        *reinterpret_cast<uint4*>(out) = make_uint4((x.x & e.x) | (y.x & ~e.x), (x.y & e.y) | (y.y & ~e.y),
-                                                    (x.z & e.z) | (y.z & ~e.z), (x.w & e.w) | (y.w & ~e.w));
+#pragma unroll
+        for (int u = 0; u < kMoveBatch; ++u) {
+            const int i = i0 + u * kMoveThreads;
+            if (i < nk) {
+                const int t = i / p.bk;
+                if (s_dst[t] >= 0) kdst[s_dst[t] * p.bk + (i - t * p.bk)] = x[u];
+            } else if (i < n) {
+                const int pr = (i - nk) / kPieces, w = 4 * (i - nk - pr * kPieces);
+                const int64_t dst = s_dst[2 * pr];
+                if (dst < 0) continue;
+                uint4 a = x[u], b4 = y[u];
+                if (s_src[2 * pr] & 1)  // an odd token's fields move down to the even ones
+                    a = make_uint4(__funnelshift_r(a.x, a.y, BV), __funnelshift_r(a.y, a.z, BV), __funnelshift_r(a.z, a.w, BV),
+                                   __funnelshift_r(a.w, up[u], BV));
+                if (2 * pr + 1 < nt && !(s_src[2 * pr + 1] & 1))  // an even token's fields move up
+                    b4 = make_uint4(__funnelshift_l(down[u], b4.x, BV), __funnelshift_l(b4.x, b4.y, BV),
+                                    __funnelshift_l(b4.y, b4.z, BV), __funnelshift_l(b4.z, b4.w, BV));
+                const uint4 e = *reinterpret_cast<const uint4*>(s_even + w);
+                *reinterpret_cast<uint4*>(vdst + (dst >> 1) * kW + w) =
+                    make_uint4((a.x & e.x) | (b4.x & ~e.x), (a.y & e.y) | (b4.y & ~e.y), (a.z & e.z) | (b4.z & ~e.z),
+                               (a.w & e.w) | (b4.w & ~e.w));
+            }
+        }
     }
 }
 
@@ -403,12 +420,13 @@ cudaError_t launch_evict(const bgtq_plan& pl, cudaStream_t s, const bgtq_cache& 
     p.H = pl.H;
     p.bk = pl.bk;
     p.status = status;
-    // CTAs per unit: as many as hold its keys in registers, 16 a thread, and
-    // more while they leave SMs idle and a thread has over 8 keys
+    // CTAs per unit: as few as hold its keys in registers, and more while they
+    // leave SMs idle and a thread has over 8 keys (32 x 8 units of up to 16384
+    // positions: 64 us with a CTA each, 74 with clusters of two)
     int csize = 1;
     const int64_t units = (int64_t)batch * pl.H, two_waves = 2 * (int64_t)std::max(1, pl.num_sms);
     auto keys = [&] { return (max_len + (int64_t)csize * kSelThreads - 1) / ((int64_t)csize * kSelThreads); };
-    while (csize < kSelMaxCluster && (keys() > 16 || (units * csize * 2 <= two_waves && keys() > 8))) csize *= 2;
+    while (csize < kSelMaxCluster && (keys() > 32 || (units * csize * 2 <= two_waves && keys() > 8))) csize *= 2;
     const int64_t kpt = keys();
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -294,17 +294,19 @@ __global__ void __launch_bounds__(kPsThreads, 1)
                 tc_fence_after();
                 const uint32_t qa = srow + s * kPsTile, acc = acc0 + (uint32_t)(2 * kPsCols * b);
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    mma_ss_warp(acc + (uint32_t)(kPsCols * j), smem_desc(sbase + kPsOffKeyExt, 16, 1024),
-                                smem_desc(sbase + kPsOffRowExt + b * kPsBox, 16, 1024), idS, 0);
-#pragma unroll
                 for (int k = 0; k < kD / 16; ++k) {
                     const uint32_t off = (uint32_t)(k >> 2) * kPsBox + (uint32_t)(k & 3) * 32;
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         mma_ss_warp(acc + (uint32_t)(kPsCols * j), smem_desc(sbase + j * kPsTile + off, 16, 1024),
-                                    smem_desc(qa + off, 16, 1024), idS, 1);
+                                    smem_desc(qa + off, 16, 1024), idS, k > 0);
                 }
+                // (the ninth step last: the sum is large only then, and the
+                // tensor cores' roundings go by its size)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    mma_ss_warp(acc + (uint32_t)(kPsCols * j), smem_desc(sbase + kPsOffKeyExt, 16, 1024),
+                                smem_desc(sbase + kPsOffRowExt + b * kPsBox, 16, 1024), idS, 1);
                 mma_commit_warp(BAR(kPsBarS + b));
                 mma_commit_warp(BAR(kPsBarQEmpty + s));
             }
@@ -490,12 +492,12 @@ __global__ void __launch_bounds__(kPsThreads, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t acc = acc0 + (uint32_t)(N * a), ka = skey + s * kPsTile;
-            mma_ss_warp(acc, smem_desc(sbase + PL::kOffKeyExt, 16, 1024), smem_desc(sbase + PL::kOffRowExt, 16, 1024), idS, 0);
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k) {
                 const uint32_t x = (uint32_t)(k >> 2), off = (uint32_t)(k & 3) * 32;
-                mma_ss_warp(acc, smem_desc(ka + x * kPsBox + off, 16, 1024), smem_desc(sbase + x * PL::kRowBox + off, 16, 1024), idS, 1);
+                mma_ss_warp(acc, smem_desc(ka + x * kPsBox + off, 16, 1024), smem_desc(sbase + x * PL::kRowBox + off, 16, 1024), idS, k > 0);
             }
+            mma_ss_warp(acc, smem_desc(sbase + PL::kOffKeyExt, 16, 1024), smem_desc(sbase + PL::kOffRowExt, 16, 1024), idS, 1);
             mma_commit_warp(BAR(kPrBarS + a));
             mma_commit_warp(BAR(kPrBarEmpty + s));
             ++n;
