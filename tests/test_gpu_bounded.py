@@ -363,6 +363,8 @@ def test_prefill_window(T, B, sinks, window, half, bits, hg):
     (640, 1, 100, 17, 129, (1, 4)),
     (515, 1, 0, 130, 64, (1, 3)),
     (1300, 1, 0, 4, 1300, (1, 8)),       # query heads shared out over CTAs
+    (1300, 2, 37, 0, 200, (2, 3)),       # and row tiles, under a window
+    (2100, 1, 0, 0, 2100, (1, 1)),       # row tiles alone
 ])
 def test_prefill_score(T, B, row0, sinks, window, hg):
     L = Layer(12, hg[0], hg[1], 384, 3, [T] * B)
