@@ -418,8 +418,10 @@ int bgtq_decode_attn_noalloc(const bgtq_plan* plan, void* stream, const void* q_
  */
 
 /* Workspace bytes of bgtq_decode_window_attn for `batch` sequences no longer
- * than max_len (zero-filled once before first use; every call leaves its
- * counters zero).  Errors: INVALID_ARG. */
+ * than max_len; enough for a call with any smaller max_len, sinks or window.
+ * Zero-filled once before first use; every call leaves its counters zero (as
+ * many as the batch, the query heads and no others: a workspace that changes
+ * its batch or its plan is zero-filled again).  Errors: INVALID_ARG. */
 int bgtq_decode_window_workspace(const bgtq_plan* plan, int batch, int64_t max_len, int64_t sinks, int64_t window,
                                  size_t* bytes);
 
@@ -449,8 +451,8 @@ int bgtq_decode_window_attn(const bgtq_plan* plan, void* stream, const void* q_f
                             int32_t* dev_status);
 
 /* Workspace bytes of bgtq_decode_score_attn: the decode's, and 4 bytes for
- * every (sequence, query head, position up to max_len).  Zero-filled once
- * before first use. */
+ * every (sequence, query head, position up to max_len); enough for any smaller
+ * max_len.  Zero-filled as bgtq_decode_window_attn's. */
 int bgtq_decode_score_workspace(const bgtq_plan* plan, int batch, int64_t max_len, size_t* bytes);
 
 /*
@@ -482,7 +484,9 @@ int bgtq_decode_score_attn(const bgtq_plan* plan, void* stream, const void* q_fp
  *                row i sees
  * Records, other arguments and errors as bgtq_prefill_attn; also INVALID_ARG
  * for sinks < 0 or window < 1.  Key tiles that no row of a query block sees
- * are neither loaded nor multiplied.
+ * are neither loaded nor multiplied.  q, k and v are finite: as in
+ * bgtq_prefill_attn a value that is not reaches the rows of its head's other
+ * positions within 128, seen or not.
  */
 int bgtq_prefill_window_attn(const bgtq_plan* plan, void* stream, const void* q_fp16, const void* k_fp16,
                              const void* v_fp16, int batch, int t, int64_t sinks, int64_t window,
@@ -500,7 +504,8 @@ int bgtq_prefill_score_workspace(const bgtq_plan* plan, int batch, int t, int ro
  *   q_fp16, k_fp16  as bgtq_prefill_attn (the prompt's own tokens)
  *   lse          device, [batch][H*G][t] float as bgtq_prefill_window_attn
  *                wrote it for the same (sinks, window); rows before row0 are
- *                not read; a row whose lse is -inf gives nothing
+ *                not read; a row whose lse is -inf gives nothing, one of
+ *                |lse / softmax_scale| above 1.6e7 NaN
  *   row0         0 <= row0 <= t: 0 counts every row, t - n the last n
  *   scores       device, [batch][H][score_stride] float: positions 0 .. t-1
  *                overwritten, the rest left; score_stride >= t
@@ -508,7 +513,7 @@ int bgtq_prefill_score_workspace(const bgtq_plan* plan, int batch, int t, int ro
  *                (NULL if 0)
  * fp16 tensor-core products, float32 sums in a fixed order.
  * Errors: INVALID_ARG, UNSUPPORTED (sizes past 2^31 rows, t > 8388480, more
- * than 65535 sequences x KV heads), WORKSPACE, CUDA.
+ * than 65535 sequences x KV heads, softmax_scale < 1e-6), WORKSPACE, CUDA.
  */
 int bgtq_prefill_score(const bgtq_plan* plan, void* stream, const void* q_fp16, const void* k_fp16, const float* lse,
                        int batch, int t, int row0, int64_t sinks, int64_t window, float softmax_scale, float* scores,

@@ -44,11 +44,11 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, dev: int | None = None) -> int | None:
     if stream is None:
         import torch
         # (the handle alone: building a Stream object costs a small call as much again)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -399,9 +399,9 @@ def _out_dtype(out) -> int:
     raise ValueError("out must be float16 or float32")
 
 
-def _need(x, name: str, dtype, shape):
-    """A contiguous CUDA tensor of this type and shape."""
-    if x.dtype == dtype and x.shape == shape and x.is_contiguous() and x.is_cuda:
+def _need(x, name: str, dtype, shape, dev: int):
+    """A contiguous tensor of this type and shape on device dev (the current one: the kernels launch there)."""
+    if x.dtype == dtype and x.shape == shape and x.is_contiguous() and x.get_device() == dev:
         return
     if x.dtype != dtype or tuple(x.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
@@ -409,31 +409,48 @@ def _need(x, name: str, dtype, shape):
         raise ValueError(f"{name} must be contiguous")
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    raise ValueError(f"{name} is on {x.device}, the current device is cuda:{dev}")
 
 
-def _here(x):
-    """The tensor is on the current device (the kernels launch there)."""
+def _device(x) -> int:
+    """The current device, or for a tensor of the host a number that _need refuses."""
     import torch
-    if x.get_device() != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {x.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return torch._C._cuda_getDevice() if x.is_cuda else -2
 
 
-def _decode_args(plan: Plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new):
+def _scratch(x, name: str, dev: int) -> int:
+    """Bytes of a workspace tensor."""
+    if not (x.get_device() == dev and x.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on the current device")
+    return x.numel() * x.element_size()
+
+
+def _on_device(cache, status, dev: int):
+    """A cache's buffers and the status word."""
+    buf = getattr(cache, "k_codes", None)  # (a view holds no tensors)
+    if buf is not None and buf.get_device() != dev:
+        raise ValueError(f"the cache is on {buf.device}, the current device is cuda:{dev}")
+    if status is not None and (status.get_device() != dev or status.element_size() != 4):
+        raise ValueError("status must be an int32 CUDA tensor on the current device")
+
+
+def _decode_args(plan: Plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new, status):
     import torch
     batch = q_fp16.shape[0]
-    _need(q_fp16, "q", torch.float16, (batch, plan.n_kv_heads * plan.group, HEAD_DIM))
-    _here(q_fp16)
-    _need(out, "out", out.dtype, q_fp16.shape)
-    _need(seq_lens, "seq_lens", torch.int32, (batch,))
+    dev = _device(q_fp16)
+    _need(q_fp16, "q", torch.float16, (batch, plan.n_kv_heads * plan.group, HEAD_DIM), dev)
+    _need(out, "out", out.dtype, q_fp16.shape, dev)
+    _need(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    _on_device(cache, status, dev)
     if cache.batch < batch:
         raise ValueError("the cache holds fewer sequences than q")
     if (k_new is None) != (v_new is None) or (k_new is None) != (pos_new is None):
         raise ValueError("k_new, v_new and pos_new are given together or not at all")
     if k_new is not None:
-        _need(k_new, "k_new", torch.float16, (batch, plan.n_kv_heads, HEAD_DIM))
-        _need(v_new, "v_new", torch.float16, (batch, plan.n_kv_heads, HEAD_DIM))
-        _need(pos_new, "pos_new", torch.int32, (batch,))
-    return batch
+        _need(k_new, "k_new", torch.float16, (batch, plan.n_kv_heads, HEAD_DIM), dev)
+        _need(v_new, "v_new", torch.float16, (batch, plan.n_kv_heads, HEAD_DIM), dev)
+        _need(pos_new, "pos_new", torch.int32, (batch,), dev)
+    return batch, dev
 
 
 def bgtq_decode_window_workspace(plan: Plan, batch: int, max_len: int, sinks: int, window: int) -> int:
@@ -446,15 +463,15 @@ def bgtq_decode_window_attn(plan: Plan, q_fp16, cache: Cache, seq_lens, max_len:
                             workspace, k_new=None, v_new=None, pos_new=None, softmax_scale: float | None = None,
                             status=None, stream=None):
     """Decode attention over positions [0, sinks) and [seq_len - window, seq_len) of the packed cache
-    (q: [B][H*G][128] float16; out: same shape, float16 or float32; workspace: a zeroed uint8 CUDA
-    tensor of bgtq_decode_window_workspace bytes).  With k_new, v_new ([B][H][128] float16) and
+    (q: [B][H*G][128] float16; out: same shape, float16 or float32; workspace: a uint8 CUDA tensor of
+    bgtq_decode_window_workspace bytes, zeroed before its first use with this plan and batch).  With k_new, v_new ([B][H][128] float16) and
     pos_new ([B] int32) the new token is quantize-appended first, in the same launch."""
-    batch = _decode_args(plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new)
+    batch, dev = _decode_args(plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new, status)
     scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
-    _check(lib().bgtq_decode_window_attn(plan.handle, _stream(stream), _ptr(q_fp16), _ptr(k_new), _ptr(v_new), _ptr(pos_new),
+    _check(lib().bgtq_decode_window_attn(plan.handle, _stream(stream, dev), _ptr(q_fp16), _ptr(k_new), _ptr(v_new), _ptr(pos_new),
                                          C.byref(cache.desc), _ptr(seq_lens), max_len, batch, sinks, window, _ptr(out),
-                                         _out_dtype(out), scale, _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(), _ptr(status)))
+                                         _out_dtype(out), scale, _ptr(workspace), _scratch(workspace, "workspace", dev),
+                                         _ptr(status)))
 
 
 def bgtq_decode_score_workspace(plan: Plan, batch: int, max_len: int) -> int:
@@ -472,14 +489,14 @@ def bgtq_decode_score_attn(plan: Plan, q_fp16, cache: Cache, seq_lens, max_len: 
     scores_in; positions from seq_len on are left as they are).  Other arguments as
     bgtq_decode_window_attn; a new token's position starts from a score of 0."""
     import torch
-    batch = _decode_args(plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new)
+    batch, dev = _decode_args(plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new, status)
     for x, name in ((scores_in, "scores_in"), (scores_out, "scores_out")):
-        _need(x, name, torch.float32, (batch, plan.n_kv_heads, cache.capacity))
+        _need(x, name, torch.float32, (batch, plan.n_kv_heads, cache.capacity), dev)
     scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
-    _check(lib().bgtq_decode_score_attn(plan.handle, _stream(stream), _ptr(q_fp16), _ptr(k_new), _ptr(v_new), _ptr(pos_new),
+    _check(lib().bgtq_decode_score_attn(plan.handle, _stream(stream, dev), _ptr(q_fp16), _ptr(k_new), _ptr(v_new), _ptr(pos_new),
                                         C.byref(cache.desc), _ptr(seq_lens), max_len, batch, _ptr(scores_in),
                                         _ptr(scores_out), _ptr(out), _out_dtype(out), scale, _ptr(workspace),
-                                        workspace.numel() * workspace.element_size(), _ptr(status)))
+                                        _scratch(workspace, "workspace", dev), _ptr(status)))
 
 
 def bgtq_prefill_window_attn(plan: Plan, q_fp16, k_fp16, v_fp16, cache: Cache, sinks: int, window: int, out, lse=None,
@@ -489,17 +506,18 @@ def bgtq_prefill_window_attn(plan: Plan, q_fp16, k_fp16, v_fp16, cache: Cache, s
     [B][H*G][T] float32 tensor that receives every row's log-sum-exp of its visible logits."""
     import torch
     b, hq, t, d = q_fp16.shape
-    _need(q_fp16, "q", torch.float16, (b, plan.n_kv_heads * plan.group, t, HEAD_DIM))
-    _here(q_fp16)
-    _need(k_fp16, "k", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM))
-    _need(v_fp16, "v", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM))
-    _need(out, "out", out.dtype, q_fp16.shape)
+    dev = _device(q_fp16)
+    _need(q_fp16, "q", torch.float16, (b, plan.n_kv_heads * plan.group, t, HEAD_DIM), dev)
+    _need(k_fp16, "k", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM), dev)
+    _need(v_fp16, "v", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM), dev)
+    _need(out, "out", out.dtype, q_fp16.shape, dev)
     if lse is not None:
-        _need(lse, "lse", torch.float32, (b, hq, t))
+        _need(lse, "lse", torch.float32, (b, hq, t), dev)
+    _on_device(cache, status, dev)
     if cache.batch < b:
         raise ValueError("the cache holds fewer sequences than q")
     scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
-    _check(lib().bgtq_prefill_window_attn(plan.handle, _stream(stream), _ptr(q_fp16), _ptr(k_fp16), _ptr(v_fp16), b, t, sinks,
+    _check(lib().bgtq_prefill_window_attn(plan.handle, _stream(stream, dev), _ptr(q_fp16), _ptr(k_fp16), _ptr(v_fp16), b, t, sinks,
                                           window, C.byref(cache.desc), _ptr(out), _out_dtype(out), scale, _ptr(lse),
                                           _ptr(status)))
 
@@ -520,15 +538,16 @@ def bgtq_prefill_score(plan: Plan, q_fp16, k_fp16, lse, scores, workspace=None, 
     workspace: a uint8 CUDA tensor of bgtq_prefill_score_workspace bytes (None if that is 0)."""
     import torch
     b, hq, t, d = q_fp16.shape
-    _need(q_fp16, "q", torch.float16, (b, plan.n_kv_heads * plan.group, t, HEAD_DIM))
-    _here(q_fp16)
-    _need(k_fp16, "k", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM))
-    _need(lse, "lse", torch.float32, (b, hq, t))
-    _need(scores, "scores", torch.float32, (b, plan.n_kv_heads, scores.shape[-1]))
+    dev = _device(q_fp16)
+    _need(q_fp16, "q", torch.float16, (b, plan.n_kv_heads * plan.group, t, HEAD_DIM), dev)
+    _need(k_fp16, "k", torch.float16, (b, plan.n_kv_heads, t, HEAD_DIM), dev)
+    _need(lse, "lse", torch.float32, (b, hq, t), dev)
+    _need(scores, "scores", torch.float32, (b, plan.n_kv_heads, scores.shape[-1]), dev)
+    _on_device(None, status, dev)
     scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
-    _check(lib().bgtq_prefill_score(plan.handle, _stream(stream), _ptr(q_fp16), _ptr(k_fp16), _ptr(lse), b, t, row0, sinks,
+    _check(lib().bgtq_prefill_score(plan.handle, _stream(stream, dev), _ptr(q_fp16), _ptr(k_fp16), _ptr(lse), b, t, row0, sinks,
                                     max(t, 1) if window is None else window, scale, _ptr(scores), scores.shape[-1],
-                                    _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                    _ptr(workspace), 0 if workspace is None else _scratch(workspace, "workspace", dev),
                                     _ptr(status)))
 
 
@@ -541,15 +560,17 @@ def bgtq_evict(plan: Plan, cache: Cache, scores, seq_lens, max_len: int, keep: i
     seq_lens, dst_lens [B] int32; kept [B][H][keep] int32: the source positions, -1 past them."""
     import torch
     batch = seq_lens.shape[0]
-    _need(seq_lens, "seq_lens", torch.int32, (batch,))
-    _here(seq_lens)
-    _need(scores, "scores", torch.float32, (batch, plan.n_kv_heads, cache.capacity))
-    _need(dst_scores, "dst_scores", torch.float32, (batch, plan.n_kv_heads, dst.capacity))
-    _need(dst_lens, "dst_lens", torch.int32, (batch,))
-    _need(kept, "kept", torch.int32, (batch, plan.n_kv_heads, keep))
+    dev = _device(seq_lens)
+    _need(seq_lens, "seq_lens", torch.int32, (batch,), dev)
+    _need(scores, "scores", torch.float32, (batch, plan.n_kv_heads, cache.capacity), dev)
+    _need(dst_scores, "dst_scores", torch.float32, (batch, plan.n_kv_heads, dst.capacity), dev)
+    _need(dst_lens, "dst_lens", torch.int32, (batch,), dev)
+    _need(kept, "kept", torch.int32, (batch, plan.n_kv_heads, keep), dev)
+    _on_device(cache, status, dev)
+    _on_device(dst, None, dev)
     if cache.batch < batch or dst.batch < batch:
         raise ValueError("a cache holds fewer sequences than seq_lens")
-    _check(lib().bgtq_evict(plan.handle, _stream(stream), C.byref(cache.desc), _ptr(scores), _ptr(seq_lens), max_len, batch,
+    _check(lib().bgtq_evict(plan.handle, _stream(stream, dev), C.byref(cache.desc), _ptr(scores), _ptr(seq_lens), max_len, batch,
                             keep, sinks, recent, C.byref(dst.desc), _ptr(dst_scores), _ptr(dst_lens), _ptr(kept),
                             _ptr(status)))
 

@@ -1032,7 +1032,7 @@ ScoreWorkspace score_workspace(const bgtq_plan& p, int batch, int64_t max_len, c
     const size_t rows = (size_t)batch * p.H * p.G;
     ScoreWorkspace w;
     w.stride = (max_len + 15) / 16 * 16;
-    w.stat = up(decode_workspace_bytes(p, batch, sp));
+    w.stat = up(decode_bounded_workspace_bytes(p, batch, sp));
     w.logit = w.stat + up(rows * sizeof(float2));
     w.bytes = w.logit + up(rows * (size_t)w.stride * sizeof(float));
     return w;
@@ -1053,8 +1053,9 @@ int bgtq_decode_window_workspace(const bgtq_plan* p, int batch, int64_t max_len,
     if (batch < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and max_len must be >= 0");
     const int rc = check_window(sinks, window);
     if (rc) return rc;
-    *bytes = decode_workspace_bytes(*p, batch,
-                                    decode_split_bounded(*p, batch, decode_window_positions(max_len, sinks, window)));
+    max_len = std::min<int64_t>(max_len, INT32_MAX);  // (no cache holds more)
+    *bytes = decode_bounded_workspace_bytes(
+        *p, batch, decode_split_bounded(*p, batch, decode_window_positions(max_len, sinks, window)));
     return BGTQ_OK;
 }
 
@@ -1069,7 +1070,7 @@ int bgtq_decode_window_attn(const bgtq_plan* p, void* stream, const void* q, con
     if ((rc = check_plan_here(p))) return rc;
     max_len = std::min(max_len, c->capacity);
     const SplitPlan sp = decode_split_bounded(*p, batch, decode_window_positions(max_len, sinks, window));
-    const size_t need = decode_workspace_bytes(*p, batch, sp);
+    const size_t need = decode_bounded_workspace_bytes(*p, batch, sp);
     if (ws_bytes < need) return set_error(BGTQ_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
     DecodeExtra x;
     x.max_len = max_len;
@@ -1085,6 +1086,7 @@ int bgtq_decode_window_attn(const bgtq_plan* p, void* stream, const void* q, con
 int bgtq_decode_score_workspace(const bgtq_plan* p, int batch, int64_t max_len, size_t* bytes) {
     if (!p || !bytes) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
     if (batch < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch and max_len must be >= 0");
+    max_len = std::min<int64_t>(max_len, INT32_MAX);  // (no cache holds more)
     *bytes = score_workspace(*p, batch, max_len, decode_split_bounded(*p, batch, max_len)).bytes;
     return BGTQ_OK;
 }
@@ -1172,6 +1174,7 @@ int bgtq_prefill_score(const bgtq_plan* p, void* stream, const void* q, const vo
         return set_error(BGTQ_ERR_INVALID_ARG, "lse and scores must be 4-byte aligned");
     if (score_stride < t) return set_error(BGTQ_ERR_INVALID_ARG, "score_stride must be at least t");
     if (!(scale > 0.0f) || !std::isfinite(scale)) return set_error(BGTQ_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+    if (scale < 1e-6f) return set_error(BGTQ_ERR_UNSUPPORTED, "softmax_scale below 1e-6");
     if ((uint64_t)batch * p->H * p->G * (uint64_t)t + 128 >= (1ull << 31) || t > 65535 * 128 ||
         (int64_t)batch * p->H > 65535)
         return set_error(BGTQ_ERR_UNSUPPORTED,

@@ -219,12 +219,15 @@ struct SplitPlan {
     int tokens_per_split = 64;
     int slack = 0;  // the newest range (split 0) holds about this many tokens fewer
     int cluster = 8;  // splits whose partials one thread-block cluster merges
+    int parts = 0;    // windowed and scoring decode: partials of a unit that the workspace has room for
 };
 SplitPlan decode_split(const bgtq_plan& p, int batch, int64_t max_len);
 // The split of the windowed and the scoring decode: as decode_split, or, when
 // its clusters would not fit the GPU at once, splits without clusters.
 SplitPlan decode_split_bounded(const bgtq_plan& p, int batch, int64_t max_len);
 size_t decode_workspace_bytes(const bgtq_plan& p, int batch, const SplitPlan& sp);
+// The same for decode_split_bounded: never less for a longer max_len.
+size_t decode_bounded_workspace_bytes(const bgtq_plan& p, int batch, const SplitPlan& sp);
 // bytes of per-(sequence, KV head, query head) arrival counters at the front
 // of the decode workspace (they must be zero before a call; calls leave them zero)
 size_t decode_counter_bytes(const bgtq_plan& p, int batch);

@@ -126,6 +126,9 @@ SplitPlan decode_split(const bgtq_plan& p, int batch, int64_t max_len) {
     sp.tokens_per_split = (int)tps;
     sp.slack = (int)slack;
     sp.n_split = (int)((n + kCluster - 1) / kCluster * kCluster);
+    // n <= ns (ranges of tps cover len + slack in ns steps, and all are whole
+    // tiles), and ns never falls as len grows, which n may
+    sp.parts = (int)((ns + kCluster - 1) / kCluster);
     return sp;
 }
 
@@ -134,30 +137,38 @@ SplitPlan decode_split_bounded(const bgtq_plan& p, int batch, int64_t max_len) {
     const int64_t len = std::max<int64_t>(max_len, 1);
     int64_t slots = (p.bk >= 1 && p.bk <= 3 && p.bv >= 1 && p.bv <= 4)
                         ? resident_ctas_for(p.bk, p.bv, p.img_ws) : 0;
-    if (slots <= 0) slots = 2 * std::max(1, p.num_sms);
+    if (slots <= 0) slots = 2 * (p.num_sms > 0 ? p.num_sms : 152);  // (a host-only plan: GB300's)
     if (units * kCluster <= slots) return decode_split(p, batch, max_len);
     // A large batch: clusters of kCluster splits would take several waves of
     // CTAs, each with its set-up (about kFixed tokens' worth of time: 5 us
     // against 13 ns a token), so a unit is cut into as few splits as fill the
-    // GPU evenly: the split count of the shortest waves x (kFixed + tokens).
+    // GPU evenly: the split count ns of the least waves x (kFixed + len / ns).
+    // (Compared as fractions, so that a longer len never takes fewer splits:
+    // the larger of two counts has no fewer waves, so it can only win through
+    // its smaller share of len.)
     constexpr int64_t kFixed = 400;
     SplitPlan best;
-    int64_t best_cost = INT64_MAX;
+    int64_t best_waves = 0, best_ns = 0;
     for (int64_t ns = (len + kMaxSplitTokensBounded - 1) / kMaxSplitTokensBounded; ns <= kMaxClusters; ++ns) {
         const int64_t slack = ns > 1 ? std::min<int64_t>(256, (len + ns - 1) / ns / 4) / kTile * kTile : 0;
         int64_t tps = (len + slack + ns - 1) / ns;
         tps = std::max<int64_t>((tps + kTile - 1) / kTile * kTile, (int64_t)kWarps * kTile);
         if (tps > kMaxSplitTokensBounded) continue;
-        const int64_t cost = (units * ns + slots - 1) / slots * (kFixed + tps);
-        if (cost >= best_cost) continue;
-        best_cost = cost;
+        const int64_t waves = (units * ns + slots - 1) / slots;
+        if (best_ns > 0 && waves * (kFixed * ns + len) * best_ns >= best_waves * (kFixed * best_ns + len) * ns) continue;
+        best_waves = waves;
+        best_ns = ns;
         const int64_t a0 = std::max<int64_t>(0, (len - tps + slack + kTile - 1) / kTile * kTile);
         best.tokens_per_split = (int)tps;
         best.slack = (int)slack;
         best.n_split = (int)(1 + (a0 + tps - 1) / tps);
         best.cluster = 1;
+        best.parts = (int)ns;
     }
-    return best_cost == INT64_MAX ? decode_split(p, batch, max_len) : best;
+    if (best_ns > 0) return best;
+    best = decode_split(p, batch, max_len);  // (longer than kMaxClusters such splits)
+    best.parts = std::max(best.parts, kMaxClusters);
+    return best;
 }
 
 size_t decode_counter_bytes(const bgtq_plan& p, int batch) {
@@ -168,6 +179,10 @@ size_t decode_workspace_bytes(const bgtq_plan& p, int batch, const SplitPlan& sp
     const size_t units = (size_t)batch * p.H;
     const size_t counters = decode_counter_bytes(p, batch);
     return counters + units * (size_t)(sp.n_split / sp.cluster) * p.G * kPartStride * sizeof(float);
+}
+
+size_t decode_bounded_workspace_bytes(const bgtq_plan& p, int batch, const SplitPlan& sp) {
+    return decode_counter_bytes(p, batch) + (size_t)batch * p.H * (size_t)sp.parts * p.G * kPartStride * sizeof(float);
 }
 
 cudaError_t launch_decode(const bgtq_plan& pl, cudaStream_t s, const void* q, const bgtq_cache& c,

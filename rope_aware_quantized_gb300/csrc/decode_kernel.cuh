@@ -956,9 +956,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
                     if (tok >= wstart && tok < t_end) lg[nt][e] = s16[nt][e] * p.scale_log2;
                 }
         }
+        float rv[2][2] = {{tr.rv[0][0], tr.rv[0][1]}, {tr.rv[1][0], tr.rv[1][1]}};
         if constexpr (kMode == kDecodeWindow) {
             // positions between the sinks and the window: the rest of the
-            // sinks' last tile and the start of the window's first
+            // sinks' last tile and the start of the window's first (their
+            // value norms too: 0 times one that is not finite is not 0)
             const int r0 = real_pos(T0);
             if (r0 < win_lo && r0 + kTile > p.sinks) {
 #pragma unroll
@@ -966,7 +968,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const int r = r0 + 8 * nt + 2 * t + e;
-                        if (r >= p.sinks && r < win_lo) lg[nt][e] = -INFINITY;
+                        if (r >= p.sinks && r < win_lo) {
+                            lg[nt][e] = -INFINITY;
+                            rv[nt][e] = 0.0f;
+                        }
                     }
             }
         }
@@ -1012,8 +1017,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
         // P' = p * rho_V of head g for tokens 2t, 2t+1 (b0) and 8+2t, 9+2t
         // (b1): the B fragment of the P.V product, split hi + lo
         uint32_t pb[2][2];
-        split_hilo(pr[0][0] * tr.rv[0][0], pr[0][1] * tr.rv[0][1], pb[0][0], pb[1][0]);
-        split_hilo(pr[1][0] * tr.rv[1][0], pr[1][1] * tr.rv[1][1], pb[0][1], pb[1][1]);
+        split_hilo(pr[0][0] * rv[0][0], pr[0][1] * rv[0][1], pb[0][0], pb[1][0]);
+        split_hilo(pr[1][0] * rv[1][0], pr[1][1] * rv[1][1], pb[0][1], pb[1][1]);
         pv_mtile<BV, 0>(acc, pb, tr.vw, vbase, s_tab);
         pv_mtile<BV, 1>(acc, pb, tr.vw, vbase, s_tab);
         pv_mtile<BV, 2>(acc, pb, tr.vw, vbase, s_tab);

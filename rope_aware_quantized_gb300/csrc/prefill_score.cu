@@ -79,7 +79,7 @@ enum {
 
 struct PsParams {
     const float* lse;  // [B][H*G][T]
-    float* out;        // [B][H][stride] or, parts > 1, [B][H][parts][T]
+    float* out;        // [B][H][stride], or [B][H][parts][T] for the join
     int64_t stride;
     int T, H, G, row0, sinks, window;
     int box;           // rows of a query head in a tile: all of them, or fewer with several heads in it
@@ -95,12 +95,13 @@ __device__ __forceinline__ float row_lse(const PsParams& p, const float* lse_row
     return counts && row < p.T ? __ldg(lse_row + row) : -INFINITY;
 }
 // The ninth step's row side: -lse / scale as 256 a + b + c / 256 with fp16 a,
-// b, c (33 bits, for |lse / scale| up to 1.6e7; the quotient as the product
-// with 1 / scale and its rounding error); a = -inf (a weight of 0) for a row
-// that does not count or saw nothing.
+// b, c (33 bits; the quotient as the product with 1 / scale and its rounding
+// error); a = -inf (a weight of 0) for a row that does not count or saw
+// nothing, NaN where |lse / scale| is past the range of a.
 __device__ __forceinline__ uint4 row_ext(const PsParams& p, float x) {
     if (!(fabsf(x) < INFINITY)) return make_uint4(x == x ? 0xFC00u : 0x7E00u, 0u, 0u, 0u);  // (a NaN stays one)
     const float n = -x * p.unit_hi, e = fmaf(-x, p.unit_lo, fmaf(-x, p.unit_hi, -n));
+    if (fabsf(n) > 256.0f * 65504.0f) return make_uint4(0x7E00u, 0u, 0u, 0u);
     const __half a = __float2half_rn(n * (1.0f / 256.0f));
     const float r1 = fmaf(-256.0f, __half2float(a), n);  // exact
     const __half b = __float2half_rn(r1);

@@ -213,3 +213,26 @@ def test_binding_checks_tensors():
         bg.bgtq_decode_window_attn(p, q, None, None, 10, 0, 4, q, q)
     with pytest.raises(ValueError, match="contiguous"):
         bg.bgtq_prefill_score(p, q.view(1, H * G, 1, 128).expand(1, H * G, 4, 128), q, q, q)
+
+
+@pytest.mark.parametrize("batch", [1, 3, 13, 37])
+def test_a_workspace_serves_every_shorter_length(batch):
+    p = plan()
+    for size in (lambda n: bg.bgtq_decode_window_workspace(p, batch, n, 20, 5000),
+                 lambda n: bg.bgtq_decode_window_workspace(p, batch, 1 << 20, 20, n),
+                 lambda n: bg.bgtq_decode_window_workspace(p, batch, n, 0, 1 << 40),
+                 lambda n: bg.bgtq_decode_score_workspace(p, batch, n)):
+        last = 0
+        for n in [*range(1, 20000, 61), *range(20000, 700000, 4001)]:
+            assert size(n) >= last, n
+            last = size(n)
+    most, far = 2 ** 31 - 1, 2 ** 63 - 1  # (no sequence is longer)
+    assert bg.bgtq_decode_window_workspace(p, batch, far, far, far) == bg.bgtq_decode_window_workspace(p, batch, most, far, far)
+    assert bg.bgtq_decode_score_workspace(p, batch, far) == bg.bgtq_decode_score_workspace(p, batch, most)
+
+
+def test_prompt_scores_refuse_scales_whose_log_sum_exp_does_not_fit():
+    rc, msg = pscore(scale=9e-7)
+    assert rc == -2 and "1e-6" in msg
+    rc, msg = pscore(scale=1e-6)
+    assert rc == -1 and "host-only" in msg

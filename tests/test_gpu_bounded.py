@@ -696,3 +696,79 @@ def test_evicted_lengths_go_straight_into_decode():
         bg.bgtq_decode_score_attn(L.plan, q, dst, lens, keep, ds, ds, out[3], ws2)
         torch.cuda.synchronize()
         assert torch.equal(out[0], out[2]) and torch.equal(out[1], out[3])
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_norms_that_are_not_finite_stay_out_of_the_windows_last_tiles(page):
+    """Records next to the sinks and next to the window, in the tiles that hold both kinds, with norms of NaN and infinity."""
+    L = Layer(33, 2, 4, 384, 3, [300])
+    cache = L.cache(304, page)
+    L.fill(cache)
+    want = window_call(L, cache, 5, 50)
+    table = cache.page_table[0].tolist() if page else None
+    for pos in (5, 9, 15, 240, 249):  # (the window starts at 250, its tile at 240)
+        for h in range(2):
+            at = (table[pos // page] * 2 + h) * page + pos % page if page else h * 304 + pos
+            cache.k_norm[at] = float("nan")
+            cache.v_norm[at] = float("inf") if pos & 1 else float("nan")
+    got = window_call(L, cache, 5, 50)
+    torch.cuda.synchronize()
+    assert torch.isfinite(got).all() and torch.equal(got, want)
+    assert torch.isnan(window_call(L, cache, 6, 50)).any()  # (position 5 seen)
+
+
+@pytest.mark.parametrize("row0", [0, 290])
+def test_prompt_scores_of_a_log_sum_exp_out_of_range(row0):
+    L = Layer(34, 1, 2, 384, 3, [300])
+    q, k, _ = prompt(L)
+    lse = torch.full((1, 2, 300), 1.4e6, device="cuda")  # 1.58e7 / 128^-0.5: weights of 0
+    n = bg.bgtq_prefill_score_workspace(L.plan, 1, 300, row0)
+    for bad in (None, 2e6, -2e6):
+        scores = torch.full((1, 1, 300), GARBAGE, device="cuda")
+        if bad is not None:
+            lse[0, 1, 295] = bad
+        bg.bgtq_prefill_score(L.plan, dev(q), dev(k), lse, scores, zeros_ws(n), row0=row0)
+        torch.cuda.synchronize()
+        seen = scores[0, 0].cpu()
+        assert torch.isnan(seen[:296]).all() if bad else (seen[:296] == 0).all()
+        assert (seen[296:] == 0).all()
+
+
+def test_a_workspace_serves_every_shorter_length_on_this_gpu():
+    L = Layer(35, 2, 4, 384, 3, [400, 90, 7])
+    for batch in (1, 3, 20, 37, 160):
+        last = [0, 0]
+        for n in range(1, 40000, 53):
+            now = [bg.bgtq_decode_window_workspace(L.plan, batch, n, 0, 1 << 40), bg.bgtq_decode_score_workspace(L.plan, batch, n)]
+            assert now[0] >= last[0] and now[1] >= last[1], (batch, n)
+            last = now
+    # one workspace over calls of growing and shrinking lengths
+    cache = L.cache(400)
+    L.fill(cache)
+    ws = zeros_ws(bg.bgtq_decode_score_workspace(L.plan, 3, 400))
+    s = torch.zeros((3, 2, 400), device="cuda")
+    for n in (7, 400, 33, 129, 400, 1):
+        M = Layer.__new__(Layer)
+        M.__dict__.update(L.__dict__, lens=[min(n, x) for x in L.lens])
+        out = score_call(M, cache, s, s, ws=ws)
+        win = window_call(M, cache, 4, 60, ws=ws)
+        torch.cuda.synchronize()
+        check_decode_out(M, out.double().cpu().numpy(), np.arange, False)
+        check_decode_out(M, win.double().cpu().numpy(), lambda x: O.decode_visible(x, 4, 60), False)
+
+
+def test_tensors_of_the_host_are_refused():
+    L = Layer(36, 1, 2, 384, 3, [20])
+    cache = L.cache(20)
+    L.fill(cache)
+    host = torch.zeros(1 << 16, dtype=torch.uint8)
+    with pytest.raises(ValueError, match="workspace"):
+        window_call(L, cache, 4, 8, ws=host)
+    with pytest.raises(ValueError, match="status"):
+        window_call(L, cache, 4, 8, status=torch.zeros(1, dtype=torch.int32))
+    s = torch.zeros((1, 1, 20), device="cuda")
+    with pytest.raises(ValueError, match="workspace"):
+        score_call(L, cache, s, s, ws=host)
+    with pytest.raises(ValueError, match="scores_out must be a CUDA"):
+        score_call(L, cache, s, s.cpu())
+    torch.cuda.synchronize()
