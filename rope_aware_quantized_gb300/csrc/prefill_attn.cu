@@ -59,7 +59,12 @@ constexpr int kTcKeys = 128;                      // keys per tile
 constexpr int kTcThreads = 384;                   // two softmax warpgroups, the MMA warp, the TMA warp, 2 encoder warps
 constexpr int kEncWarps = 2;                      // warps that encode records alongside the attention
 constexpr int kEncWarp0 = 10;
-constexpr int kWinThreads = kEncWarp0 * 32;       // the windowed instance has no encoder warps
+// The windowed instance has no encoder warps: its last four warps give their
+// registers to the softmax warps (a row's 128 logits and their packed
+// probabilities spill at 168 registers a thread: 855 us against 830 for 32768
+// rows under a window of 4096).  More than the block was launched with would
+// be waited for without end: the launcher checks the sum.
+constexpr int kWinSoftmaxRegs = 184, kWinOtherRegs = 128;
 constexpr uint32_t kTcTile = kTcRows * kD * 2;    // one 128 x 128 fp16 tile: 32 KB
 constexpr uint32_t kTcBox = kTcTile / 2;          // one 64-column box of it (128 rows x 128 B)
 constexpr uint32_t kOffQ = 0;                     // Q_g at + g kTcTile
@@ -273,7 +278,7 @@ __device__ __forceinline__ void softmax_rows(const PfParams& p, uint32_t tmem, i
 }
 
 template <bool kWin>
-__global__ void __launch_bounds__(kWin ? kWinThreads : kTcThreads, 1)
+__global__ void __launch_bounds__(kTcThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                    const __grid_constant__ CUtensorMap tv, PfParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -318,173 +323,177 @@ __global__ void __launch_bounds__(kWin ? kWinThreads : kTcThreads, 1)
     // may still read or write is touched before this)
     if constexpr (kWin) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-    if (warp == 9) {
-        // ---- TMA: Q of the CTA's heads, then K and V tiles through two stages
-        if (lane == 0) {
-            int used[2] = {0, 0};
-            const int qrow = ((b * p.H * p.G) + hq0) * p.T + q0;
-            mbar_expect_tx(BAR(kBarQ), ng * kTcTile);
-            for (int g = 0; g < ng; ++g)
-                for (int x = 0; x < 2; ++x)
-                    tma_load_2d(sbase + kOffQ + g * kTcTile + x * kTcBox, &tq, 64 * x, qrow + g * p.T, BAR(kBarQ));
-            const int krow = (b * p.H + h) * p.T;
-            auto load_tile = [&](uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
-                if constexpr (kWin)
-                    tma_load_3d(dst, map, x, row, b * p.H + h, bar);
-                else
-                    tma_load_2d(dst, map, x, krow + row, bar);
-            };
-            for (int j = 0; j < nkt; ++j) {
-                const int s = j & 1;
-                const uint32_t par = (uint32_t)((j >> 1) - 1) & 1u;
-                if (j >= 2 && !mbar_wait(BAR(kBarKEmpty + s), par, abort_flag, p.status)) break;
-                mbar_expect_tx(BAR(kBarKFull + s), kTcTile);
-                for (int x = 0; x < 2; ++x)
-                    load_tile(sbase + kOffK + s * kTcTile + x * kTcBox, &tk, 64 * x, kt.tile(j) * kTcKeys, BAR(kBarKFull + s));
-                if (j >= 2 && !mbar_wait(BAR(kBarVEmpty + s), par, abort_flag, p.status)) {
-                    used[s] = 2 * j + 1;  // K of tile j in flight, V not
-                    break;
+    if (warp >= 8) {
+        if constexpr (kWin) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWinOtherRegs));
+        if (warp == 9) {
+            // ---- TMA: Q of the CTA's heads, then K and V tiles through two stages
+            if (lane == 0) {
+                int used[2] = {0, 0};
+                const int qrow = ((b * p.H * p.G) + hq0) * p.T + q0;
+                mbar_expect_tx(BAR(kBarQ), ng * kTcTile);
+                for (int g = 0; g < ng; ++g)
+                    for (int x = 0; x < 2; ++x)
+                        tma_load_2d(sbase + kOffQ + g * kTcTile + x * kTcBox, &tq, 64 * x, qrow + g * p.T, BAR(kBarQ));
+                const int krow = (b * p.H + h) * p.T;
+                auto load_tile = [&](uint32_t dst, const CUtensorMap* map, int x, int row, uint32_t bar) {
+                    if constexpr (kWin)
+                        tma_load_3d(dst, map, x, row, b * p.H + h, bar);
+                    else
+                        tma_load_2d(dst, map, x, krow + row, bar);
+                };
+                for (int j = 0; j < nkt; ++j) {
+                    const int s = j & 1;
+                    const uint32_t par = (uint32_t)((j >> 1) - 1) & 1u;
+                    if (j >= 2 && !mbar_wait(BAR(kBarKEmpty + s), par, abort_flag, p.status)) break;
+                    mbar_expect_tx(BAR(kBarKFull + s), kTcTile);
+                    for (int x = 0; x < 2; ++x)
+                        load_tile(sbase + kOffK + s * kTcTile + x * kTcBox, &tk, 64 * x, kt.tile(j) * kTcKeys, BAR(kBarKFull + s));
+                    if (j >= 2 && !mbar_wait(BAR(kBarVEmpty + s), par, abort_flag, p.status)) {
+                        used[s] = 2 * j + 1;  // K of tile j in flight, V not
+                        break;
+                    }
+                    mbar_expect_tx(BAR(kBarVFull + s), kTcTile);
+                    for (int x = 0; x < 2; ++x)
+                        load_tile(sbase + kOffV + s * kTcTile + x * kTcBox, &tv, 64 * x, kt.tile(j) * kTcKeys, BAR(kBarVFull + s));
+                    used[s] = 2 * j + 2;
                 }
-                mbar_expect_tx(BAR(kBarVFull + s), kTcTile);
-                for (int x = 0; x < 2; ++x)
-                    load_tile(sbase + kOffV + s * kTcTile + x * kTcBox, &tv, 64 * x, kt.tile(j) * kTcKeys, BAR(kBarVFull + s));
-                used[s] = 2 * j + 2;
-            }
-            // every copy issued has landed before the CTA ends (normally at
-            // once: the MMA thread waited for them)
-            mbar_wait(BAR(kBarQ), 0, abort_flag, p.status, false);
-            for (int s = 0; s < 2; ++s) {
-                if (used[s] == 0) continue;
-                const int jl = (used[s] - 1) >> 1;  // last tile on this stage
-                const uint32_t par = (uint32_t)(jl >> 1) & 1u;
-                mbar_wait(BAR(kBarKFull + s), par, abort_flag, p.status, false);
-                if (used[s] & 1) {  // its V was not issued: the previous use's V
-                    if (jl >= 2) mbar_wait(BAR(kBarVFull + s), par ^ 1u, abort_flag, p.status, false);
-                } else {
-                    mbar_wait(BAR(kBarVFull + s), par, abort_flag, p.status, false);
-                }
-            }
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // ---- MMA issue
-        constexpr uint32_t idS = instr_desc(kTcRows, kTcKeys, 0);
-        constexpr uint32_t idO = instr_desc(kTcRows, kD, 1);
-        if constexpr (kWin) {
-            // the whole warp runs the loop, an elected lane issues
-            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-            auto wait = [&](int bar, uint32_t parity) -> bool {
-                return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity & 1u, abort_flag, p.status));
-            };
-            auto issue_s = [&](int g, int j) {
-                const uint32_t qa = sbase + kOffQ + g * kTcTile, ka = sbase + kOffK + (j & 1) * kTcTile;
-#pragma unroll
-                for (int k = 0; k < kD / 16; ++k) {
-                    const uint32_t off = (uint32_t)(k >> 2) * kTcBox + (uint32_t)(k & 3) * 32;
-                    mma_ss_warp(tm + 128u * g, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), idS, k > 0);
-                }
-                mma_commit_warp(BAR(kBarS + g));
-            };
-            auto issue_pv = [&](int g, int j) {
-                const uint32_t va = sbase + kOffV + (j & 1) * kTcTile;
-#pragma unroll
-                for (int k = 0; k < kTcKeys / 16; ++k)
-                    mma_ts_warp(tm + 256u + 128u * g, tm + 128u * g + 8u * k, smem_desc(va + 2048u * k, kTcBox, 1024), idO,
-                                (j > 0 || k > 0) ? 1u : 0u);
-            };
-            bool ok = wait(kBarQ, 0) && wait(kBarKFull, 0);
-            if (ok) {
-                tc_fence_after();
-                for (int g = 0; g < ng; ++g) issue_s(g, 0);
-                mma_commit_warp(BAR(kBarKEmpty));
-            }
-            for (int j = 0; ok && j < nkt; ++j) {
-                const int s = j & 1;
-                const bool next = j + 1 < nkt;
-                // (the tiles first: their waits pass while the softmax runs)
-                ok = wait(kBarVFull + s, (uint32_t)(j >> 1)) && (!next || wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)));
-                for (int g = 0; g < ng && ok; ++g) {
-                    ok = wait(kBarP + g, (uint32_t)j);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(g, j);
-                    if (next) {
-                        issue_s(g, j + 1);
+                // every copy issued has landed before the CTA ends (normally at
+                // once: the MMA thread waited for them)
+                mbar_wait(BAR(kBarQ), 0, abort_flag, p.status, false);
+                for (int s = 0; s < 2; ++s) {
+                    if (used[s] == 0) continue;
+                    const int jl = (used[s] - 1) >> 1;  // last tile on this stage
+                    const uint32_t par = (uint32_t)(jl >> 1) & 1u;
+                    mbar_wait(BAR(kBarKFull + s), par, abort_flag, p.status, false);
+                    if (used[s] & 1) {  // its V was not issued: the previous use's V
+                        if (jl >= 2) mbar_wait(BAR(kBarVFull + s), par ^ 1u, abort_flag, p.status, false);
                     } else {
-                        mma_commit_warp(BAR(kBarO + g));
+                        mbar_wait(BAR(kBarVFull + s), par, abort_flag, p.status, false);
                     }
                 }
-                if (!ok) break;
-                mma_commit_warp(BAR(kBarVEmpty + s));
-                if (next) mma_commit_warp(BAR(kBarKEmpty + (s ^ 1)));
             }
-            // every MMA issued has completed before the CTA ends
-            mma_commit_warp(BAR(kBarDrain));
-            mbar_wait(BAR(kBarDrain), 0, abort_flag, p.status, false);
-        } else if (lane == 0) {
-            auto issue_s = [&](int g, int j) {
-                const uint32_t qa = sbase + kOffQ + g * kTcTile, ka = sbase + kOffK + (j & 1) * kTcTile;
+            __syncwarp();
+        } else if (warp == 8) {
+            // ---- MMA issue
+            constexpr uint32_t idS = instr_desc(kTcRows, kTcKeys, 0);
+            constexpr uint32_t idO = instr_desc(kTcRows, kD, 1);
+            if constexpr (kWin) {
+                // the whole warp runs the loop, an elected lane issues
+                const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+                auto wait = [&](int bar, uint32_t parity) -> bool {
+                    return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity & 1u, abort_flag, p.status));
+                };
+                auto issue_s = [&](int g, int j) {
+                    const uint32_t qa = sbase + kOffQ + g * kTcTile, ka = sbase + kOffK + (j & 1) * kTcTile;
 #pragma unroll
-                for (int k = 0; k < kD / 16; ++k) {
-                    const uint32_t off = (uint32_t)(k >> 2) * kTcBox + (uint32_t)(k & 3) * 32;
-                    mma_ss(tmem + 128u * g, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), idS, k > 0);
-                }
-                mma_commit(BAR(kBarS + g));
-            };
-            auto issue_pv = [&](int g, int j) {
-                const uint32_t va = sbase + kOffV + (j & 1) * kTcTile;
-#pragma unroll
-                for (int k = 0; k < kTcKeys / 16; ++k)
-                    mma_ts(tmem + 256u + 128u * g, tmem + 128u * g + 8u * k, smem_desc(va + 2048u * k, kTcBox, 1024), idO,
-                           (j > 0 || k > 0) ? 1u : 0u);
-            };
-            bool ok = mbar_wait(BAR(kBarQ), 0, abort_flag, p.status) && mbar_wait(BAR(kBarKFull), 0, abort_flag, p.status);
-            if (ok) {
-                tc_fence_after();
-                for (int g = 0; g < ng; ++g) issue_s(g, 0);
-                mma_commit(BAR(kBarKEmpty));
-            }
-            for (int j = 0; ok && j < nkt; ++j) {
-                const int s = j & 1;
-                const bool next = j + 1 < nkt;
-                if (!mbar_wait(BAR(kBarVFull + s), (uint32_t)(j >> 1) & 1u, abort_flag, p.status)) break;
-                for (int g = 0; g < ng && ok; ++g) {
-                    ok = mbar_wait(BAR(kBarP + g), (uint32_t)j & 1u, abort_flag, p.status);
-                    if (ok && next && g == 0)
-                        ok = mbar_wait(BAR(kBarKFull + (s ^ 1)), (uint32_t)((j + 1) >> 1) & 1u, abort_flag, p.status);
-                    if (!ok) break;
-                    tc_fence_after();
-                    issue_pv(g, j);
-                    if (next) {
-                        issue_s(g, j + 1);
-                    } else {
-                        mma_commit(BAR(kBarO + g));
+                    for (int k = 0; k < kD / 16; ++k) {
+                        const uint32_t off = (uint32_t)(k >> 2) * kTcBox + (uint32_t)(k & 3) * 32;
+                        mma_ss_warp(tm + 128u * g, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), idS, k > 0);
                     }
+                    mma_commit_warp(BAR(kBarS + g));
+                };
+                auto issue_pv = [&](int g, int j) {
+                    const uint32_t va = sbase + kOffV + (j & 1) * kTcTile;
+#pragma unroll
+                    for (int k = 0; k < kTcKeys / 16; ++k)
+                        mma_ts_warp(tm + 256u + 128u * g, tm + 128u * g + 8u * k, smem_desc(va + 2048u * k, kTcBox, 1024), idO,
+                                    (j > 0 || k > 0) ? 1u : 0u);
+                };
+                bool ok = wait(kBarQ, 0) && wait(kBarKFull, 0);
+                if (ok) {
+                    tc_fence_after();
+                    for (int g = 0; g < ng; ++g) issue_s(g, 0);
+                    mma_commit_warp(BAR(kBarKEmpty));
                 }
-                if (!ok) break;
-                mma_commit(BAR(kBarVEmpty + s));
-                if (next) mma_commit(BAR(kBarKEmpty + (s ^ 1)));
+                for (int j = 0; ok && j < nkt; ++j) {
+                    const int s = j & 1;
+                    const bool next = j + 1 < nkt;
+                    // (the tiles first: their waits pass while the softmax runs)
+                    ok = wait(kBarVFull + s, (uint32_t)(j >> 1)) && (!next || wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)));
+                    for (int g = 0; g < ng && ok; ++g) {
+                        ok = wait(kBarP + g, (uint32_t)j);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(g, j);
+                        if (next) {
+                            issue_s(g, j + 1);
+                        } else {
+                            mma_commit_warp(BAR(kBarO + g));
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit_warp(BAR(kBarVEmpty + s));
+                    if (next) mma_commit_warp(BAR(kBarKEmpty + (s ^ 1)));
+                }
+                // every MMA issued has completed before the CTA ends
+                mma_commit_warp(BAR(kBarDrain));
+                mbar_wait(BAR(kBarDrain), 0, abort_flag, p.status, false);
+            } else if (lane == 0) {
+                auto issue_s = [&](int g, int j) {
+                    const uint32_t qa = sbase + kOffQ + g * kTcTile, ka = sbase + kOffK + (j & 1) * kTcTile;
+#pragma unroll
+                    for (int k = 0; k < kD / 16; ++k) {
+                        const uint32_t off = (uint32_t)(k >> 2) * kTcBox + (uint32_t)(k & 3) * 32;
+                        mma_ss(tmem + 128u * g, smem_desc(qa + off, 16, 1024), smem_desc(ka + off, 16, 1024), idS, k > 0);
+                    }
+                    mma_commit(BAR(kBarS + g));
+                };
+                auto issue_pv = [&](int g, int j) {
+                    const uint32_t va = sbase + kOffV + (j & 1) * kTcTile;
+#pragma unroll
+                    for (int k = 0; k < kTcKeys / 16; ++k)
+                        mma_ts(tmem + 256u + 128u * g, tmem + 128u * g + 8u * k, smem_desc(va + 2048u * k, kTcBox, 1024), idO,
+                               (j > 0 || k > 0) ? 1u : 0u);
+                };
+                bool ok = mbar_wait(BAR(kBarQ), 0, abort_flag, p.status) && mbar_wait(BAR(kBarKFull), 0, abort_flag, p.status);
+                if (ok) {
+                    tc_fence_after();
+                    for (int g = 0; g < ng; ++g) issue_s(g, 0);
+                    mma_commit(BAR(kBarKEmpty));
+                }
+                for (int j = 0; ok && j < nkt; ++j) {
+                    const int s = j & 1;
+                    const bool next = j + 1 < nkt;
+                    if (!mbar_wait(BAR(kBarVFull + s), (uint32_t)(j >> 1) & 1u, abort_flag, p.status)) break;
+                    for (int g = 0; g < ng && ok; ++g) {
+                        ok = mbar_wait(BAR(kBarP + g), (uint32_t)j & 1u, abort_flag, p.status);
+                        if (ok && next && g == 0)
+                            ok = mbar_wait(BAR(kBarKFull + (s ^ 1)), (uint32_t)((j + 1) >> 1) & 1u, abort_flag, p.status);
+                        if (!ok) break;
+                        tc_fence_after();
+                        issue_pv(g, j);
+                        if (next) {
+                            issue_s(g, j + 1);
+                        } else {
+                            mma_commit(BAR(kBarO + g));
+                        }
+                    }
+                    if (!ok) break;
+                    mma_commit(BAR(kBarVEmpty + s));
+                    if (next) mma_commit(BAR(kBarKEmpty + (s ^ 1)));
+                }
+                // every MMA issued has completed before the CTA ends
+                mma_commit(BAR(kBarDrain));
+                mbar_wait(BAR(kBarDrain), 0, abort_flag, p.status, false);
             }
-            // every MMA issued has completed before the CTA ends
-            mma_commit(BAR(kBarDrain));
-            mbar_wait(BAR(kBarDrain), 0, abort_flag, p.status, false);
-        }
-        __syncwarp();
-    } else if (!kWin && warp >= kEncWarp0) {
-        // ---- record encoder: the block's 128 positions are shared out over
-        // the CTAs of the KV head's query-head pairs (an even share each, so a
-        // V pair record is never split); encoded while the others attend
-        const int n = min(kTcRows, p.T - q0);
-        const int share = ((n + npair - 1) / npair + 1) & ~1;
-        const int e0 = pair * share, e1 = min(n, e0 + share);
-        if (e0 < e1) {
-            const int ew = warp - kEncWarp0;
-            stage_thresholds(s_thr, p.thr, tid - kEncWarp0 * 32, kEncWarps * 32);
-            asm volatile("bar.sync 1, %0;" ::"n"(kEncWarps * 32) : "memory");
-            encode_block(p, b, h, q0 + e0, e1 - e0, 0, p.T, s_thr, s_rec[ew], s_vmask[ew], ew, lane, kEncWarps);
+            __syncwarp();
+        } else if (!kWin && warp >= kEncWarp0) {
+            // ---- record encoder: the block's 128 positions are shared out over
+            // the CTAs of the KV head's query-head pairs (an even share each, so a
+            // V pair record is never split); encoded while the others attend
+            const int n = min(kTcRows, p.T - q0);
+            const int share = ((n + npair - 1) / npair + 1) & ~1;
+            const int e0 = pair * share, e1 = min(n, e0 + share);
+            if (e0 < e1) {
+                const int ew = warp - kEncWarp0;
+                stage_thresholds(s_thr, p.thr, tid - kEncWarp0 * 32, kEncWarps * 32);
+                asm volatile("bar.sync 1, %0;" ::"n"(kEncWarps * 32) : "memory");
+                encode_block(p, b, h, q0 + e0, e1 - e0, 0, p.T, s_thr, s_rec[ew], s_vmask[ew], ew, lane, kEncWarps);
+            }
         }
     } else {
         // ---- softmax warpgroups
+        if constexpr (kWin) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kWinSoftmaxRegs));
         const int g = warp >> 2;
         if (g < ng)
             softmax_rows<kWin>(p, tmem, g, b, hq0 + g, q0, kt, BAR(kBarS + g), BAR(kBarP + g), BAR(kBarO + g), abort_flag, warp,
@@ -523,7 +532,10 @@ cudaError_t launch_prefill(const bgtq_plan& pl, cudaStream_t s, const void* q, c
                 cudaFuncSetAttribute(prefill_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
             if (e == cudaSuccess)
                 e = cudaFuncSetAttribute(prefill_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
+            cudaFuncAttributes fa;
+            if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, prefill_kernel<true>);
             if (e != cudaSuccess) return e;
+            if (2 * kWinSoftmaxRegs + kWinOtherRegs > 3 * fa.numRegs) return cudaErrorInvalidConfiguration;
             done[dev] = true;
         }
     }
@@ -568,7 +580,7 @@ cudaError_t launch_prefill(const bgtq_plan& pl, cudaStream_t s, const void* q, c
         attr.val.programmaticStreamSerializationAllowed = 1;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = grid;
-        cfg.blockDim = dim3(kWinThreads, 1, 1);
+        cfg.blockDim = dim3(kTcThreads, 1, 1);
         cfg.dynamicSmemBytes = kTcSmem;
         cfg.stream = s;
         cfg.attrs = &attr;
