@@ -38,6 +38,11 @@
 // own key there, so the running maximum is finite before a tile that a row
 // sees nothing of.  Only the diagonal tile, those at the window's low edge and
 // those at the sinks' end are masked.  It also gives each row's log-sum-exp.
+// 32768 rows x 16 query heads under a window of 4096: 830 us with the append
+// (31 us), 1.24 PFLOP/s of the visible pairs' products; a tile's softmax (1690
+// clocks a head) and its own head's MMAs (1100) take turns.  Tried and slower:
+// P handed over in halves (850 us), chunks of 64 keys with two buffers of S
+// per head (925), two threads a row (1466).
 // Every wait is bounded: after kWaitNs it sets BGTQ_STATUS_TIMEOUT, the CTA
 // skips the rest of its work, lets its copies and MMAs land and frees its
 // tensor memory.
