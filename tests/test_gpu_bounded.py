@@ -772,3 +772,90 @@ def test_tensors_of_the_host_are_refused():
     with pytest.raises(ValueError, match="scores_out must be a CUDA"):
         score_call(L, cache, s, s.cpu())
     torch.cuda.synchronize()
+
+
+def test_prefill_window_into_a_paged_cache_with_a_recent_key_buffer():
+    T = 300
+    L = Layer(37, 2, 3, 384, 3, [T, T])
+    q, k, v = prompt(L)
+    pair = []
+    for call in (lambda c, o, st: bg.bgtq_prefill_window_attn(L.plan, dev(q), dev(k), dev(v), c, 0, T, o, status=st),
+                 lambda c, o, st: bg.bgtq_prefill_attn(L.plan, dev(q), dev(k), dev(v), c, o, status=st)):
+        c, o, st = L.cache(304, page=16, recent=20), torch.empty(q.shape, device="cuda"), lens32([0])
+        c.page_table[1, 3] = -1  # (its records are nowhere)
+        call(c, o, st)
+        torch.cuda.synchronize()
+        assert int(st.item()) == bg.STATUS_PAGE_RANGE
+        pair.append((c, o))
+    (a, oa), (b, ob) = pair
+    for n in ("k_codes", "v_codes", "k_norm", "v_norm", "k_recent"):
+        assert torch.equal(getattr(a, n), getattr(b, n)), n
+    # fp16 probabilities on both sides: 2^-11 sum w |v| each, at most 2^-10 max |v|; as much again for the sums
+    assert (oa - ob).abs().max().item() < 2.0 ** -9 * np.abs(v.astype(np.float32)).max()
+
+
+def test_prompt_calls_captured_and_on_two_streams():
+    """Prefill, scores and the cut of a layer in one graph, replayed on new inputs; the scores of two layers at once."""
+    T, keep = 700, 90
+    layers = [Layer(38 + i, 2, 4, 384, 3, [T]) for i in range(2)]
+    P = [prompt(L) for L in layers]
+    plan = layers[0].plan
+    n = bg.bgtq_prefill_score_workspace(plan, 1, T, 0)
+    assert n > 0
+
+    class Run:
+        def __init__(self, L):
+            self.q, self.k, self.v = (torch.zeros(x.shape, dtype=torch.float16, device="cuda") for x in P[0])
+            self.full, self.cut = bg.Cache(plan, 1, T), bg.Cache(plan, 1, keep)
+            self.out = torch.empty(self.q.shape, dtype=torch.float16, device="cuda")
+            self.lse = torch.empty(self.q.shape[:3], device="cuda")
+            self.scores, self.kept_scores = torch.empty((1, 2, T), device="cuda"), torch.empty((1, 2, keep), device="cuda")
+            self.kept, self.lens = torch.empty((1, 2, keep), dtype=torch.int32, device="cuda"), lens32([0])
+            self.src, self.ws = lens32([T]), zeros_ws(n)
+            self.feed(L)
+
+        def feed(self, i):
+            for x, y in zip((self.q, self.k, self.v), P[i]):
+                x.copy_(dev(y))
+
+        def go(self):
+            bg.bgtq_prefill_window_attn(plan, self.q, self.k, self.v, self.full, 3, 200, self.out, lse=self.lse)
+            bg.bgtq_prefill_score(plan, self.q, self.k, self.lse, self.scores, self.ws, sinks=3, window=200)
+            bg.bgtq_evict(plan, self.full, self.scores, self.src, T, keep, 3, 20, self.cut, self.kept_scores, self.lens, self.kept)
+
+        def results(self):
+            return [x.clone() for x in (self.out, self.lse, self.scores, self.kept_scores, self.kept, self.lens,
+                                        self.cut.k_codes, self.cut.v_codes, self.cut.k_norm, self.cut.v_norm)]
+
+    def equal(a, b):
+        return all(torch.equal(x, y) for x, y in zip(a, b))
+
+    want = []
+    for i in range(2):
+        r = Run(i)
+        torch.cuda.synchronize()
+        r.go()
+        torch.cuda.synchronize()
+        want.append(r.results())
+    assert not equal(*want)
+    # one graph, captured on another stream
+    r, side, g = Run(0), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        r.go()
+    for i in (0, 1, 0):
+        r.feed(i)
+        for x in (r.scores, r.kept_scores, r.out, r.lse):
+            x.fill_(GARBAGE)
+        g.replay()
+        torch.cuda.synchronize()
+        assert equal(r.results(), want[i])
+    # two layers at once
+    runs, streams = [Run(0), Run(1)], [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for x, s in zip(runs, streams):
+            with torch.cuda.stream(s):
+                x.go()
+    torch.cuda.synchronize()
+    assert equal(runs[0].results(), want[0]) and equal(runs[1].results(), want[1])
