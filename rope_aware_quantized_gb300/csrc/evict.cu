@@ -67,7 +67,8 @@ struct EvictParams {
     int32_t* status;
 };
 
-// Length of sequence b, cut to what the cache and the call allow.
+// Length of sequence b, cut to what the cache and the call allow (read by the
+// selection alone, after its wait).
 __device__ __forceinline__ int evict_len(const EvictParams& p, int b, bool report) {
     const int n = p.seq_lens[b];
     const int64_t lim = min(p.cap, p.max_len);
@@ -288,10 +289,14 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
     const int h = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const size_t unit = (size_t)b * p.H + h;
     if (tid < 8 * BV) s_even[tid] = even_fields<BV>(tid);
-    const int m = min(evict_len(p, b, false), p.keep);
+    evict_pdl_wait();
+    // The kept count is the one that the selection wrote, read after the wait:
+    // seq_lens may come from a kernel that is still running when this one
+    // starts, and another count than the selection's would take the -1 past
+    // the kept positions for positions.  (At most as many as `kept` holds.)
+    const int m = min(p.dst_lens[b], (int)min((int64_t)p.keep, min(p.cap, p.max_len)));
     const int d0 = blockIdx.x * kMoveTok;
     const int nt = min(kMoveTok, m - d0);
-    evict_pdl_wait();
     if (nt <= 0) return;
     for (int i = tid; i < nt; i += kMoveThreads) {
         const int pos = p.kept[unit * (size_t)p.keep + d0 + i];
