@@ -546,7 +546,10 @@ int bgtq_prefill_score(const bgtq_plan* plan, void* stream, const void* q_fp16, 
  *   dst_lens     device, [batch] int32: min(n, keep); may be the seq_lens of the
  *                next call on the stream
  *   kept         device, [batch][H][keep] int32: the source positions, -1
- *                past them
+ *                past them; the second launch reads it, so two calls that may
+ *                overlap on the GPU need two
+ * No buffer that is written (dst's, dst_scores, dst_lens, kept) may overlap
+ * another buffer of the call (INVALID_ARG; the page pools above excepted).
  * Two launches; every result is the same on every run.
  * Errors: INVALID_ARG, UNSUPPORTED (a recent-key buffer, more than 65535
  * sequences), CAPACITY, CUDA.  An unmapped page sets BGTQ_STATUS_PAGE_RANGE.

@@ -1043,6 +1043,19 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+// A buffer of an eviction.
+struct Span {
+    const void* at;
+    size_t bytes;
+    const char* name;
+};
+bool meet(const Span& a, const Span& b) {
+    return a.at && b.at && a.bytes > 0 && b.bytes > 0 && overlap(a.at, a.bytes, b.at, b.bytes);
+}
+int overlap_error(const Span& a, const Span& b) {
+    return set_error(BGTQ_ERR_INVALID_ARG, "%s overlaps %s", a.name, b.name);
+}
+
 }  // namespace
 
 extern "C" {
@@ -1229,10 +1242,35 @@ int bgtq_evict(const bgtq_plan* p, void* stream, const bgtq_cache* c, const floa
                       overlap(c->v_codes, ns * 16 * p->bv, dst->v_codes, nd * 16 * p->bv) ||
                       overlap(c->k_norm, ns * 4, dst->k_norm, nd * 4) || overlap(c->v_norm, ns * 4, dst->v_norm, nd * 4)))
         return set_error(BGTQ_ERR_INVALID_ARG, "the destination's records overlap the source's");
-    if (overlap(scores, units * (size_t)c->capacity * 4, dst_scores, units * (size_t)dst->capacity * 4) ||
-        overlap(seq_lens, (size_t)batch * 4, dst_lens, (size_t)batch * 4))
-        return set_error(BGTQ_ERR_INVALID_ARG, "dst_scores or dst_lens overlaps scores or seq_lens");
+    // nor may any other buffer that is written meet one that is read: the move
+    // reads the positions of `kept` while others of its blocks write
+    const size_t tables = (size_t)batch * 4;
+    const Span in[] = {{scores, units * (size_t)c->capacity * 4, "scores"},
+                       {seq_lens, (size_t)batch * 4, "seq_lens"},
+                       {c->page_table, c->page_table ? tables * (size_t)c->max_pages : 0, "the source's page table"},
+                       {dst->page_table, dst->page_table ? tables * (size_t)dst->max_pages : 0, "the destination's page table"},
+                       {c->k_codes, ns * 16 * p->bk, "the source's k_codes"},
+                       {c->v_codes, ns * 16 * p->bv, "the source's v_codes"},
+                       {c->k_norm, ns * 4, "the source's k_norm"},
+                       {c->v_norm, ns * 4, "the source's v_norm"}};
+    const Span written[] = {{dst_scores, units * (size_t)dst->capacity * 4, "dst_scores"},
+                            {dst_lens, (size_t)batch * 4, "dst_lens"},
+                            {kept, units * (size_t)keep * 4, "kept"},
+                            {dst->k_codes, nd * 16 * p->bk, "the destination's k_codes"},
+                            {dst->v_codes, nd * 16 * p->bv, "the destination's v_codes"},
+                            {dst->k_norm, nd * 4, "the destination's k_norm"},
+                            {dst->v_norm, nd * 4, "the destination's v_norm"}};
+    constexpr int kIn = sizeof(in) / sizeof(in[0]), kWritten = sizeof(written) / sizeof(written[0]), kRecords = 4;
+    for (int i = 0; i < kWritten - kRecords; ++i)
+        for (int j = 0; j < kIn; ++j)
+            if (meet(written[i], in[j])) return overlap_error(written[i], in[j]);
     if ((rc = check_plan_here(p))) return rc;
+    for (int i = 0; i < kWritten; ++i)
+        for (int j = 0; j < i; ++j)
+            if (meet(written[i], written[j])) return overlap_error(written[i], written[j]);
+    for (int i = kWritten - kRecords; i < kWritten; ++i)
+        for (int j = 0; j < (one_pool ? kIn - kRecords : kIn); ++j)
+            if (meet(written[i], in[j])) return overlap_error(written[i], in[j]);
     const cudaError_t e = launch_evict(*p, (cudaStream_t)stream, *c, scores, seq_lens, max_len, batch, (int)keep, (int)sinks,
                                        (int)recent, *dst, dst_scores, dst_lens, kept, status);
     if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "evict launch: %s", cudaGetErrorString(e));

@@ -299,10 +299,18 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p)
     const int nt = min(kMoveTok, m - d0);
     if (nt <= 0) return;
     for (int i = tid; i < nt; i += kMoveThreads) {
-        const int pos = p.kept[unit * (size_t)p.keep + d0 + i];
+        int pos = p.kept[unit * (size_t)p.keep + d0 + i];
+        int64_t dst = p.dmap.slot(b, h, d0 + i);
+        if (dst < 0 && p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
+        if (pos < 0 || pos >= min(p.cap, p.max_len)) {
+            // not the selection's: a call on another stream has written to
+            // this call's `kept` (nothing is read or moved by it)
+            if (p.status) atomicOr(p.status, BGTQ_STATUS_SEQLEN_CAPACITY);
+            pos = 0;
+            dst = -1;
+        }
         int64_t src = p.map.slot(b, h, pos);
-        const int64_t dst = p.dmap.slot(b, h, d0 + i);
-        if ((src < 0 || dst < 0) && p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
+        if (src < 0 && p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
         if (src < 0) src = (int64_t)h << p.map.lp | (pos & ((1 << p.map.lp) - 1));  // an unmapped page: page 0 is read
         s_src[i] = src;
         s_dst[i] = dst;
