@@ -463,9 +463,10 @@ int bgtq_decode_score_workspace(const bgtq_plan* plan, int batch, int64_t max_le
  *                         KV head h of softmax_t(scale q_g . k_t),  t < seq_len
  *   scores_in, scores_out  device, [batch][H][capacity] float, 8-byte aligned,
  *                one array or two that do not overlap (also for a paged
- *                cache: by position); positions from seq_len on are neither
- *                read nor written; a new token's position starts from 0
- *                whatever scores_in holds there
+ *                cache: by position); a new token's position starts from 0
+ *                whatever scores_in holds there, and where pos_new >= seq_len
+ *                (appended, not attended) scores_out is set to 0 there; the
+ *                other positions from seq_len on are neither read nor written
  * Two launches on `stream`; sums in float32, the query heads in order (the
  * same bits on every run).
  * Other arguments and errors as bgtq_decode_window_attn.

@@ -487,7 +487,8 @@ def bgtq_decode_score_attn(plan: Plan, q_fp16, cache: Cache, seq_lens, max_len: 
     weight: scores_out[b][h][t] = scores_in[b][h][t] + the weights of position t summed over the
     query heads of KV head h, t < seq_len ([B][H][capacity] float32 each; scores_out may be
     scores_in; positions from seq_len on are left as they are).  Other arguments as
-    bgtq_decode_window_attn; a new token's position starts from a score of 0."""
+    bgtq_decode_window_attn; a new token's position starts from a score of 0, also where
+    pos_new >= seq_len (appended, not attended)."""
     import torch
     batch, dev = _decode_args(plan, q_fp16, cache, seq_lens, out, k_new, v_new, pos_new, status)
     for x, name in ((scores_in, "scores_in"), (scores_out, "scores_out")):

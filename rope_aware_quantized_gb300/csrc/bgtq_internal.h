@@ -251,7 +251,8 @@ cudaError_t launch_decode(const bgtq_plan& p, cudaStream_t s, const void* q, con
 int64_t decode_window_positions(int64_t max_len, int64_t sinks, int64_t window);
 // scores_out[b][h][t] = scores_in[b][h][t] (0 at a fused step's new position)
 // + the attention weights of position t summed over the KV head's query
-// heads, t < seq_lens[b] <= max_len, from what a scoring decode left.
+// heads, t < seq_lens[b] <= max_len, from what a scoring decode left; 0 at a
+// new position from seq_lens[b] on.
 cudaError_t launch_score_add(const bgtq_plan& p, cudaStream_t s, const bgtq_cache& c, const int32_t* seq_lens,
                              int64_t max_len, int batch, const DecodeExtra& extra, const int32_t* pos_new,
                              const float* scores_in, float* scores_out);

@@ -9,6 +9,8 @@
 // merged (m, L); a second launch turns them into weights.  At a cache of 128K
 // tokens the logits of a layer are 8 MB and stay in the 129 MB L2 between the
 // two launches.  Sums run over the query heads in order: no atomics.
+#include <algorithm>
+
 #include "decode_kernel.cuh"
 
 namespace bgtq {
@@ -38,6 +40,9 @@ __global__ void __launch_bounds__(kScoreThreads) score_add_kernel(ScoreParams p)
     const int t0 = (blockIdx.x * kScoreThreads + threadIdx.x) * kScoreTok;
     const int fresh = p.pos_new ? p.pos_new[b] : -1;  // a new position has no weight yet
     pdl_wait();  // the logits, and the scores a previous kernel may be writing
+    // a new position that this step does not attend (at or past the length)
+    // starts at 0 as well: no other call would set it
+    if (fresh >= seq && fresh < p.cap && blockIdx.x == 0 && threadIdx.x == 0) p.out[unit * (size_t)p.cap + fresh] = 0.0f;
     if (t0 >= seq) return;
     // every head's statistics and logits in flight at once, then the sums in
     // the heads' order
@@ -76,7 +81,7 @@ cudaError_t launch_decode_score(const DecodeParams& p, dim3 grid, cudaStream_t s
 cudaError_t launch_score_add(const bgtq_plan& pl, cudaStream_t s, const bgtq_cache& c, const int32_t* seq_lens,
                              int64_t max_len, int batch, const DecodeExtra& extra, const int32_t* pos_new,
                              const float* scores_in, float* scores_out) {
-    if (max_len == 0) return cudaSuccess;
+    if (max_len == 0 && !pos_new) return cudaSuccess;
     ScoreParams p;
     p.logit = extra.logit;
     p.stride = extra.logit_stride;
@@ -91,7 +96,7 @@ cudaError_t launch_score_add(const bgtq_plan& pl, cudaStream_t s, const bgtq_cac
     p.G = pl.G;
     constexpr int64_t per_block = kScoreThreads * kScoreTok;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((max_len + per_block - 1) / per_block), (unsigned)pl.H, (unsigned)batch);
+    cfg.gridDim = dim3((unsigned)std::max<int64_t>(1, (max_len + per_block - 1) / per_block), (unsigned)pl.H, (unsigned)batch);
     cfg.blockDim = dim3(kScoreThreads, 1, 1);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
