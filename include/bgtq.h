@@ -21,13 +21,17 @@
  *   - `stream` is a cudaStream_t passed as void* (NULL = legacy default
  *     stream).  Device work is enqueued asynchronously on it; no call
  *     synchronises the host except bgtq_plan_create/destroy.
- *   - The quantize-append and decode kernels launch with programmatic
- *     dependent launch: each may start while the previous kernel on the
- *     stream is still running, does its plan-static set-up, and waits for
- *     that kernel to finish before it reads q, k, v, pos_start or the cache.
- *     The decode kernel reads seq_lens BEFORE that wait, so seq_lens must not
- *     be written by a kernel that triggers its dependents early (no kernel
- *     of this library writes it; ordinary kernels and copies are fine).
+ *   - The quantize-append, decode, windowed prefill and eviction kernels
+ *     launch with programmatic dependent launch: each may start while the
+ *     previous kernel on the stream is still running, does its plan-static
+ *     set-up, and waits for that kernel to finish before it reads q, k, v,
+ *     the scores or the cache.
+ *     The decode kernels read seq_lens and pos_new, the append reads
+ *     pos_start BEFORE that wait, so these must not be written by a kernel
+ *     that triggers its dependents early (ordinary kernels and copies are
+ *     fine; of this library's kernels only bgtq_evict's write lengths, and
+ *     they let no kernel after the call start early).  bgtq_evict reads
+ *     everything after the wait.
  *   - head_dim must be 128.  Inputs must be finite: NaN/Inf inputs give
  *     unspecified codes, never a fault.
  *   - Errors discovered on the device (positions beyond the cache capacity,
@@ -483,8 +487,9 @@ int bgtq_decode_score_attn(const bgtq_plan* plan, void* stream, const void* q_fp
  *   lse          device, [batch][H*G][t] float or NULL: natural logarithm of
  *                the sum of exp(softmax_scale q_i . k_j) over the keys j that
  *                row i sees
- * Records, other arguments and errors as bgtq_prefill_attn; also INVALID_ARG
- * for sinks < 0 or window < 1.  Key tiles that no row of a query block sees
+ * Records, precision (probabilities rounded to fp16 before they meet the
+ * values, whatever the output's type), other arguments and errors as
+ * bgtq_prefill_attn; also INVALID_ARG for sinks < 0 or window < 1.  Key tiles that no row of a query block sees
  * are neither loaded nor multiplied.  q, k and v are finite: as in
  * bgtq_prefill_attn a value that is not reaches the rows of its head's other
  * positions within 128, seen or not.

@@ -115,7 +115,9 @@ constexpr int kMaxClusters = 64;  // clusters per (sequence, head)
 constexpr int64_t kMaxSplitTokens = 4096;  // longest token split of one CTA
 constexpr int kWinPre = 256;               // longest fp16 key window of the precomputed-logit instance (1)
 // (windowed and scoring instances: twice as long, so that a large batch of
-// windows of 4096 tokens is one split each; 86 -> 73 us for 32 x 8 of them)
+// windows of 4096 tokens is one split each; 86 -> 73 us for 32 x 8 of them.
+// 32 x 8 full windows of 8192 + 16, two splits each, take 135 us: no more per
+// visible token than 69 us for 4096 + 16)
 constexpr int64_t kMaxSplitTokensBounded = 2 * kMaxSplitTokens;
 // 16-token tiles of one warp
 template <int kMode>
@@ -505,8 +507,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
 
     // The next kernel may launch right away; everything this kernel reads
     // that an earlier kernel may still be writing (q, the cache, the
-    // workspace) is read only after pdl_wait().  seq_lens is never written by
-    // this library's kernels.  Every CTA passes pdl_wait() before it exits.
+    // workspace) is read only after pdl_wait().  seq_lens and pos_new are read
+    // before it: a kernel that writes lengths or positions must not let its
+    // dependents start early.  (Of this library's kernels the eviction's write
+    // lengths; its last one has no early trigger.)  Every CTA passes
+    // pdl_wait() before it exits.
     pdl_trigger();
     const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -634,7 +639,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) decode_kernel(DecodeParams p) 
     }
     // paged: the token slots of all the warp's tiles (at most kMaxTilesPerWarp:
     // a paged cache holds at most kMaxSplitTokens * kCluster * kMaxClusters
-    // positions, so a split is at most kMaxSplitTokens long) and of the new
+    // positions, so a split is at most kMaxSplitTokens long; one of the windowed
+    // and scoring instances at most kMaxSplitTokensBounded) and of the new
     // token, looked up before the wait (the page table is read like seq_lens),
     // so that the main loop only reads a slot from shared memory
     int64_t sl_new = 0;

@@ -9,7 +9,8 @@
 // same order.  The threshold (the score that the last kept position has) is
 // found by an exact radix selection: three histograms of 11, 11 and 10 bits
 // from the top, each summed over the cluster through distributed shared
-// memory, one cluster barrier apiece.  Equal scores at the threshold are
+// memory between two cluster barriers; a seventh one joins the counts of what
+// is kept.  Equal scores at the threshold are
 // taken from the lowest position.  Every CTA then counts its share, and its
 // warps write their positions at the index that the counts before them give:
 // no atomics on global memory, the same result on every run.  The kernel is

@@ -39,8 +39,15 @@
 // sees nothing of.  Only the diagonal tile, those at the window's low edge and
 // those at the sinks' end are masked.  It also gives each row's log-sum-exp.
 // 32768 rows x 16 query heads under a window of 4096: 830 us with the append
-// (31 us), 1.24 PFLOP/s of the visible pairs' products; a tile's softmax (1690
-// clocks a head) and its own head's MMAs (1100) take turns.  Tried and slower:
+// (31 us), 1.24 PFLOP/s of the visible pairs' products.  A tile of both heads
+// takes 3480 clocks: a head's softmax works 1690 of them and waits 1790 for its
+// next S, of which its P.V and S products need 1024 at the tensor cores' full
+// rate.  The rest of the wait has not been taken apart; the other head's
+// products use the same tensor cores, and chains into one accumulator run below
+// their full rate (two interleaved chains of S 1553 TFLOP/s, one 985).
+// Probabilities are fp16, as in the plain instance: an output is off by 1.7e-4
+// (2-norm, in fp32; a plain fp32 form 6e-7), 2.7e-4 with fp16's own 2.1e-4; P
+// as two parts would take half as many products again.  Tried and slower:
 // P handed over in halves (850 us), chunks of 64 keys with two buffers of S
 // per head (925), two threads a row (1466).
 // Every wait is bounded: after kWaitNs it sets BGTQ_STATUS_TIMEOUT, the CTA
