@@ -72,6 +72,7 @@ extern "C" {
 #define BGTQ_STATUS_SEQLEN_CAPACITY 2 /* seq_len > capacity or < 0: clamped */
 #define BGTQ_STATUS_PAGE_RANGE 4      /* a page_table entry outside [0, n_pages) was met: writes to that
                                          page skipped, reads use page 0 (output unspecified) */
+#define BGTQ_STATUS_ROPE_RANGE 32     /* a rotary position outside [0, n_pos) was met: that row was skipped */
 #define BGTQ_STATUS_BOUNDS 16         /* library built with BGTQ_DEBUG_BOUNDS only: an index (record slot,
                                          position against the capacity, page entry, table entry) failed
                                          its range check; that access was skipped */
@@ -563,6 +564,176 @@ int bgtq_prefill_score(const bgtq_plan* plan, void* stream, const void* q_fp16, 
 int bgtq_evict(const bgtq_plan* plan, void* stream, const bgtq_cache* cache, const float* scores,
                const int32_t* seq_lens, int64_t max_len, int batch, int64_t keep, int64_t sinks, int64_t recent,
                const bgtq_cache* dst, float* dst_scores, int32_t* dst_lens, int32_t* kept, int32_t* dev_status);
+
+/*
+ * ---- Rotary positions.  The paper's keys are cached after their rotation
+ * ("under RoPE a key's contribution to a logit is a sum over 2-D frequency
+ * blocks", English abstract); these calls apply it, so that a model's
+ * projections go to the cache, and its queries to attention, as they are.
+ * Block i of 64 is the pair of dims (i, i + 64) of layout 0 or (2i, 2i + 1) of
+ * layout 1, rotated by the angle of position p = pos[axis[i]]:
+ *   lo' = lo cos[p][i] - hi sin[p][i],  hi' = hi cos[p][i] + lo sin[p][i]
+ * in float32, every product and the sum rounded, then rounded once to the
+ * output's type: the same bits whichever call does it.
+ */
+typedef struct {
+    const float* cos;      /* device, [n_pos][64], 16-byte aligned */
+    const float* sin;      /* device, [n_pos][64], 16-byte aligned */
+    int64_t n_pos;         /* rows of the tables, 1 <= n_pos <= 2^31 - 1 */
+    int axes;              /* 1..4: position axes (time, or time, height and width, ...) */
+    const uint8_t* axis;   /* host, [64]: axis of each block, < axes; NULL: axis 0 for all */
+    int layout;            /* 0 or 1, as rope_layout of a plan */
+} bgtq_rope;
+
+/* Rows [batch][heads][t][128] anywhere in memory: row (b, h, i) starts at
+ * data + b stride_b + h stride_h + i stride_t elements (strides of inputs may
+ * be 0; every row 16-byte aligned).  A view of a projection's output, for one. */
+typedef struct {
+    void* data;
+    int64_t stride_b, stride_h, stride_t;
+} bgtq_rows;
+
+#define BGTQ_F16 0
+#define BGTQ_F32 1
+#define BGTQ_BF16 2
+
+/*
+ * bgtq_rope_table — cos[p][i] = scale cos(p inv_freq[i]), sin likewise, for
+ * p < n_pos, angles and functions in 64 bits, rounded once.
+ *   inv_freq   host, [64], finite (0 leaves a block as it is)
+ *   scale      finite; the factor that some context extensions put on cos and sin
+ *   cos, sin   device, [n_pos][64] float
+ * Errors: INVALID_ARG, CUDA.
+ */
+int bgtq_rope_table(void* stream, const double* inv_freq, int64_t n_pos, double scale, float* cos, float* sin);
+
+/*
+ * bgtq_rope_rows — rotate the rows of queries and keys in one launch.
+ *   pos          device, [axes][batch][t] int32; a row with a position outside
+ *                [0, n_pos) is not written (BGTQ_STATUS_ROPE_RANGE)
+ *   q, q_out     n_q heads of rows; q_out may be q (same strides and type)
+ *   k, k_out     n_k heads of rows, or NULL with n_k = 0
+ *   in_dtype, out_dtype  BGTQ_F16, BGTQ_F32 or BGTQ_BF16, of q and k alike
+ *   inverse      1: rotate back (sin negated), which is also the gradient of
+ *                the rotation
+ * Output rows must not overlap one another, nor inputs unless in place (the
+ * former and each output against its own input are checked).
+ * Errors: INVALID_ARG, UNSUPPORTED (batch * t >= 2^31), CUDA.
+ */
+int bgtq_rope_rows(void* stream, const bgtq_rope* rope, const int32_t* pos, int batch, int t, const bgtq_rows* q,
+                   const bgtq_rows* q_out, int n_q, const bgtq_rows* k, const bgtq_rows* k_out, int n_k, int in_dtype,
+                   int out_dtype, int inverse, int32_t* dev_status);
+
+/*
+ * bgtq_rope_append — bgtq_quantize_append of keys that are not rotated yet:
+ * the records, norms and recent keys are those of bgtq_rope_rows (to fp16)
+ * followed by bgtq_quantize_append, bit for bit, without the rotated keys
+ * passing through memory.
+ *   rope       its layout must be the plan's
+ *   pos        device, [axes][batch][t_new] int32: the keys' rotary positions,
+ *              which need not be their cache positions (a cache that was cut,
+ *              a prompt with images); a token with one outside [0, n_pos) is
+ *              not appended (BGTQ_STATUS_ROPE_RANGE).  NULL: pos_start[b] + i on every axis
+ *   k, v       [batch][H][t_new][128] half
+ *   other arguments and errors as bgtq_quantize_append; also UNSUPPORTED for
+ *   more than 32767 sequences
+ */
+int bgtq_rope_append(const bgtq_plan* plan, void* stream, const bgtq_rope* rope, const int32_t* pos,
+                     const bgtq_rows* k, const bgtq_rows* v, int batch, int t_new, const int32_t* pos_start,
+                     const bgtq_cache* cache, int32_t* dev_status);
+
+/*
+ * ---- The 4-bit cache: keys and values in blocks of 16 of 4 bits each
+ * (e2m1: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives) under a scale of 8
+ * bits, 4.5 bits a value, 144 bytes for a token and head.  The paper has no
+ * counterpart; it is what a layer takes that was not calibrated, or that the
+ * packed cache's widths up to 3 bits a key do not serve.
+ * A block's scale s is amax/6 rounded to the nearest number of 5 exponent and
+ * 3 mantissa bits (ties to even; its byte is bits 14..7 of that number in
+ * fp16), at most 10240; x is coded as the nearest e2m1 number to x/s (ties
+ * to the even code, at most 6; the sign of x is kept).  A value s e2m1 is
+ * exact in fp16.  A block whose magnitudes are all at most 6 * 2^-18 (2.3e-5) becomes 0.
+ * The records of positions 16 g .. 16 g + 15 of a head are one group of 2304
+ * bytes, laid out for the tensor cores' fragments (dim d, position p of the
+ * group, nibble 0 = bits 0..3):
+ *   key code     byte 64 p + 16 (d/4 mod 4) + 2 (d/16) + (d/2 mod 2), nibble d mod 2
+ *   value code   byte 1024 + 512 (d/64) + 64 (d mod 8) + 16 (p/2 mod 4) +
+ *                4 (d/16 mod 4) + 2 (p/8) + (d/8 mod 2), nibble p mod 2
+ *   key scale    byte 2048 + 8 p + d/16
+ *   value scale  byte 2176 + 32 (p/2 mod 4) + 4 (d/16) + 2 (p/8) + p mod 2
+ */
+typedef struct {
+    void* groups;     /* device, [B][H][capacity/16][2304] bytes, or paged: [n_pages][H][P/16][2304]; 16-byte aligned */
+    int64_t capacity; /* positions per (sequence, head), a multiple of 16, at most 2^30 */
+    int n_heads;      /* KV heads H, 1..4096 */
+    const int32_t* page_table; /* device, [B][max_pages], or NULL: contiguous; as in bgtq_cache */
+    int64_t max_pages;         /* capacity = max_pages * page_tokens */
+    int64_t page_tokens;       /* P: a power of two, 16 <= P <= 2^20 */
+    int64_t n_pages;
+} bgtq_fp4_cache;
+
+/* Bytes of the groups of `batch` sequences of `capacity` positions (a multiple
+ * of 16); for a paged cache batch = n_pages, capacity = page_tokens.  Host only. */
+int bgtq_fp4_cache_bytes(int n_kv_heads, int batch, int64_t capacity, size_t* bytes);
+
+/*
+ * bgtq_fp4_append — encode and store new tokens.
+ *   rope, pos  NULL: k is rotated already; else k is rotated on the way (to
+ *              fp16, as bgtq_rope_rows), pos as in bgtq_rope_append
+ *   k, v       [batch][H][t_new][128] half
+ *   pos_start  device, [batch] int32: first cache position of each sequence; a
+ *              sequence with pos_start < 0 or pos_start + t_new > capacity is
+ *              skipped (BGTQ_STATUS_APPEND_CAPACITY)
+ * Other positions of the cache keep their bytes.  An unmapped page: those
+ * tokens are skipped (BGTQ_STATUS_PAGE_RANGE).  Inputs are finite: one that is
+ * not gives unspecified codes of its own block.
+ * Errors: INVALID_ARG, UNSUPPORTED (more than 65535 sequences), CUDA.
+ */
+int bgtq_fp4_append(void* stream, const bgtq_rope* rope, const int32_t* pos, const bgtq_rows* k, const bgtq_rows* v,
+                    int batch, int t_new, const int32_t* pos_start, const bgtq_fp4_cache* cache, int32_t* dev_status);
+
+/* Workspace bytes of bgtq_fp4_attn for `batch` sequences no longer than
+ * max_len; enough for a call with a smaller batch, t, max_len.  Zero-filled
+ * once before first use; every call leaves its counters zero, so one workspace
+ * serves calls of any shape in turn. */
+int bgtq_fp4_attn_workspace(int n_kv_heads, int group, int batch, int t, int64_t max_len, size_t* bytes);
+
+/*
+ * bgtq_fp4_attn — attention of each sequence's last t tokens over the 4-bit
+ * cache, which holds them (append first): t = 1 is a decode step, t = 2..
+ * a few drafted tokens, more a prompt's chunk.
+ *   rope, pos  NULL: q is rotated already; else rotated on the way (to fp16),
+ *              pos device [axes][batch][t] int32 or NULL: the row's cache position
+ *              on every axis; a row with a position outside [0, n_pos) gives
+ *              zeros (BGTQ_STATUS_ROPE_RANGE)
+ *   q          [batch][H*group][t][128] half
+ *   group      query heads per KV head, 1..8; query head h reads KV head h / group
+ *   seq_lens   device, [batch] int32: tokens n of each sequence, the t new ones
+ *              included; row i is at position n - t + i and sees the positions up
+ *              to its own; a row before position 0 gives zeros
+ *   max_len    host bound of seq_lens; a longer sequence is cut to it
+ *              (BGTQ_STATUS_SEQLEN_CAPACITY; its rows are then the cut one's last)
+ *   out        device, [batch][H*group][t][128], half (out_dtype 0) or float
+ *              (1), 16-byte aligned
+ *   workspace  device, 256-byte aligned, bgtq_fp4_attn_workspace bytes; two
+ *              calls that may overlap on the GPU need two
+ * Logits are fp16 products summed in fp32, probabilities taken in 22 bits.
+ * Positions from n on, and their bytes, do not matter.
+ * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (more than 65535 sequences,
+ * batch * H > 65535, sizes past 2^31 rows), CUDA.
+ */
+int bgtq_fp4_attn(void* stream, const bgtq_rope* rope, const int32_t* pos, const bgtq_rows* q, int group, int batch,
+                  int t, const bgtq_fp4_cache* cache, const int32_t* seq_lens, int64_t max_len, void* out,
+                  int out_dtype, float softmax_scale, void* workspace, size_t ws_bytes, int32_t* dev_status);
+
+/*
+ * bgtq_fp4_dequant — positions [t0, t1) of (sequence b, head) back to float32,
+ * for inspection.  k_out, v_out: device, [t1-t0][128] float, either may be
+ * NULL; `batch` as the cache's.  An unmapped page gives zeros.
+ * Errors: INVALID_ARG, CUDA.
+ */
+int bgtq_fp4_dequant(void* stream, const bgtq_fp4_cache* cache, int batch, int b, int head, int64_t t0, int64_t t1,
+                     float* k_out, float* v_out);
 
 /*
  * bgtq_logit_mae — RoPE-logit fidelity diagnostic: for every query head, the

@@ -16,13 +16,14 @@ import ctypes as C
 
 import numpy as np
 
-from ._native import BgtqCache, BgtqHeadTables, lib
+from ._native import BgtqCache, BgtqFp4Cache, BgtqHeadTables, BgtqRope, BgtqRows, lib
 
 HEAD_DIM = 128
 BGTQ_PLAN_HOST_ONLY = 1
 STATUS_APPEND_CAPACITY = 1
 STATUS_SEQLEN_CAPACITY = 2
 STATUS_PAGE_RANGE = 4
+STATUS_ROPE_RANGE = 32
 
 
 class BgtqError(RuntimeError):
@@ -576,6 +577,239 @@ def bgtq_evict(plan: Plan, cache: Cache, scores, seq_lens, max_len: int, keep: i
                             _ptr(status)))
 
 
+# ----------------------------------------------------------------------------- rotary positions
+
+class Rope:
+    """Rotary tables and how blocks meet positions: cos, sin [n_pos][64] float32 CUDA tensors (of
+    bgtq_rope_table, or the caller's own); layout 0 pairs dims (i, i + 64), 1 (2i, 2i + 1);
+    axis: the position axis of each of the 64 blocks (None: one axis), `sections` gives the same as
+    block counts per axis in order, (16, 24, 24) for 16 blocks of time, 24 of height and 24 of width."""
+
+    def __init__(self, cos, sin, layout: int = 0, axis=None, sections=None):
+        import torch
+        for x, name in ((cos, "cos"), (sin, "sin")):
+            if x.dtype != torch.float32 or x.dim() != 2 or x.shape[1] != HEAD_DIM // 2 or not x.is_contiguous() or not x.is_cuda:
+                raise ValueError(f"{name} must be a contiguous [n_pos][64] float32 CUDA tensor")
+        if cos.shape != sin.shape or cos.device != sin.device:
+            raise ValueError("cos and sin must have one shape and one device")
+        if axis is not None and sections is not None:
+            raise ValueError("axis and sections are given one or the other")
+        if sections is not None:
+            axis = [a for a, n in enumerate(sections) for _ in range(n)]
+        if axis is not None and (len(axis) != HEAD_DIM // 2 or min(axis) < 0 or max(axis) > 3):
+            raise ValueError("axis names one of at most 4 axes for each of the 64 blocks")
+        self.cos, self.sin, self.layout = cos, sin, layout
+        self.axes = 1 if axis is None else max(axis) + 1
+        self.axis = None if axis is None else np.ascontiguousarray(axis, dtype=np.uint8)
+        self.device = cos.get_device()
+        self.desc = BgtqRope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], self.axes, _ptr(self.axis), layout)
+
+
+def _rope_args(rope, pos, batch: int, t: int, dev: int):
+    """The descriptor and the positions' pointer; pos [axes][B][T] int32 (one axis: also [B][T]) or None."""
+    import torch
+    if rope is None:
+        if pos is not None:
+            raise ValueError("pos without rope")
+        return None, None
+    if rope.device != dev:
+        raise ValueError(f"the rope's tables are on cuda:{rope.device}, the current device is cuda:{dev}")
+    if pos is not None and not (rope.axes == 1 and pos.shape == (batch, t) and pos.dtype == torch.int32 and pos.is_contiguous()
+                                and pos.get_device() == dev):
+        _need(pos, "pos", torch.int32, (rope.axes, batch, t), dev)
+    return C.byref(rope.desc), _ptr(pos)
+
+
+def _rows(x, name: str, dtype, shape, dev: int) -> BgtqRows:
+    """Rows of a [B][heads][T][128] tensor of any strides but the innermost."""
+    if (dtype is not None and x.dtype != dtype) or x.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    if x.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor on the current device")
+    st = x.stride()
+    if st[3] != 1 and x.numel():
+        raise ValueError(f"{name}: the 128 elements of a row must be contiguous")
+    return BgtqRows(x.data_ptr(), st[0], st[1], st[2])
+
+
+def bgtq_rope_table(inv_freq, n_pos: int, scale: float = 1.0, device="cuda", stream=None):
+    """(cos, sin) [n_pos][64] float32: scale cos(p inv_freq[i]) and scale sin(p inv_freq[i]), computed in 64 bits."""
+    import torch
+    f = np.ascontiguousarray(np.asarray(inv_freq, dtype=np.float64))
+    if f.shape != (HEAD_DIM // 2,):
+        raise ValueError("inv_freq must hold 64 frequencies")
+    if n_pos < 1:
+        raise ValueError("n_pos must be >= 1")
+    cos = torch.empty((n_pos, HEAD_DIM // 2), dtype=torch.float32, device=device)
+    sin = torch.empty_like(cos)
+    _device_is_current(cos, "device")
+    _check(lib().bgtq_rope_table(_stream(stream, cos.get_device()), f.ctypes.data, n_pos, scale, _ptr(cos), _ptr(sin)))
+    return cos, sin
+
+
+def _device_is_current(x, name: str):
+    if x.get_device() != _device(x):
+        raise ValueError(f"{name} must be the current CUDA device")
+
+
+def _row_dtype(x) -> int:
+    import torch
+    try:
+        return {torch.float16: 0, torch.float32: 1, torch.bfloat16: 2}[x.dtype]
+    except KeyError:
+        raise ValueError("rows must be float16, float32 or bfloat16") from None
+
+
+def bgtq_rope_rows(rope: Rope, pos, q, q_out, k=None, k_out=None, inverse: bool = False, status=None, stream=None):
+    """Rotate queries and keys by their positions in one launch: q, q_out [B][n_q][T][128] and k, k_out
+    [B][n_k][T][128] (None: q alone), of any strides but the innermost (a transposed view of a
+    projection's [B][T][heads][128] output, for one); float16, float32 or bfloat16, one type for q and k,
+    one for q_out and k_out, which may be q and k themselves.  pos: [axes][B][T] int32, or [B][T] with
+    one axis; a row with a position outside the tables is not written.  inverse: rotate back (the
+    gradient of the rotation)."""
+    b, nq, t, _ = q.shape
+    dev = _device(q)
+    rd, pp = _rope_args(rope, pos, b, t, dev)
+    if rope is None or pos is None:
+        raise ValueError("rope and pos are needed")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out are given together or not at all")
+    qi, qo = _rows(q, "q", None, (b, nq, t, HEAD_DIM), dev), _rows(q_out, "q_out", None, (b, nq, t, HEAD_DIM), dev)
+    nk, ki, ko = 0, None, None
+    if k is not None:
+        nk = k.shape[1]
+        ki, ko = _rows(k, "k", q.dtype, (b, nk, t, HEAD_DIM), dev), _rows(k_out, "k_out", q_out.dtype, (b, nk, t, HEAD_DIM), dev)
+    _on_device(None, status, dev)
+    _check(lib().bgtq_rope_rows(_stream(stream, dev), rd, pp, b, t, C.byref(qi), C.byref(qo), nq,
+                                None if ki is None else C.byref(ki), None if ko is None else C.byref(ko), nk,
+                                _row_dtype(q), _row_dtype(q_out), 1 if inverse else 0, _ptr(status)))
+
+
+def bgtq_rope_append(plan: Plan, rope: Rope, pos, k, v, pos_start, cache: Cache, status=None, stream=None):
+    """bgtq_quantize_append of keys that are not rotated yet (k, v [B][H][T_new][128] float16 of any
+    strides but the innermost): rotated by pos ([axes][B][T_new] int32, [B][T_new] with one axis, None:
+    pos_start[b] + i) to float16 on the way, the same records as the two calls.  A token with a
+    position outside the tables is not appended."""
+    import torch
+    b, h, t, _ = k.shape
+    dev = _device(k)
+    shape = (b, plan.n_kv_heads, t, HEAD_DIM)
+    kr, vr = _rows(k, "k", torch.float16, shape, dev), _rows(v, "v", torch.float16, shape, dev)
+    if rope is None:
+        raise ValueError("rope is needed")
+    rd, pp = _rope_args(rope, pos, b, t, dev)
+    _need(pos_start, "pos_start", torch.int32, (b,), dev)
+    _on_device(cache, status, dev)
+    if cache.batch < b:
+        raise ValueError("the cache holds fewer sequences than k")
+    _check(lib().bgtq_rope_append(plan.handle, _stream(stream, dev), rd, pp, C.byref(kr), C.byref(vr), b, t, _ptr(pos_start),
+                                  C.byref(cache.desc), _ptr(status)))
+
+
+# ----------------------------------------------------------------------------- the 4-bit cache
+
+def bgtq_fp4_cache_bytes(n_kv_heads: int, batch: int, capacity: int) -> int:
+    n = C.c_size_t()
+    _check(lib().bgtq_fp4_cache_bytes(n_kv_heads, batch, capacity, C.byref(n)))
+    return n.value
+
+
+class Fp4Cache:
+    """One layer's 4-bit cache (e2m1 codes under a scale for each 16 values, 144 bytes a token and
+    head) in a caller-owned torch CUDA tensor; capacity a multiple of 16.  Contiguous, or paged as
+    Cache is (page_tokens a power of two from 16; write `page_table` in place)."""
+
+    def __init__(self, n_kv_heads: int, batch: int, capacity: int, device="cuda", page_tokens: int = 0, n_pages: int = 0):
+        import torch
+        if capacity % 16:
+            raise ValueError("capacity must be a multiple of 16")
+        self.n_kv_heads, self.batch, self.capacity, self.page_tokens = n_kv_heads, batch, capacity, page_tokens
+        self.page_table, self.max_pages, self.n_pages = None, 0, 0
+        if page_tokens:
+            if capacity % page_tokens:
+                raise ValueError("a paged cache needs capacity to be a multiple of page_tokens")
+            self.max_pages = capacity // page_tokens
+            self.n_pages = n_pages or batch * self.max_pages
+            n = bgtq_fp4_cache_bytes(n_kv_heads, self.n_pages, page_tokens)
+            ident = torch.arange(batch * self.max_pages, dtype=torch.int32, device=device)
+            self.page_table = torch.where(ident < self.n_pages, ident, torch.full_like(ident, -1))
+            self.page_table = self.page_table.view(batch, self.max_pages).contiguous()
+        else:
+            n = bgtq_fp4_cache_bytes(n_kv_heads, batch, capacity)
+        self.groups = torch.zeros(n, dtype=torch.uint8, device=device)
+        self.desc = BgtqFp4Cache(self.groups.data_ptr(), capacity, n_kv_heads, _ptr(self.page_table), self.max_pages,
+                                 page_tokens, self.n_pages)
+
+    def nbytes(self) -> int:
+        return self.groups.numel()
+
+
+def _on_fp4(cache: Fp4Cache, batch: int, status, dev: int):
+    if cache.groups.get_device() != dev:
+        raise ValueError(f"the cache is on {cache.groups.device}, the current device is cuda:{dev}")
+    if cache.batch < batch:
+        raise ValueError("the cache holds fewer sequences than the call")
+    _on_device(None, status, dev)
+
+
+def bgtq_fp4_append(k, v, pos_start, cache: Fp4Cache, rope: Rope | None = None, pos=None, status=None, stream=None):
+    """Encode and store new tokens (k, v [B][H][T_new][128] float16 of any strides but the innermost) at
+    positions pos_start[b] ..; with rope the keys are rotated on the way, pos as in bgtq_rope_append."""
+    import torch
+    b, h, t, _ = k.shape
+    dev = _device(k)
+    shape = (b, cache.n_kv_heads, t, HEAD_DIM)
+    kr, vr = _rows(k, "k", torch.float16, shape, dev), _rows(v, "v", torch.float16, shape, dev)
+    rd, pp = _rope_args(rope, pos, b, t, dev)
+    _need(pos_start, "pos_start", torch.int32, (b,), dev)
+    _on_fp4(cache, b, status, dev)
+    _check(lib().bgtq_fp4_append(_stream(stream, dev), rd, pp, C.byref(kr), C.byref(vr), b, t, _ptr(pos_start),
+                                 C.byref(cache.desc), _ptr(status)))
+
+
+def bgtq_fp4_attn_workspace(n_kv_heads: int, group: int, batch: int, t: int, max_len: int) -> int:
+    n = C.c_size_t()
+    _check(lib().bgtq_fp4_attn_workspace(n_kv_heads, group, batch, t, max_len, C.byref(n)))
+    return n.value
+
+
+def bgtq_fp4_attn(q, cache: Fp4Cache, seq_lens, max_len: int, out, workspace, rope: Rope | None = None, pos=None,
+                  softmax_scale: float | None = None, status=None, stream=None):
+    """Attention of each sequence's last T tokens over the 4-bit cache that holds them (append first):
+    q [B][H*G][T][128] float16 of any strides but the innermost (T = 1: also [B][H*G][128]), out the same
+    shape, contiguous, float16 or float32; seq_lens [B] int32 counts the T tokens; row i, at position
+    seq_len - T + i, sees the positions up to its own.  With rope the queries are rotated on the way, by
+    pos ([axes][B][T] int32, [B][T] with one axis) or their own positions.  workspace: a uint8 CUDA
+    tensor of bgtq_fp4_attn_workspace bytes, zeroed before its first use."""
+    import torch
+    if q.dim() == 3:
+        q, out = q.unsqueeze(2), out.unsqueeze(2)
+    b, hq, t, _ = q.shape
+    dev = _device(q)
+    if hq % cache.n_kv_heads or not 1 <= hq // cache.n_kv_heads <= 8:
+        raise ValueError("q must have 1 to 8 query heads for each KV head")
+    qr = _rows(q, "q", torch.float16, (b, hq, t, HEAD_DIM), dev)
+    _need(out, "out", out.dtype, (b, hq, t, HEAD_DIM), dev)
+    rd, pp = _rope_args(rope, pos, b, t, dev)
+    _need(seq_lens, "seq_lens", torch.int32, (b,), dev)
+    _on_fp4(cache, b, status, dev)
+    scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
+    _check(lib().bgtq_fp4_attn(_stream(stream, dev), rd, pp, C.byref(qr), hq // cache.n_kv_heads, b, t, C.byref(cache.desc),
+                               _ptr(seq_lens), max_len, _ptr(out), _out_dtype(out), scale, _ptr(workspace),
+                               _scratch(workspace, "workspace", dev), _ptr(status)))
+
+
+def bgtq_fp4_dequant(cache: Fp4Cache, b: int, head: int, t0: int, t1: int, k_out=None, v_out=None, stream=None):
+    """Positions [t0, t1) of (sequence b, head) back to float32 rows [t1 - t0][128], for inspection."""
+    import torch
+    dev = cache.groups.get_device()
+    for x, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if x is not None:
+            _need(x, name, torch.float32, (t1 - t0, HEAD_DIM), _device(x))
+    _check(lib().bgtq_fp4_dequant(_stream(stream, dev), C.byref(cache.desc), cache.batch, b, head, t0, t1, _ptr(k_out),
+                                  _ptr(v_out)))
+
+
 def bgtq_dequant_debug(plan: Plan, cache: Cache, b: int, head: int, t0: int, t1: int, k_out=None, v_out=None,
                        codec_domain: bool = False, stream=None):
     _check(lib().bgtq_dequant_debug(plan.handle, _stream(stream), C.byref(cache.desc), cache.batch, b, head, t0, t1,
@@ -588,5 +822,6 @@ __all__ = [
     "bgtq_decode_attn_noalloc", "bgtq_logit_mae", "bgtq_prefill_attn", "bgtq_prefill_chunk_workspace", "bgtq_prefill_chunk_attn",
     "bgtq_plan_save", "bgtq_plan_load", "bgtq_dequant_debug", "bgtq_decode_window_workspace", "bgtq_decode_window_attn",
     "bgtq_decode_score_workspace", "bgtq_decode_score_attn", "bgtq_prefill_window_attn", "bgtq_prefill_score_workspace",
-    "bgtq_prefill_score", "bgtq_evict",
+    "bgtq_prefill_score", "bgtq_evict", "Rope", "bgtq_rope_table", "bgtq_rope_rows", "bgtq_rope_append", "Fp4Cache",
+    "bgtq_fp4_cache_bytes", "bgtq_fp4_append", "bgtq_fp4_attn_workspace", "bgtq_fp4_attn", "bgtq_fp4_dequant",
 ]

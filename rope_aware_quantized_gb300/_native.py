@@ -21,6 +21,20 @@ class BgtqCache(C.Structure):
                 ("n_pages", C.c_int64)]
 
 
+class BgtqRope(C.Structure):
+    _fields_ = [("cos", C.c_void_p), ("sin", C.c_void_p), ("n_pos", C.c_int64), ("axes", C.c_int),
+                ("axis", C.c_void_p), ("layout", C.c_int)]
+
+
+class BgtqRows(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("stride_b", C.c_int64), ("stride_h", C.c_int64), ("stride_t", C.c_int64)]
+
+
+class BgtqFp4Cache(C.Structure):
+    _fields_ = [("groups", C.c_void_p), ("capacity", C.c_int64), ("n_heads", C.c_int), ("page_table", C.c_void_p),
+                ("max_pages", C.c_int64), ("page_tokens", C.c_int64), ("n_pages", C.c_int64)]
+
+
 class BgtqHeadTables(C.Structure):
     _fields_ = [("n_coded", C.c_int), ("perm", C.POINTER(C.c_uint8)), ("width", C.POINTER(C.c_uint8)),
                 ("piece", C.POINTER(C.c_uint8)), ("sign_k", C.POINTER(C.c_int8)), ("sign_v", C.POINTER(C.c_int8)),
@@ -77,6 +91,21 @@ EXPORTS = {
     "bgtq_evict": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(BgtqCache), C.c_void_p, C.c_void_p, C.c_int64, C.c_int,
                              C.c_int64, C.c_int64, C.c_int64, C.POINTER(BgtqCache), C.c_void_p, C.c_void_p, C.c_void_p,
                              C.c_void_p]),
+    "bgtq_rope_table": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_double, C.c_void_p, C.c_void_p]),
+    "bgtq_rope_rows": (C.c_int, [C.c_void_p, C.POINTER(BgtqRope), C.c_void_p, C.c_int, C.c_int, C.POINTER(BgtqRows),
+                                 C.POINTER(BgtqRows), C.c_int, C.POINTER(BgtqRows), C.POINTER(BgtqRows), C.c_int, C.c_int,
+                                 C.c_int, C.c_int, C.c_void_p]),
+    "bgtq_rope_append": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(BgtqRope), C.c_void_p, C.POINTER(BgtqRows),
+                                   C.POINTER(BgtqRows), C.c_int, C.c_int, C.c_void_p, C.POINTER(BgtqCache), C.c_void_p]),
+    "bgtq_fp4_cache_bytes": (C.c_int, [C.c_int, C.c_int, C.c_int64, C.POINTER(C.c_size_t)]),
+    "bgtq_fp4_append": (C.c_int, [C.c_void_p, C.POINTER(BgtqRope), C.c_void_p, C.POINTER(BgtqRows), C.POINTER(BgtqRows),
+                                  C.c_int, C.c_int, C.c_void_p, C.POINTER(BgtqFp4Cache), C.c_void_p]),
+    "bgtq_fp4_attn_workspace": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int64, C.POINTER(C.c_size_t)]),
+    "bgtq_fp4_attn": (C.c_int, [C.c_void_p, C.POINTER(BgtqRope), C.c_void_p, C.POINTER(BgtqRows), C.c_int, C.c_int, C.c_int,
+                                C.POINTER(BgtqFp4Cache), C.c_void_p, C.c_int64, C.c_void_p, C.c_int, C.c_float, C.c_void_p,
+                                C.c_size_t, C.c_void_p]),
+    "bgtq_fp4_dequant": (C.c_int, [C.c_void_p, C.POINTER(BgtqFp4Cache), C.c_int, C.c_int, C.c_int, C.c_int64, C.c_int64,
+                                   C.c_void_p, C.c_void_p]),
     "bgtq_logit_mae": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.POINTER(BgtqCache), C.c_int64,
                                  C.c_int, C.c_float, C.c_void_p]),
     "bgtq_dequant_debug": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(BgtqCache), C.c_int, C.c_int, C.c_int,

@@ -1,6 +1,6 @@
 """Builds the CUDA library libbgtq.so in-tree for sm_103a (GB300).
 
-Three translation units are compiled in parallel with nvcc and linked into
+The translation units are compiled in parallel with nvcc and linked into
 one shared library exporting the C ABI declared in include/bgtq.h.
 """
 
@@ -28,6 +28,13 @@ SOURCES = [
     ("codec_bulk_k1.cu", ["--fmad=false"]),
     ("codec_bulk_k2.cu", ["--fmad=false"]),
     ("codec_bulk_k3.cu", ["--fmad=false"]),
+    ("codec_rope_k1.cu", ["--fmad=false"]),
+    ("codec_rope_k2.cu", ["--fmad=false"]),
+    ("codec_rope_k3.cu", ["--fmad=false"]),
+    ("rope_host.cpp", []),
+    ("rope.cu", []),
+    ("fp4_append.cu", []),
+    ("fp4_attn.cu", []),
     ("decode_attn.cu", []),
     ("decode_attn_paged.cu", []),
     ("decode_attn_noalloc.cu", []),

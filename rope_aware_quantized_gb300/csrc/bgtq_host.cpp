@@ -977,9 +977,8 @@ int bgtq_prefill_chunk_attn(const bgtq_plan* p, void* stream, const void* q, con
 
 }  // extern "C"
 
-namespace {
+namespace bgtq {
 
-// The plan's device tables, on the current device.
 int check_plan_here(const bgtq_plan* p) {
     const int rc = check_plan(p);
     if (rc) return rc;
@@ -988,6 +987,10 @@ int check_plan_here(const bgtq_plan* p) {
         return set_error(BGTQ_ERR_INVALID_ARG, "the plan was built on device %d, the current device is %d", p->device, dev);
     return BGTQ_OK;
 }
+
+}  // namespace bgtq
+
+namespace {
 
 // Arguments that the windowed and the scoring decode share.
 int check_decode_call(const bgtq_plan* p, const void* q, const void* k_new, const void* v_new, const int32_t* pos_new,

@@ -163,6 +163,8 @@ cudaError_t launch_prefill_score(const bgtq_plan& pl, cudaStream_t s, const void
 // Host checks of a cache descriptor (buffers, alignment, capacity, the
 // recent-key buffer, paging); sets the thread's error message.
 int check_cache(const bgtq_plan* p, const bgtq_cache* c);
+// The plan's device tables, on the current device.
+int check_plan_here(const bgtq_plan* p);
 
 inline CacheMap make_cache_map(const bgtq_cache& c, int H, int batch, int32_t* status) {
     CacheMap m;

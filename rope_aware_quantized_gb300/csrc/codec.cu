@@ -28,7 +28,12 @@ constexpr int kPairsPerBlock = 16;  // token pairs each quantize_append block en
 // the rows of its next group before encoding the current one.  A pair that
 // is only half appended has its V record merged in place with atomic AND/OR,
 // so nothing is read back.
-__global__ void __launch_bounds__(128) quantize_append_kernel(QParams p) {
+// Keys that are rotated on the way (Par = RQParams): an element's partner, cos
+// and sin are loaded with it and the pair turned (half the work twice: such
+// appends are a few tokens, bound by latency); a token with a position
+// outside the tables is skipped whole.
+template <class Par>
+__global__ void __launch_bounds__(128) quantize_append_kernel(Par p) {
     __shared__ float s_thr[kThrCompact];
     __shared__ uint32_t rec[kWarpsQ][2][8 * kPairMaxW];  // records being assembled per warp
     __shared__ uint32_t rmask[2][8 * kPairMaxW];
@@ -58,6 +63,17 @@ __global__ void __launch_bounds__(128) quantize_append_kernel(QParams p) {
     const int64_t end = (int64_t)ps + p.t_new;
     const int64_t P0 = (int64_t)(ps >> 1) + (int64_t)blockIdx.x * kPairsPerBlock;
 
+    auto valid = [&](int64_t pos, int (&rp)[kMaxAxes]) -> bool {
+        if (pos < ps || pos >= end) return false;
+        if constexpr (kRotates<Par>) {
+            if (!rope_positions(p.rope, (int64_t)b * p.t_new + (pos - ps), pos, rp)) {
+                if (lane == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_ROPE_RANGE);
+                return false;
+            }
+        }
+        return true;
+    };
+
     if (is_k) {
         // ---- keys: warp w encodes tokens 2P + w of pairs P = P0 + i, i + 1
         const int krec_words = 4 * p.bk;
@@ -65,10 +81,16 @@ __global__ void __launch_bounds__(128) quantize_append_kernel(QParams p) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int64_t pos = 2 * (P0 + i + n) + warp;
-                if (pos >= ps && pos < end) {
-                    const __half* row = p.k + (unit * p.t_new + (size_t)(pos - ps)) * kD;
+                int rp[kMaxAxes];
+                if (valid(pos, rp)) {
+                    const __half* row = new_key(p, b, h, pos - ps);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) xh[n][k] = row[el.src[k]];
+                    for (int k = 0; k < 4; ++k) {
+                        if constexpr (kRotates<Par>)
+                            xh[n][k] = rope_elem(p.rope, rp, row, el.src[k]);
+                        else
+                            xh[n][k] = row[el.src[k]];
+                    }
                 }
             }
         };
@@ -82,7 +104,8 @@ __global__ void __launch_bounds__(128) quantize_append_kernel(QParams p) {
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int64_t pos = 2 * (P0 + i + n) + warp;
-                has[n] = pos >= ps && pos < end;
+                int rp[kMaxAxes];
+                has[n] = valid(pos, rp);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x[n][k] = has[n] ? __fmul_rn(__half2float(cur[n][k]), el.wh[k]) : 0.0f;
             }
@@ -108,7 +131,19 @@ __global__ void __launch_bounds__(128) quantize_append_kernel(QParams p) {
                 if (lane == 0) p.kn[sl] = rho[n];
                 if (p.recent > 0 && pos >= end - p.recent) {
                     // fp16 recent-key ring: the key as given, slot pos mod W
-                    const uint2 nat = *(reinterpret_cast<const uint2*>(p.k + (unit * p.t_new + (size_t)(pos - ps)) * kD) + lane);
+                    const __half* row = new_key(p, b, h, pos - ps);
+                    uint2 nat;
+                    if constexpr (kRotates<Par>) {
+                        int rp[kMaxAxes];
+                        rope_positions(p.rope, (int64_t)b * p.t_new + (pos - ps), pos, rp);
+                        __half e[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) e[k] = rope_elem(p.rope, rp, row, 4 * lane + k);
+                        nat = make_uint2(__half_as_ushort(e[0]) | (uint32_t)__half_as_ushort(e[1]) << 16,
+                                         __half_as_ushort(e[2]) | (uint32_t)__half_as_ushort(e[3]) << 16);
+                    } else {
+                        nat = *(reinterpret_cast<const uint2*>(row) + lane);
+                    }
                     *(reinterpret_cast<uint2*>(p.k_recent + (unit * p.recent + pos % p.recent) * kD) + lane) = nat;
                 }
             }
@@ -131,8 +166,7 @@ __global__ void __launch_bounds__(128) quantize_append_kernel(QParams p) {
 #pragma unroll
         for (int par = 0; par < 2; ++par) {
             const int64_t pos = pos0 + par;
-            if (pos >= ps && pos < end)
-                xr[par] = *(reinterpret_cast<const uint2*>(p.v + (unit * p.t_new + (size_t)(pos - ps)) * kD) + lane);
+            if (pos >= ps && pos < end) xr[par] = *(reinterpret_cast<const uint2*>(new_value(p, b, h, pos - ps)) + lane);
         }
     };
     uint2 cur[2] = {make_uint2(0, 0), make_uint2(0, 0)}, nxt[2] = {make_uint2(0, 0), make_uint2(0, 0)};
@@ -142,7 +176,8 @@ __global__ void __launch_bounds__(128) quantize_append_kernel(QParams p) {
         const int64_t pos0 = 2 * P;
         if (pos0 >= end) break;
         if (i + 2 < kPairsPerBlock) load(i + 2, nxt);
-        const bool has[2] = {pos0 >= ps, pos0 + 1 < end};
+        int rp[kMaxAxes];
+        const bool has[2] = {kRotates<Par> ? valid(pos0, rp) : pos0 >= ps, kRotates<Par> ? valid(pos0 + 1, rp) : pos0 + 1 < end};
         float x[2][4];
 #pragma unroll
         for (int par = 0; par < 2; ++par) {
@@ -297,11 +332,10 @@ __global__ void __launch_bounds__(128) dequant_kernel(DqParams p) {
 
 }  // namespace
 
-cudaError_t launch_quantize_append(const bgtq_plan& pl, cudaStream_t s, const void* k, const void* v, int batch,
-                                   int t_new, const int32_t* pos_start, const bgtq_cache& c, int32_t* status) {
-    QParams p;
-    p.k = static_cast<const __half*>(k);
-    p.v = static_cast<const __half*>(v);
+namespace {
+
+void fill_params(QParams& p, const bgtq_plan& pl, int batch, int t_new, const int32_t* pos_start, const bgtq_cache& c,
+                 int32_t* status) {
     p.t_new = t_new;
     p.H = pl.H;
     p.pos_start = pos_start;
@@ -321,6 +355,10 @@ cudaError_t launch_quantize_append(const bgtq_plan& pl, cudaStream_t s, const vo
     p.status = status;
     p.k_recent = static_cast<__half*>(c.k_recent);
     p.recent = c.recent;
+}
+
+template <class P>
+cudaError_t launch_append(const bgtq_plan& pl, cudaStream_t s, const P& p, int batch) {
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
     cudaLaunchAttribute attr;
@@ -331,15 +369,39 @@ cudaError_t launch_quantize_append(const bgtq_plan& pl, cudaStream_t s, const vo
     // Bulk appends (prefill) take the two-lanes-per-token kernel, which reads
     // whole fp16 rows with 16-byte loads (its grid's z holds two blocks per
     // sequence); small appends (decode), other widths and batches of more
-    // than 32767 sequences the warp-per-token kernel.
-    const bool aligned = ((reinterpret_cast<uintptr_t>(k) | reinterpret_cast<uintptr_t>(v)) & 15) == 0;
-    if (t_new >= kBulkMinTokens && aligned && pl.bk >= 1 && pl.bk <= 3 && pl.bv >= 1 && pl.bv <= 4 && batch <= 32767)
+    // than 32767 sequences the warp-per-token kernel.  (Rows of a rotated
+    // append are 16-byte aligned: its entry point checks.)
+    const bool aligned = ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 15) == 0;
+    if (p.t_new >= kBulkMinTokens && aligned && pl.bk >= 1 && pl.bk <= 3 && pl.bv >= 1 && pl.bv <= 4 && batch <= 32767)
         return launch_quantize_append_bulk(p, pl.bk, pl.bv, batch, s);
-    const int64_t pairs = (int64_t)t_new / 2 + 1;
+    const int64_t pairs = (int64_t)p.t_new / 2 + 1;
     const int64_t per_block = kPairsPerBlock;
     cfg.gridDim = dim3((unsigned)((pairs + per_block - 1) / per_block), (unsigned)pl.H, (unsigned)batch);
     cfg.blockDim = dim3(32 * kWarpsQ, 1, 1);
-    return cudaLaunchKernelEx(&cfg, quantize_append_kernel, p);
+    return cudaLaunchKernelEx(&cfg, quantize_append_kernel<P>, p);
+}
+
+}  // namespace
+
+cudaError_t launch_quantize_append(const bgtq_plan& pl, cudaStream_t s, const void* k, const void* v, int batch,
+                                   int t_new, const int32_t* pos_start, const bgtq_cache& c, int32_t* status) {
+    QParams p;
+    p.k = static_cast<const __half*>(k);
+    p.v = static_cast<const __half*>(v);
+    fill_params(p, pl, batch, t_new, pos_start, c, status);
+    return launch_append(pl, s, p, batch);
+}
+
+cudaError_t launch_rope_append(const bgtq_plan& pl, cudaStream_t s, const RopeParams& r, const RowsView& k, const RowsView& v,
+                               int batch, int t_new, const int32_t* pos_start, const bgtq_cache& c, int32_t* status) {
+    RQParams p;
+    p.k = static_cast<const __half*>(k.p);
+    p.v = static_cast<const __half*>(v.p);
+    fill_params(p, pl, batch, t_new, pos_start, c, status);
+    p.rope = r;
+    p.ksb = k.sb, p.ksh = k.sh, p.kst = k.st;
+    p.vsb = v.sb, p.vsh = v.sh, p.vst = v.st;
+    return launch_append(pl, s, p, batch);
 }
 
 cudaError_t launch_dequant(const bgtq_plan& pl, cudaStream_t s, const bgtq_cache& c, int batch, int b, int head,

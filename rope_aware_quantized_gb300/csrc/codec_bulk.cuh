@@ -175,23 +175,46 @@ __device__ __forceinline__ float half_scale_norm(float (&z)[64], int n, const fl
 // token's column of the key rows; rec: the token's record being assembled.
 // Every lane of the warp takes part (inactive tokens encode zeros and store
 // nothing).
-template <int BK>
-__device__ __forceinline__ void bulk_key_half(const QParams& p, int nc, int hf, const int* s_end, const float2* pw,
+template <int BK, class P>
+__device__ __forceinline__ void bulk_key_half(const P& p, int nc, int hf, const int* s_end, const float2* pw,
                                               const float* is, const uint4* cp, const uint32_t* pk, uint32_t* row,
-                                              uint32_t* rec, const uint4 (&w4)[8], bool act, size_t unit, int64_t pos,
-                                              int64_t end, int64_t sl) {
+                                              uint32_t* rec, uint4 (&w4)[8], bool act, size_t unit, int64_t pos,
+                                              int64_t end, int64_t sl, const int (&rp)[kMaxAxes]) {
+    // 16-byte pieces w4[0..3] and w4[4..7] of the row start at q0 and q1
+    int q0 = 8 * hf, q1 = 8 * hf + 4;
+    if constexpr (kRotates<P>) {
+        // this half's 32 blocks, eight at a time; rounded to fp16 as the cached key is
+        auto turn = [&](int m, uint4& wa, uint4& wb) {
+            uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
+            rope_rotate8(p.rope, rp, 32 * hf + 8 * m, a, b);
+            wa = make_uint4(a[0], a[1], a[2], a[3]);
+            wb = make_uint4(b[0], b[1], b[2], b[3]);
+        };
+        if (act && p.rope.layout == 0) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) turn(m, w4[m], w4[4 + m]);
+        } else if (act) {
+#pragma unroll
+            for (int m = 0; m < 4; ++m) turn(m, w4[2 * m], w4[2 * m + 1]);
+        }
+        if (p.rope.layout == 0) {
+            q0 = 4 * hf;
+            q1 = 8 + 4 * hf;
+        }
+    }
     if (act && p.recent > 0 && pos >= end - p.recent) {
         // fp16 recent-key ring: the key as given, slot pos mod W
-        uint4* rdst = reinterpret_cast<uint4*>(p.k_recent + (unit * p.recent + pos % p.recent) * kD) + 8 * hf;
+        uint4* rdst = reinterpret_cast<uint4*>(p.k_recent + (unit * p.recent + pos % p.recent) * kD);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) rdst[i] = w4[i];
+        for (int i = 0; i < 8; ++i) rdst[(i < 4 ? q0 : q1 - 4) + i] = w4[i];
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        row[32 * hf + 4 * i] = w4[i].x;
-        row[32 * hf + 4 * i + 1] = w4[i].y;
-        row[32 * hf + 4 * i + 2] = w4[i].z;
-        row[32 * hf + 4 * i + 3] = w4[i].w;
+        uint32_t* dst = row + 4 * ((i < 4 ? q0 : q1 - 4) + i);
+        dst[0] = w4[i].x;
+        dst[1] = w4[i].y;
+        dst[2] = w4[i].z;
+        dst[3] = w4[i].w;
     }
 #pragma unroll
     for (int i = 0; i < 2 * BK; ++i) rec[2 * BK * hf + i] = 0;
@@ -254,8 +277,8 @@ __device__ __forceinline__ void bulk_key_half(const QParams& p, int nc, int hf, 
 // words 4 BV hf .. 4 BV hf + 4 BV - 1 of the V pair record).  The thread pair
 // (even, odd token: lanes l, l ^ 1) of a half shares those words.  Every lane
 // of the warp takes part.
-template <int BV>
-__device__ __forceinline__ void bulk_value_half(const QParams& p, int hf, int par, const float* sv,
+template <int BV, class P>
+__device__ __forceinline__ void bulk_value_half(const P& p, int hf, int par, const float* sv,
                                                 const uint32_t* s_cell, uint32_t cell_base, const uint4 (&w4)[8],
                                                 bool act, int ps, int64_t pos, int64_t end, int64_t sl) {
     float z[64];
@@ -303,7 +326,8 @@ __device__ __forceinline__ void bulk_value_half(const QParams& p, int hf, int pa
 #pragma unroll
         for (int i = 0; i < kHW; ++i) vw[i] = 0;
     }
-    const bool partner = (pos ^ 1) >= ps && (pos ^ 1) < end;
+    bool partner = (pos ^ 1) >= ps && (pos ^ 1) < end;
+    if constexpr (kRotates<P>) partner = __shfl_xor_sync(0xffffffffu, (int)act, 1) != 0;  // (a token may be skipped)
     uint32_t full[kHW];
 #pragma unroll
     for (int i = 0; i < kHW; ++i) full[i] = vw[i] | __shfl_xor_sync(0xffffffffu, vw[i], 1);
@@ -341,8 +365,8 @@ __device__ __forceinline__ void bulk_value_half(const QParams& p, int hf, int pa
     }
 }
 
-template <int BK, int BV>
-__global__ void __launch_bounds__(kBulkThreads, kBulkMinBlocks) quantize_append_bulk_kernel(QParams p) {
+template <int BK, int BV, class P>
+__global__ void __launch_bounds__(kBulkThreads, kBulkMinBlocks) quantize_append_bulk_kernel(P p) {
     __shared__ float2 s_pw[2 * kPwRow];  // keys: (whitening x sign, source dim) per codec coordinate (0 past n_coded)
     __shared__ float s_is[2 * kFRow];    // 1/sqrt(piece) (keys)
     __shared__ float s_sv[2 * kFRow];    // value signs
@@ -373,16 +397,30 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkMinBlocks) quantize_append_
     const int tk = 16 * warp + (lane & 15);  // the block's token of this lane
     const int64_t end = (int64_t)ps + p.t_new;
     const int64_t pos = (int64_t)(ps & ~1) + (int64_t)blockIdx.x * kBulkTok + tk;
-    const bool act = pos >= ps && pos < end;
+    bool act = pos >= ps && pos < end;
     const size_t unit = (size_t)b * p.H + h;
+    int rp[kMaxAxes] = {};
+    if constexpr (kRotates<P>) {
+        if (act && !rope_positions(p.rope, (int64_t)b * p.t_new + (pos - ps), pos, rp)) {
+            act = false;
+            if (hf == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_ROPE_RANGE);
+        }
+    }
     // this half of the token's fp16 row (zeros for an inactive token): issued
     // first, so that the plan-static set-up below runs while it is in flight
     uint4 w4[8];
     if (act) {
-        const __half* x = is_v ? p.v : p.k;
-        const uint4* src = reinterpret_cast<const uint4*>(x + (unit * p.t_new + (size_t)(pos - ps)) * kD) + 8 * hf;
+        const uint4* src = reinterpret_cast<const uint4*>(is_v ? new_value(p, b, h, pos - ps) : new_key(p, b, h, pos - ps));
+        int q0 = 8 * hf, q1 = 8 * hf + 4;
+        if constexpr (kRotates<P>) {
+            // (keys of layout 0: both dims of this half's blocks)
+            if (!is_v && p.rope.layout == 0) {
+                q0 = 4 * hf;
+                q1 = 8 + 4 * hf;
+            }
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w4[i] = __ldg(src + i);
+        for (int i = 0; i < 8; ++i) w4[i] = __ldg(src + (i < 4 ? q0 : q1 - 4) + i);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w4[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -440,19 +478,20 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkMinBlocks) quantize_append_
     if (sl < 0 && p.status && hf == 0) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
     if (!is_v)
         bulk_key_half<BK>(p, nc, hf, s_end, s_pw + hf * kPwRow, s_is + hf * kFRow, s_cp + hf * kCpRow, s_pk + hf * kPkRow,
-                          s_dyn + tk * kRowWords, s_rec + tk * (4 * BK + 1), w4, act, unit, pos, end, sl);
+                          s_dyn + tk * kRowWords, s_rec + tk * (4 * BK + 1), w4, act, unit, pos, end, sl, rp);
     else
         bulk_value_half<BV>(p, hf, tk & 1, s_sv + hf * kFRow, s_cell, cell_base, w4, act, ps, pos, end, sl);
 }
 
 }  // namespace
 
-// Launch the bulk kernel for key width BK (instantiated in codec_bulk_k<BK>.cu).
-template <int BK>
-cudaError_t launch_bulk_bk(const QParams& p, int bv, int batch, cudaStream_t s);
+// Launch the bulk kernel for key width BK (P = QParams instantiated in
+// codec_bulk_k<BK>.cu, RQParams in codec_rope_k<BK>.cu).
+template <int BK, class P>
+cudaError_t launch_bulk_bk(const P& p, int bv, int batch, cudaStream_t s);
 
-template <int BK>
-cudaError_t launch_bulk_bk_impl(const QParams& p, int bv, int batch, cudaStream_t s) {
+template <int BK, class P>
+cudaError_t launch_bulk_bk_impl(const P& p, int bv, int batch, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.stream = s;
     cudaLaunchAttribute attr;
@@ -473,10 +512,10 @@ cudaError_t launch_bulk_bk_impl(const QParams& p, int bv, int batch, cudaStream_
         return e != cudaSuccess ? e : cudaLaunchKernelEx(&cfg, kernel, p);
     };
     switch (bv) {
-        case 1: return go(quantize_append_bulk_kernel<BK, 1>);
-        case 2: return go(quantize_append_bulk_kernel<BK, 2>);
-        case 3: return go(quantize_append_bulk_kernel<BK, 3>);
-        case 4: return go(quantize_append_bulk_kernel<BK, 4>);
+        case 1: return go(quantize_append_bulk_kernel<BK, 1, P>);
+        case 2: return go(quantize_append_bulk_kernel<BK, 2, P>);
+        case 3: return go(quantize_append_bulk_kernel<BK, 3, P>);
+        case 4: return go(quantize_append_bulk_kernel<BK, 4, P>);
         default: return cudaErrorInvalidValue;
     }
 }

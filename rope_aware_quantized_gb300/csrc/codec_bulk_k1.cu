@@ -4,8 +4,8 @@
 namespace bgtq {
 
 template <>
-cudaError_t launch_bulk_bk<1>(const QParams& p, int bv, int batch, cudaStream_t s) {
-    return launch_bulk_bk_impl<1>(p, bv, batch, s);
+cudaError_t launch_bulk_bk<1, QParams>(const QParams& p, int bv, int batch, cudaStream_t s) {
+    return launch_bulk_bk_impl<1, QParams>(p, bv, batch, s);
 }
 
 }  // namespace bgtq

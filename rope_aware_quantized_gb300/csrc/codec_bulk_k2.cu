@@ -4,8 +4,8 @@
 namespace bgtq {
 
 template <>
-cudaError_t launch_bulk_bk<2>(const QParams& p, int bv, int batch, cudaStream_t s) {
-    return launch_bulk_bk_impl<2>(p, bv, batch, s);
+cudaError_t launch_bulk_bk<2, QParams>(const QParams& p, int bv, int batch, cudaStream_t s) {
+    return launch_bulk_bk_impl<2, QParams>(p, bv, batch, s);
 }
 
 }  // namespace bgtq

@@ -12,7 +12,10 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "bgtq_internal.h"
+#include "rope.cuh"
 
 namespace bgtq {
 
@@ -39,10 +42,39 @@ struct QParams {
     int64_t recent;
 };
 
+// The same for keys that are rotated on the way: rows anywhere in memory.
+struct RQParams : QParams {
+    RopeParams rope;
+    int64_t ksb, ksh, kst, vsb, vsh, vst;  // strides of k and v in elements
+};
+template <class P>
+inline constexpr bool kRotates = std::is_same<P, RQParams>::value;
+
+#ifdef __CUDACC__
+namespace {
+// Row i of (b, h) of the new keys and values.
+template <class P>
+__device__ __forceinline__ const __half* new_key(const P& p, int b, int h, int64_t i) {
+    if constexpr (kRotates<P>)
+        return p.k + b * p.ksb + h * p.ksh + i * p.kst;
+    else
+        return p.k + (((size_t)b * p.H + h) * p.t_new + (size_t)i) * kD;
+}
+template <class P>
+__device__ __forceinline__ const __half* new_value(const P& p, int b, int h, int64_t i) {
+    if constexpr (kRotates<P>)
+        return p.v + b * p.vsb + h * p.vsh + i * p.vst;
+    else
+        return p.v + (((size_t)b * p.H + h) * p.t_new + (size_t)i) * kD;
+}
+}  // namespace
+#endif
+
 // Appends at least this long (and of the widths below) take the
 // two-lanes-per-token bulk kernel; it launches it on `s`.
 constexpr int kBulkMinTokens = 64;
 cudaError_t launch_quantize_append_bulk(const QParams& p, int bk, int bv, int batch, cudaStream_t s);
+cudaError_t launch_quantize_append_bulk(const RQParams& p, int bk, int bv, int batch, cudaStream_t s);
 
 namespace {
 

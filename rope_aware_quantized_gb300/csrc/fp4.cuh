@@ -1,0 +1,142 @@
+// The 4-bit cache: its groups, and the arithmetic of its codes and scales.
+//
+// Blocks of 16 values: 4-bit codes (e2m1) under an 8-bit scale whose byte is
+// bits 14..7 of an fp16 number (5 exponent bits, 3 mantissa bits), so that a
+// scale becomes fp16 by a shift, a code by the hardware's conversion, and
+// their product (2 + 4 significant bits, never below 2^-18) is exact in fp16:
+// no second scale for the row, no rounding when the cache is read.  A group
+// holds 16 positions of one head, keys and values, in the order in which the
+// lanes of an m16n8k16 product want them (bgtq.h gives the byte of every
+// value): 2304 contiguous bytes, which one bulk copy brings in.
+#pragma once
+
+#include "rope.cuh"
+
+namespace bgtq {
+
+constexpr int kGroup = 16;           // positions of a group
+constexpr int kGroupBytes = 2304;
+constexpr int kGroupV = 1024;        // value codes
+constexpr int kGroupKs = 2048;       // key scales
+constexpr int kGroupVs = 2176;       // value scales
+constexpr int kScaleMax = 226;       // byte of 10240: 6 x 10240 is finite in fp16
+
+struct Fp4Map {
+    uint8_t* base;
+    const int32_t* page_table;  // [B][max_pages], nullptr: contiguous
+    int64_t cap_groups;         // groups of a sequence
+    int64_t max_pages, n_pages;
+    int H, lg;                  // lg = log2(P / 16)
+#ifdef __CUDACC__
+    // nullptr when the page_table entry is outside [0, n_pages)
+    __device__ __forceinline__ uint8_t* group(int b, int h, int64_t gi) const {
+        if (!page_table) return base + (((int64_t)b * H + h) * cap_groups + gi) * kGroupBytes;
+        const int32_t pg = page_table[(int64_t)b * max_pages + (gi >> lg)];
+        if (pg < 0 || (int64_t)pg >= n_pages) return nullptr;
+        return base + ((((int64_t)pg * H + h) << lg) + (gi & (((int64_t)1 << lg) - 1))) * kGroupBytes;
+    }
+#endif
+};
+
+inline Fp4Map make_fp4_map(const bgtq_fp4_cache& c) {
+    Fp4Map m;
+    m.base = static_cast<uint8_t*>(c.groups);
+    m.page_table = c.page_table;
+    m.cap_groups = c.capacity / kGroup;
+    m.max_pages = c.page_table ? c.max_pages : 1;
+    m.n_pages = c.page_table ? c.n_pages : 1;
+    m.H = c.n_heads;
+    m.lg = 0;
+    if (c.page_table)
+        while (((int64_t)kGroup << m.lg) < c.page_tokens) ++m.lg;
+    return m;
+}
+
+// What bgtq_fp4_attn runs: the one-pass kernel for up to kFp4Rows query rows
+// of a KV head, or the tensor-core tiles over a decoded copy.
+constexpr int kFp4Rows = 32;
+struct Fp4Attn {
+    RopeParams rope;
+    RowsView q;
+    Fp4Map map;
+    const int32_t* seq_lens;
+    int64_t cap, max_len;
+    int batch, t, group;
+    void* out;
+    int out_dtype;
+    float scale;
+    void* ws;
+    int32_t* status;
+};
+size_t fp4_attn_workspace_bytes(int H, int group, int batch, int t, int64_t max_len);
+cudaError_t launch_fp4_attn(cudaStream_t s, const Fp4Attn& a);
+cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsView& k, const RowsView& v, int batch, int t_new,
+                              const int32_t* pos_start, const bgtq_fp4_cache& c, int32_t* status);
+cudaError_t launch_fp4_dequant(cudaStream_t s, const bgtq_fp4_cache& c, int b, int head, int64_t t0, int64_t t1, float* k_out,
+                               float* v_out);
+
+#ifdef __CUDACC__
+namespace {
+
+// Two neighbouring scale bytes (of `w`, at bytes lo and lo + 1) as two fp16.
+template <int kLo>
+__device__ __forceinline__ __half2 fp4_scales(uint32_t w) {
+    const uint32_t u = __byte_perm(w, 0u, kLo == 0 ? 0x1404 : 0x3424) >> 1;
+    return *reinterpret_cast<const __half2*>(&u);
+}
+
+// The four code pairs of a word: byte i gives the numbers of its low and high nibble.
+__device__ __forceinline__ void fp4_numbers(uint32_t w, __half2 (&x)[4]) {
+    uint32_t u[4];
+    asm("{\n .reg .b8 a, b, c, d;\n mov.b32 {a, b, c, d}, %4;\n cvt.rn.f16x2.e2m1x2 %0, a;\n cvt.rn.f16x2.e2m1x2 %1, b;\n"
+        " cvt.rn.f16x2.e2m1x2 %2, c;\n cvt.rn.f16x2.e2m1x2 %3, d;\n}\n"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const __half2*>(&u[i]);
+}
+
+// Byte of the scale of a block whose largest magnitude is amax: amax / 6 to
+// four significant bits, ties to even, steps of 2^-17 below 2^-14.
+__device__ __forceinline__ uint32_t fp4_scale_byte(float amax) {
+    const float y = __fdiv_rn(amax, 6.0f);
+    const uint32_t u = __float_as_uint(y);
+    const uint32_t norm = ((u + 0x7ffffu + ((u >> 20) & 1u)) >> 20) - (112u << 3);
+    const uint32_t sub = (uint32_t)__float2int_rn(__fmul_rn(y, 131072.0f));
+    return min(y < 6.103515625e-5f ? sub : norm, (uint32_t)kScaleMax);
+}
+
+// 16 fp16 values (8 words) -> 16 codes in dim order (2 words) and the scale
+// byte.  The quotient x/s is correctly rounded where it has to be: one
+// correction of x r with the exact remainder makes a quotient that is a
+// midpoint of two codes come out as that midpoint, and any other is at least
+// 2^-18 of itself away from one (x has 11 bits, s four, a midpoint three).
+__device__ __forceinline__ uint32_t fp4_encode(const uint32_t (&w)[8], uint32_t (&code)[2]) {
+    __half2 m = __habs2(*reinterpret_cast<const __half2*>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+    const uint32_t byte = fp4_scale_byte(fmaxf(__low2float(m), __high2float(m)));
+    const float s = __half2float(__ushort_as_half((unsigned short)(byte << 7)));
+    const float r = byte ? __frcp_rn(s) : 0.0f;
+#pragma unroll
+    for (int hw = 0; hw < 2; ++hw) {
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[4 * hw + i]));
+            const float a = __fmul_rn(x.x, r), b = __fmul_rn(x.y, r);
+            const float qa = __fmaf_rn(__fmaf_rn(-a, s, x.x), r, a), qb = __fmaf_rn(__fmaf_rn(-b, s, x.y), r, b);
+            uint32_t e;
+            asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(e) : "f"(qb), "f"(qa));
+            // (the correction turns a quotient -0 into +0: the sign is x's own)
+            c |= (e | ((w[4 * hw + i] >> 12) & 0x8u) | ((w[4 * hw + i] >> 24) & 0x80u)) << (8 * i);
+        }
+        code[hw] = c;
+    }
+    return byte;
+}
+
+}  // namespace
+#endif
+
+}  // namespace bgtq
