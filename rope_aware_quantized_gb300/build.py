@@ -35,6 +35,7 @@ SOURCES = [
     ("rope.cu", []),
     ("fp4_append.cu", []),
     ("fp4_attn.cu", []),
+    ("fp4_tiles.cu", []),
     ("decode_attn.cu", []),
     ("decode_attn_paged.cu", []),
     ("decode_attn_noalloc.cu", []),

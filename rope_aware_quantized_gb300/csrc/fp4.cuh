@@ -70,6 +70,9 @@ struct Fp4Attn {
 };
 size_t fp4_attn_workspace_bytes(int H, int group, int batch, int t, int64_t max_len);
 cudaError_t launch_fp4_attn(cudaStream_t s, const Fp4Attn& a);
+// The tiles' part (fp4_tiles.cu); ws behind the counters of the one-pass kernel.
+size_t fp4_tiles_workspace_bytes(int64_t heads, int64_t rows, int64_t max_len);
+cudaError_t launch_fp4_tiles(cudaStream_t s, const Fp4Attn& a, void* ws);
 cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsView& k, const RowsView& v, int batch, int t_new,
                               const int32_t* pos_start, const bgtq_fp4_cache& c, int32_t* status);
 cudaError_t launch_fp4_dequant(cudaStream_t s, const bgtq_fp4_cache& c, int b, int head, int64_t t0, int64_t t1, float* k_out,

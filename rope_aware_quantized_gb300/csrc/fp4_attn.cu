@@ -435,7 +435,7 @@ size_t one_pass_bytes(int64_t heads, int64_t rows, int64_t max_len) {
     const int64_t units = heads * row_blocks(rows);
     const int64_t groups = std::max<int64_t>(1, (max_len + kGroup - 1) / kGroup);
     const int64_t slots = std::min<int64_t>(kMaxSlots, units * ((groups + kWarps - 1) / kWarps));
-    return kCounterBytes + (size_t)slots * 8 * row_tiles(rows) * (8 + 4 * kD);
+    return (size_t)slots * 8 * row_tiles(rows) * (8 + 4 * kD);
 }
 
 template <int NQ>
@@ -469,11 +469,14 @@ cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
 }  // namespace
 
 size_t fp4_attn_workspace_bytes(int H, int group, int batch, int t, int64_t max_len) {
-    return one_pass_bytes((int64_t)batch * H, (int64_t)t * group, max_len);
+    const int64_t heads = (int64_t)batch * H, rows = (int64_t)t * group;
+    const size_t few = one_pass_bytes(heads, std::min<int64_t>(rows, kFp4Rows), max_len);
+    return kCounterBytes + std::max(few, rows > kFp4Rows ? fp4_tiles_workspace_bytes(heads, rows, max_len) : 0);
 }
 
 cudaError_t launch_fp4_attn(cudaStream_t s, const Fp4Attn& a) {
     const int64_t rows = (int64_t)a.t * a.group;
+    if (rows > kFp4Rows) return launch_fp4_tiles(s, a, static_cast<char*>(a.ws) + kCounterBytes);
     const int64_t units = (int64_t)a.batch * a.map.H * row_blocks(rows);
     const Split sp = split_for(units, std::min(a.max_len, a.cap));
     AttnParams p;
