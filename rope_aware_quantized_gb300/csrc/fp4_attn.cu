@@ -5,7 +5,7 @@
 // out = sum_j softmax_j(scale q.k_j) v_j over the positions a row sees; split
 // over the positions, one running maximum and sum per warp, partials joined by
 // log-sum-exp.  A warp takes groups of 16 positions, brought to shared memory
-// by bulk copies of 2304 bytes, kStages in flight a warp:
+// by bulk copies of 2304 bytes, several in flight a warp:
 //   S^T = K Q^T   (16 positions x 8 rows, K 16 dims a step): codes to fp16 by
 //                 the hardware's conversion, times the block's scale, exact;
 //                 the products are fp16 x fp16 in fp32
@@ -32,28 +32,28 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;         // groups in flight a warp
+template <int NQ>
+constexpr int kStagesOf = NQ == 4 ? 3 : 4;  // groups in flight a warp (four row tiles: what shared memory leaves)
 constexpr int kRowPad = 132;       // floats of a row of partial output in shared memory (keeps the warp's stores on 32 banks)
 constexpr float kLift = 8.0f, kRange = 15.0f;
 constexpr float kLow = -1.0e30f;   // "no position yet"
-constexpr int kMaxSlots = 152 * 16;  // partials of all units that a workspace has room for
+constexpr int kUnitCost = 32;      // what a unit's start and end take of a CTA, in groups
 
 struct AttnParams {
     RopeParams rope;
     RowsView q;
     Fp4Map map;
     const int32_t* seq_lens;
-    int64_t cap, max_len;
-    int t, group, H;
-    int row_blocks;   // blocks of 8 NQ rows of a KV head's t * group; a unit is one of them
-    int parts;        // splits of a unit (workspace slots)
-    int part_groups;  // groups of a split
+    int max_len;
+    int batch, t, group, H;
+    int clusters;        // of the launch
+    int least;           // groups that a cluster takes at least
     void* out;
     int out_dtype;
     float scale_log2;
-    uint32_t* counters;
-    float2* part_ml;  // [slot][rows]: (m, l)
-    float* part_o;    // [slot][rows][128]
+    uint32_t* counters;  // [cluster][rank]: arrivals at the unit that is split and begins in that cluster
+    float2* part_ml;     // [cluster][2][R]: (m, l)
+    float* part_o;       // [cluster][2][R][128]
     int32_t* status;
 };
 
@@ -83,11 +83,11 @@ struct State {
     float m[NQ][2], l[NQ][2];
 };
 
-// One group: img in shared memory, base its first position, lim the last
+// One group (`first`: of the warp's in this segment): img in shared memory, base its first position, lim the last
 // position each of the lane's rows sees; kEdge: some position is not seen by
 // every row (past n: its scales do not count).
 template <int NQ, bool kEdge>
-__device__ __forceinline__ void attend(State<NQ>& st, const uint32_t (&q)[8][NQ][2], const uint8_t* img, int base, int n,
+__device__ __forceinline__ void attend(State<NQ>& st, bool first, const uint32_t (&q)[8][NQ][2], const uint8_t* img, int base, int n,
                                        const int (&lim)[NQ][2], float c, int lane) {
     const int g = lane >> 2, cl = lane & 3;
     float s[NQ][4];
@@ -117,16 +117,17 @@ __device__ __forceinline__ void attend(State<NQ>& st, const uint32_t (&q)[8][NQ]
         }
     }
     // logits of positions g (0, 1) and g + 8 (2, 3), rows 2 cl (0, 2) and 2 cl + 1 (1, 3)
-    bool over = false;
+    // (x: above the row's reference)
+    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            s[i][e] *= c;
+            s[i][e] = fmaf(s[i][e], c, -st.m[i][e & 1]);
             if (kEdge && base + g + 8 * (e >> 1) > lim[i][e & 1]) s[i][e] = -INFINITY;
-            over |= s[i][e] > st.m[i][e & 1] + kRange;
+            top = fmaxf(top, s[i][e]);
         }
-    if (__any_sync(0xffffffffu, over)) {
+    if (first || __any_sync(0xffffffffu, top > kRange)) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
 #pragma unroll
@@ -134,9 +135,14 @@ __device__ __forceinline__ void attend(State<NQ>& st, const uint32_t (&q)[8][NQ]
                 float mt = fmaxf(s[i][e], s[i][e + 2]);
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-                if (mt > st.m[i][e] + kRange) {
-                    const float f = ex2(st.m[i][e] - (mt - kLift));  // (0 the first time)
-                    st.m[i][e] = mt - kLift;
+                // (the first group sets the reference: a row that sees nothing of the warp's
+                // lowest positions sees none of its others)
+                if (mt > kRange || (first && mt != -INFINITY)) {
+                    const float up = mt - kLift;
+                    const float f = first ? 1.0f : ex2(-up);
+                    st.m[i][e] += up;
+                    s[i][e] -= up;
+                    s[i][e + 2] -= up;
                     st.l[i][e] *= f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -151,7 +157,7 @@ __device__ __forceinline__ void attend(State<NQ>& st, const uint32_t (&q)[8][NQ]
     for (int i = 0; i < NQ; ++i)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const float p0 = ex2(s[i][2 * x] - st.m[i][0]), p1 = ex2(s[i][2 * x + 1] - st.m[i][1]);
+            const float p0 = ex2(s[i][2 * x]), p1 = ex2(s[i][2 * x + 1]);
             st.l[i][0] += p0;
             st.l[i][1] += p1;
             const __half2 h = __floats2half2_rn(p0, p1);
@@ -188,281 +194,520 @@ __device__ __forceinline__ void attend(State<NQ>& st, const uint32_t (&q)[8][NQ]
 }
 
 template <int NQ>
-constexpr int smem_ring() {
-    return kWarps * kStages * kGroupBytes;
-}
+constexpr int smem_ring = kWarps * kStagesOf<NQ> * kGroupBytes;
 template <int NQ>
-constexpr int smem_merge() {
-    return kWarps * 8 * NQ * kRowPad * 4;
+constexpr int smem_bytes = smem_ring<NQ> + kWarps * 8 * NQ * kRowPad * 4;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
 }
-template <int NQ>
-constexpr int smem_bytes() {
-    return smem_ring<NQ>() > smem_merge<NQ>() ? smem_ring<NQ>() : smem_merge<NQ>();
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
 }
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster_v2(uint32_t a) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(a) : "memory");
+    return v;
+}
+
+// The work is a list of groups, unit (sequence, KV head) after unit, cut into
+// equal ranges, one for each cluster of CTAs.  With few units a range is
+// ceil(groups / (clusters - units)) groups and every unit is padded to whole
+// ranges, so that a cluster has one unit and starts and ends once; with many,
+// a unit is followed by kUnitCost empty places (what its start and end take of
+// a CTA, in groups), and a range may hold several units and parts of two more.
+// A unit in one cluster is finished there; one in several leaves a partial in
+// each (the first or a later unit of the range), which the last cluster to
+// arrive joins.  All of it follows from seq_lens, which every CTA sums up for
+// itself.
+struct Share {
+    int per;    // places of a cluster
+    int total;  // places of all units
+    bool pad;
+    __device__ __forceinline__ int places(int groups) const {
+        return pad ? (groups + per - 1) / per * per : groups + kUnitCost;
+    }
+};
 
 template <int NQ>
 __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int R = 8 * NQ;
+    constexpr int R = 8 * NQ, kStages = kStagesOf<NQ>;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) __half s_q[R][kD + 8];
-    __shared__ float s_m[kWarps][R], s_l[kWarps][R];
+    __shared__ __align__(16) float s_part[R][kD];
+    __shared__ float2 s_part_ml[R], s_ml[kWarps][R];
     __shared__ int s_lim[R];
     __shared__ __align__(8) uint64_t s_bar[kWarps * kStages];
     __shared__ int s_abort, s_last;
+    __shared__ int s_scan[kWarps], s_at[2];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int unit = blockIdx.x, part = blockIdx.y;
-    const int head = unit / p.row_blocks, row0 = (unit - head * p.row_blocks) * R;
-    const int b = head / p.H, h = head - b * p.H;
-    const int rows = min(R, p.t * p.group - row0);  // of this unit
+    const int cs = (int)cluster_size(), rank = (int)cluster_rank();
+    const int k = (int)blockIdx.x / cs;
+    const int rows = p.t * p.group, units = p.batch * p.H;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid < kWarps * kStages) mbar_init(smem_u32(&s_bar[tid]), 1);
     if (tid == 0) s_abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    int64_t n64 = p.seq_lens[b];
-    if (n64 < 0 || n64 > p.max_len) {
-        if (tid == 0 && part == 0 && h == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_SEQLEN_CAPACITY);
-        n64 = n64 < 0 ? 0 : p.max_len;
+    auto seq_len = [&](int b) -> int {
+        const int n = p.seq_lens[b];
+        return min(max(n, 0), p.max_len);
+    };
+    // (a sequence without positions: one group, so that its zeros are written)
+    auto groups_of = [](int n) -> int { return max(1, (n + kGroup - 1) / kGroup); };
+    // ---- the cluster's range: where it begins
+    Share sh;
+    sh.pad = 2 * units <= p.clusters;
+    int b = 0, start = 0, n = 0;  // start: places before sequence b
+    {
+        const int each = (p.batch + kThreads - 1) / kThreads;
+        const int b0 = min(tid * each, p.batch), b1 = min(b0 + each, p.batch);
+        // sum over all sequences, and before this thread's (whole block)
+        auto scan = [&](int mine, int& before) -> int {
+            int run = mine;
+#pragma unroll
+            for (int x = 1; x < 32; x <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, run, x);
+                if (lane >= x) run += o;
+            }
+            if (lane == 31) s_scan[warp] = run;
+            __syncthreads();
+            int all = 0;
+            before = run - mine;
+#pragma unroll
+            for (int x = 0; x < kWarps; ++x) {
+                if (x < warp) before += s_scan[x];
+                all += s_scan[x];
+            }
+            return all;
+        };
+        int sum = 0, before = 0;
+        if (p.batch == 1) {
+            n = seq_len(0);
+            sh.total = groups_of(n) * p.H;
+        } else {
+            for (int x = b0; x < b1; ++x) sum += groups_of(seq_len(x)) * p.H;
+            sh.total = scan(sum, before);
+        }
+        if (sh.pad) {
+            sh.per = max(p.least, (sh.total + p.clusters - units - 1) / (p.clusters - units));
+            if (p.batch == 1) {
+                sh.total = sh.places(groups_of(n)) * p.H;
+            } else {
+                sum = 0;
+                for (int x = b0; x < b1; ++x) sum += sh.places(groups_of(seq_len(x))) * p.H;
+                __syncthreads();
+                sh.total = scan(sum, before);
+            }
+        } else {
+            before += min(b0, p.batch) * p.H * kUnitCost;
+            sum += (b1 - b0) * p.H * kUnitCost;
+            sh.total += units * kUnitCost;
+            sh.per = max(p.least, (sh.total + p.clusters - 1) / p.clusters);
+        }
+        const int lo = k * sh.per;
+        if (p.batch > 1) {
+            if (lo >= before && lo < before + sum) {
+                int at = before, x = b0;
+                for (;; ++x) {
+                    const int g = sh.places(groups_of(seq_len(x))) * p.H;
+                    if (lo < at + g) break;
+                    at += g;
+                }
+                s_at[0] = x;
+                s_at[1] = at;
+            }
+            __syncthreads();
+        }
+        if (lo >= sh.total) return;  // (the whole cluster)
+        if (p.batch > 1) {
+            b = s_at[0];
+            start = s_at[1];
+            n = seq_len(b);
+        }
     }
-    const int n = (int)n64;
-    // groups that the unit's last row sees
-    const int n_groups = (max(0, n - p.t + 1 + (row0 + rows - 1) / p.group) + kGroup - 1) / kGroup;
-    const int active = max(1, (n_groups + p.part_groups - 1) / p.part_groups);  // splits that have positions
-    if (part >= active) return;
+    const int lo = k * sh.per, hi = min(sh.total, lo + sh.per);
+    int h = (lo - start) / sh.places(groups_of(n));
+    start += h * sh.places(groups_of(n));
     __syncthreads();  // barriers initialised
-    const int g0 = part * p.part_groups, g1 = min(n_groups, g0 + p.part_groups);
-    // ---- the warp's first groups
+
     uint8_t* ring = smem + warp * (kStages * kGroupBytes);
+    float* so = reinterpret_cast<float*>(smem + smem_ring<NQ>);
     const uint32_t ring_a = smem_u32(ring), bar_a = smem_u32(&s_bar[warp * kStages]);
     volatile int* abort_flag = &s_abort;
-    auto fetch = [&](int gi, int stage) {
-        const uint8_t* src = p.map.group(b, h, gi);
-        if (!src) {
-            if (p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
-            src = p.map.base;  // (some group of the pool: the output is unspecified)
-        }
-        mbar_expect_tx(bar_a + 8 * stage, kGroupBytes);
-        bulk_copy(ring_a + stage * kGroupBytes, src, kGroupBytes, bar_a + 8 * stage);
-    };
-    if (lane == 0)
-        for (int s = 0; s < kStages; ++s)
-            if (g0 + warp + s * kWarps < g1) fetch(g0 + warp + s * kWarps, s);
-    // ---- the query rows (row r: token r / group, query head h group + r mod group), rotated
-    for (int r = warp; r < R; r += kWarps) {
-        uint2 w = make_uint2(0u, 0u);
-        int lim = n - 1;
-        if (r < rows) {
-            const int i = (row0 + r) / p.group, a = row0 + r - i * p.group;
-            lim = n - p.t + i;
-            const __half* row = static_cast<const __half*>(p.q.p) + b * p.q.sb + (int64_t)(h * p.group + a) * p.q.sh + i * p.q.st;
-            if (p.rope.cos) {
-                int pos[kMaxAxes];
-                if (lim >= 0 && rope_positions(p.rope, (int64_t)b * p.t + i, lim, pos)) {
-                    __half e[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) e[k] = rope_elem(p.rope, pos, row, 4 * lane + k);
-                    w = make_uint2(__half_as_ushort(e[0]) | (uint32_t)__half_as_ushort(e[1]) << 16,
-                                   __half_as_ushort(e[2]) | (uint32_t)__half_as_ushort(e[3]) << 16);
-                } else {
-                    if (lim >= 0 && lane == 0 && part == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_ROPE_RANGE);
-                    lim = -1;
-                }
-            } else {
-                w = *reinterpret_cast<const uint2*>(row + 4 * lane);
-            }
-        }
-        *reinterpret_cast<uint2*>(&s_q[r][4 * lane]) = w;
-        if (lane == 0) s_lim[r] = lim;
-    }
-    __syncthreads();
     const int g = lane >> 2, cl = lane & 3;
-    uint32_t q[8][NQ][2];
-    int lim[NQ][2], lim_min = n - 1;
-    State<NQ> st;
-#pragma unroll
-    for (int i = 0; i < NQ; ++i) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint2 w = *reinterpret_cast<const uint2*>(&s_q[8 * i + g][16 * j + 4 * cl]);
-            q[j][i][0] = w.x;
-            q[j][i][1] = w.y;
-            st.o[j][i][0] = st.o[j][i][1] = st.o[j][i][2] = st.o[j][i][3] = 0.0f;
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            lim[i][e] = s_lim[8 * i + 2 * cl + e];
-            lim_min = min(lim_min, lim[i][e]);
-            st.m[i][e] = kLow;
-            st.l[i][e] = 0.0f;
-        }
-    }
-    lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-    // ---- the groups
     int stage = 0;
     uint32_t parity = 0;
-    for (int gi = g0 + warp; gi < g1; gi += kWarps) {
-        if (!__all_sync(0xffffffffu, mbar_wait(bar_a + 8 * stage, parity, abort_flag, p.status))) {
-            // gave up: the warp's own copies land (or time out once more) before the CTA ends
-            for (int s = 0; s < kStages && gi + s * kWarps < g1; ++s) {
-                mbar_wait(bar_a + 8 * stage, parity, abort_flag, p.status, false);
+    const int step = cs * kWarps;  // warps of the cluster take the groups in turn
+    while (start < hi) {
+        // ---- unit (b, h): its groups [g0, g1) are the cluster's
+        const int unit_groups = groups_of(n), unit_end = start + unit_groups;
+        const int next_start = start + sh.places(unit_groups);
+        const int g0 = max(lo - start, 0), seg_end = min(unit_end, hi) - start, g1 = min(seg_end, (n + kGroup - 1) / kGroup);
+        if (g0 < seg_end) {
+            const int gw = g0 + rank * kWarps + warp;
+            // ---- the query rows (row r: token r / group, query head h group + r mod
+            // group): a warp brings rows warp, warp + 8, ..; a lane 4 elements
+            // and their partners, loads first
+            uint2 qa[NQ], qb[NQ];
+            int q_lim[NQ], q_pos[NQ][kMaxAxes];
+            bool q_ok[NQ];
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int r = warp + kWarps * i;
+                qa[i] = qb[i] = make_uint2(0u, 0u);
+                q_lim[i] = n - 1;
+                q_ok[i] = true;
+                if (r < rows) {
+                    const int x = r / p.group, a = r - x * p.group;
+                    q_lim[i] = n - p.t + x;
+                    const __half* row = static_cast<const __half*>(p.q.p) + b * p.q.sb + (int64_t)(h * p.group + a) * p.q.sh + x * p.q.st;
+                    qa[i] = *reinterpret_cast<const uint2*>(row + 4 * lane);
+                    if (p.rope.cos) {
+                        if (p.rope.layout == 0) qb[i] = *reinterpret_cast<const uint2*>(row + ((4 * lane) ^ 64));
+                        q_ok[i] = rope_positions(p.rope, (int64_t)b * p.t + x, q_lim[i], q_pos[i]);
+                    }
+                }
+            }
+            auto fetch = [&](int gi, int st) {
+                const uint8_t* src = p.map.group(b, h, gi);
+                if (!src) {
+                    if (p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
+                    src = p.map.base;  // (some group of the pool: the output is unspecified)
+                }
+                mbar_expect_tx(bar_a + 8 * st, kGroupBytes);
+                bulk_copy(ring_a + st * kGroupBytes, src, kGroupBytes, bar_a + 8 * st);
+            };
+            if (lane == 0)
+                for (int s = 0, st = stage; s < kStages; ++s) {
+                    if (gw + s * step < g1) fetch(gw + s * step, st);
+                    if (++st == kStages) st = 0;
+                }
+            if (tid == 0 && rank == 0 && h == 0 && g0 == 0 && p.status && n != p.seq_lens[b])
+                atomicOr(p.status, BGTQ_STATUS_SEQLEN_CAPACITY);
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+                const int r = warp + kWarps * i;
+                uint2 w = qa[i];
+                if (p.rope.cos && r < rows) {
+                    if (q_lim[i] >= 0 && q_ok[i]) {
+                        float2 x0 = rope_f2(qa[i].x), x1 = rope_f2(qa[i].y);
+                        float c[4], s[4];
+                        if (p.rope.layout == 0) {
+                            // blocks 4 (lane mod 16) ..: this lane has one dim of each, lane ^ 16 the other
+                            float2 y0 = rope_f2(qb[i].x), y1 = rope_f2(qb[i].y);
+                            rope_load4(p.rope, q_pos[i], 4 * (lane & 15), c, s);
+                            if (lane < 16) {
+                                rope_pair(x0.x, y0.x, c[0], s[0]);
+                                rope_pair(x0.y, y0.y, c[1], s[1]);
+                                rope_pair(x1.x, y1.x, c[2], s[2]);
+                                rope_pair(x1.y, y1.y, c[3], s[3]);
+                            } else {
+                                rope_pair(y0.x, x0.x, c[0], s[0]);
+                                rope_pair(y0.y, x0.y, c[1], s[1]);
+                                rope_pair(y1.x, x1.x, c[2], s[2]);
+                                rope_pair(y1.y, x1.y, c[3], s[3]);
+                            }
+                        } else {
+                            // blocks 2 lane and 2 lane + 1 of the four from 4 (lane / 2)
+                            rope_load4(p.rope, q_pos[i], 4 * (lane >> 1), c, s);
+                            const bool up = lane & 1;
+                            rope_pair(x0.x, x0.y, up ? c[2] : c[0], up ? s[2] : s[0]);
+                            rope_pair(x1.x, x1.y, up ? c[3] : c[1], up ? s[3] : s[1]);
+                        }
+                        w = make_uint2(rope_h2(x0.x, x0.y), rope_h2(x1.x, x1.y));
+                    } else {
+                        if (q_lim[i] >= 0 && lane == 0 && rank == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_ROPE_RANGE);
+                        w = make_uint2(0u, 0u);
+                        q_lim[i] = -1;
+                    }
+                }
+                *reinterpret_cast<uint2*>(&s_q[r][4 * lane]) = w;
+                if (lane == 0) s_lim[r] = q_lim[i];
+            }
+            __syncthreads();
+            uint32_t q[8][NQ][2];
+            int lim[NQ][2], lim_min = n - 1;
+            State<NQ> st;
+#pragma unroll
+            for (int i = 0; i < NQ; ++i) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(&s_q[8 * i + g][16 * j + 4 * cl]);
+                    q[j][i][0] = w.x;
+                    q[j][i][1] = w.y;
+                    st.o[j][i][0] = st.o[j][i][1] = st.o[j][i][2] = st.o[j][i][3] = 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    lim[i][e] = s_lim[8 * i + 2 * cl + e];
+                    lim_min = min(lim_min, lim[i][e]);
+                    st.m[i][e] = 0.0f;
+                    st.l[i][e] = 0.0f;
+                }
+            }
+            lim_min = __reduce_min_sync(0xffffffffu, lim_min);
+            // ---- the groups
+            for (int gi = gw; gi < g1; gi += step) {
+                if (!__all_sync(0xffffffffu, mbar_wait(bar_a + 8 * stage, parity, abort_flag, p.status))) {
+                    // gave up: the warp's own copies land (or time out once more) before the CTA ends
+                    for (int s = 0; s < kStages && gi + s * step < g1; ++s) {
+                        mbar_wait(bar_a + 8 * stage, parity, abort_flag, p.status, false);
+                        if (++stage == kStages) {
+                            stage = 0;
+                            parity ^= 1u;
+                        }
+                    }
+                    break;
+                }
+                const uint8_t* img = ring + stage * kGroupBytes;
+                if (gi * kGroup + kGroup - 1 <= lim_min)
+                    attend<NQ, false>(st, gi == gw, q, img, gi * kGroup, n, lim, p.scale_log2, lane);
+                else
+                    attend<NQ, true>(st, gi == gw, q, img, gi * kGroup, n, lim, p.scale_log2, lane);
+                __syncwarp();
+                if (lane == 0 && gi + kStages * step < g1) fetch(gi + kStages * step, stage);
                 if (++stage == kStages) {
                     stage = 0;
                     parity ^= 1u;
                 }
             }
-            break;
-        }
-        const uint8_t* img = ring + stage * kGroupBytes;
-        if (gi * kGroup + kGroup - 1 <= lim_min)
-            attend<NQ, false>(st, q, img, gi * kGroup, n, lim, p.scale_log2, lane);
-        else
-            attend<NQ, true>(st, q, img, gi * kGroup, n, lim, p.scale_log2, lane);
-        __syncwarp();
-        if (lane == 0 && gi + kStages * kWarps < g1) fetch(gi + kStages * kWarps, stage);
-        if (++stage == kStages) {
-            stage = 0;
-            parity ^= 1u;
-        }
-    }
-    // ---- the CTA's partial: the warps' joined in shared memory
+            // ---- the warps' partials, in shared memory
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
+            for (int i = 0; i < NQ; ++i) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+                for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) st.l[i][e] += __shfl_xor_sync(0xffffffffu, st.l[i][e], x);
-    __syncthreads();  // every warp is done with its ring
-    if (s_abort) return;
-    float* so = reinterpret_cast<float*>(smem);
+                    for (int e = 0; e < 4; ++e)
+                        so[(warp * R + 8 * i + 2 * cl + (e & 1)) * kRowPad + 16 * j + g + 8 * (e >> 1)] = st.o[j][i][e];
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) {
+                for (int e = 0; e < 2; ++e) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                so[(warp * R + 8 * i + 2 * cl + (e & 1)) * kRowPad + 16 * j + g + 8 * (e >> 1)] = st.o[j][i][e];
-        if (g == 0) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                s_m[warp][8 * i + 2 * cl + e] = st.m[i][e];
-                s_l[warp][8 * i + 2 * cl + e] = st.l[i][e];
+                    for (int x = 4; x < 32; x <<= 1) st.l[i][e] += __shfl_xor_sync(0xffffffffu, st.l[i][e], x);
+                    if (g == 0)
+                        s_ml[warp][8 * i + 2 * cl + e] = make_float2(st.l[i][e] == 0.0f ? kLow : st.m[i][e], st.l[i][e]);
+                }
             }
-        }
-    }
-    __syncthreads();
-    auto write_row = [&](int r, float4 o, float l) {
-        const float inv = l > 0.0f ? 1.0f / l : 0.0f;
-        const int i = (row0 + r) / p.group, a = row0 + r - i * p.group;
-        const int64_t at = (((int64_t)b * p.H * p.group + h * p.group + a) * p.t + i) * kD + 4 * lane;
-        if (p.out_dtype)
-            *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        else
-            *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + at) =
-                make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
-    };
-    const int64_t slot0 = (int64_t)unit * p.parts;
-    for (int r = warp; r < rows; r += kWarps) {
-        float m = kLow, l = 0.0f;
+            if (cs > 1)
+                cluster_sync();
+            else
+                __syncthreads();
+            // ---- joined: rank x of the cluster has rows x, x + cs, ..; a warp joins the
+            // partials that one CTA holds of one of them, then (cs > 1) the CTAs'
+            auto write_row = [&](int r, float4 o, float l) {
+                const float inv = l > 0.0f ? 1.0f / l : l != l ? l : 0.0f;
+                const int x = r / p.group, a = r - x * p.group;
+                const int64_t at = (((int64_t)b * p.H * p.group + h * p.group + a) * p.t + x) * kD + 4 * lane;
+                if (p.out_dtype)
+                    *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+                else
+                    *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + at) =
+                        make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
+            };
+            const bool whole = start >= lo && unit_end <= hi;
+            const int64_t slot = 2 * (int64_t)k + (start > lo ? 1 : 0);
+            auto leave = [&](int r, float m, float4 o, float l) {
+                if (whole) {
+                    write_row(r, o, l);
+                } else {
+                    *reinterpret_cast<float4*>(p.part_o + (slot * R + r) * kD + 4 * lane) = o;
+                    if (lane == 0) p.part_ml[slot * R + r] = make_float2(m, l);
+                }
+            };
+            const int mine = (rows - rank + cs - 1) / cs;  // this rank's rows
+            for (int it = warp; it < mine * cs; it += kWarps) {
+                const int r = rank + it / cs * cs, from = it % cs;
+                float2 ml[kWarps];
+                float4 v[kWarps];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][r]);
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int w = 0; w < kWarps; ++w) {
+                    const uint32_t am = smem_u32(&s_ml[w][r]), ao = smem_u32(so + (w * R + r) * kRowPad + 4 * lane);
+                    ml[w] = ld_cluster_v2(cs > 1 ? map_rank(am, from) : am);
+                    v[w] = ld_cluster_v4(cs > 1 ? map_rank(ao, from) : ao);
+                }
+                float m = kLow, l = 0.0f;
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(s_m[w][r] - m);
-            l += f * s_l[w][r];
-            const float4 x = *reinterpret_cast<const float4*>(so + (w * R + r) * kRowPad + 4 * lane);
-            o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
-        }
-        if (active == 1) {
-            write_row(r, o, l);
-        } else {
-            *reinterpret_cast<float4*>(p.part_o + ((slot0 + part) * R + r) * kD + 4 * lane) = o;
-            if (lane == 0) p.part_ml[(slot0 + part) * R + r] = make_float2(m, l);
-        }
-    }
-    if (active == 1) return;
-    // ---- the unit's last CTA joins the partials
-    __threadfence();
-    __syncthreads();
-    if (tid == 0) {
-        const uint32_t before = atomicAdd(p.counters + unit, 1u);
-        s_last = before + 1 == (uint32_t)active;
-        if (s_last) p.counters[unit] = 0;
-    }
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    for (int r = warp; r < rows; r += kWarps) {
-        float m = kLow;
-        for (int x = lane; x < active; x += 32) m = fmaxf(m, __ldcg(&p.part_ml[(slot0 + x) * R + r]).x);
+                for (int w = 0; w < kWarps; ++w) m = fmaxf(m, ml[w].x);
 #pragma unroll
-        for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-        float l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int x = 0; x < active; ++x) {
-            const float2 ml = __ldcg(&p.part_ml[(slot0 + x) * R + r]);
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + ((slot0 + x) * R + r) * kD + 4 * lane));
-            const float f = ex2(ml.x - m);
-            l += f * ml.y;
-            o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = ex2(ml[w].x - m);
+                    l += f * ml[w].y;
+                    o.x += f * v[w].x, o.y += f * v[w].y, o.z += f * v[w].z, o.w += f * v[w].w;
+                }
+                if (cs == 1) {
+                    leave(r, m, o, l);
+                } else {
+                    *reinterpret_cast<float4*>(&s_part[it][4 * lane]) = o;
+                    if (lane == 0) s_part_ml[it] = make_float2(m, l);
+                }
+            }
+            // the `count` partials of row r from s_part[first] on, joined
+            auto join = [&](int first, int count, auto&& done) {
+                float m = kLow, l = 0.0f;
+                for (int x = 0; x < count; ++x) m = fmaxf(m, s_part_ml[first + x].x);
+                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int x = 0; x < count; ++x) {
+                    const float2 ml = s_part_ml[first + x];
+                    const float4 v = *reinterpret_cast<const float4*>(&s_part[first + x][4 * lane]);
+                    const float f = ex2(ml.x - m);
+                    l += f * ml.y;
+                    o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+                }
+                done(m, o, l);
+            };
+            if (cs > 1) {
+                __syncthreads();
+                for (int x = warp; x < mine; x += kWarps)
+                    join(x * cs, cs, [&](float m, float4 o, float l) { leave(rank + x * cs, m, o, l); });
+            }
+            if (!whole) {
+                // ---- the last cluster to arrive joins the unit's partials (a rank its rows)
+                const int k0 = start / sh.per, k1 = (unit_end - 1) / sh.per;
+                __threadfence();
+                __syncthreads();
+                if (tid == 0) {
+                    uint32_t* count = p.counters + k0 * 8 + rank;
+                    s_last = atomicAdd(count, 1u) == (uint32_t)(k1 - k0);
+                    if (s_last) *count = 0;
+                }
+                __syncthreads();
+                if (s_last) {
+                    __threadfence();
+                    // `each` warps a row, every one a share of the clusters
+                    const int each = max(1, kWarps / max(mine, 1));
+                    for (int it = warp; it < mine * each; it += kWarps) {
+                        const int r = rank + it / each * cs;
+                        auto slot_of = [&](int x) { return (2 * (int64_t)x + (start > x * sh.per ? 1 : 0)) * R + r; };
+                        float m = kLow, l = 0.0f;
+                        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        for (int x0 = k0 + it % each; x0 <= k1; x0 += 8 * each) {
+                            float2 ml[8];
+                            float4 v[8];
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) {
+                                const int x = x0 + y * each;
+                                if (x > k1) {
+                                    ml[y] = make_float2(kLow, 0.0f);
+                                    v[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                    continue;
+                                }
+                                ml[y] = __ldcg(&p.part_ml[slot_of(x)]);
+                                v[y] = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot_of(x) * kD + 4 * lane));
+                            }
+                            float top = m;
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) top = fmaxf(top, ml[y].x);
+                            const float f0 = ex2(m - top);
+                            m = top;
+                            l *= f0;
+                            o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+                            for (int y = 0; y < 8; ++y) {
+                                const float f = ex2(ml[y].x - m);
+                                l += f * ml[y].y;
+                                o.x += f * v[y].x, o.y += f * v[y].y, o.z += f * v[y].z, o.w += f * v[y].w;
+                            }
+                        }
+                        if (each == 1) {
+                            write_row(r, o, l);
+                        } else {
+                            *reinterpret_cast<float4*>(&s_part[it][4 * lane]) = o;
+                            if (lane == 0) s_part_ml[it] = make_float2(m, l);
+                        }
+                    }
+                    if (each > 1) {
+                        __syncthreads();
+                        for (int x = warp; x < mine; x += kWarps)
+                            join(x * each, each, [&](float, float4 o, float l) { write_row(rank + x * cs, o, l); });
+                    }
+                }
+            }
+            if (cs > 1)
+                cluster_sync();  // what other ranks read of this CTA is free, and nobody leaves before
+            else
+                __syncthreads();  // s_q, the merge area and s_last are free again
         }
-        write_row(r, o, l);
+        // ---- the next unit
+        start = next_start;
+        if (start < hi && ++h == p.H) {
+            h = 0;
+            n = seq_len(++b);
+        }
     }
-}
-
-// How a unit's positions are split.
-struct Split {
-    int parts, part_groups;
-};
-Split split_for(int64_t units, int64_t max_len) {
-    const int64_t groups = std::max<int64_t>(1, (max_len + kGroup - 1) / kGroup);
-    // one wave of two CTAs a SM where the units are few; about eight splits'
-    // worth of CTAs a SM slot, of ragged sequences, where they are many
-    const int64_t want = units < 152 ? std::max<int64_t>(1, 2 * 152 / units) : std::max<int64_t>(1, kMaxSlots / units);
-    int64_t per = (groups + want - 1) / want;
-    per = std::max<int64_t>(per, units < 152 ? kWarps : 8 * kWarps);
-    per = (per + kWarps - 1) / kWarps * kWarps;
-    return {(int)((groups + per - 1) / per), (int)per};
 }
 
 int row_tiles(int64_t rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
-int64_t row_blocks(int64_t rows) { return (rows + 31) / 32; }
 
-constexpr size_t kCounterBytes = (size_t)kMaxSlots * 4;  // a unit that is split has two slots at least
+constexpr int kMaxClusters = 2 * 152;  // two CTAs a SM, no clusters
+constexpr size_t kCounterBytes = (size_t)kMaxClusters * 8 * 4;
 
-size_t one_pass_bytes(int64_t heads, int64_t rows, int64_t max_len) {
-    const int64_t units = heads * row_blocks(rows);
-    const int64_t groups = std::max<int64_t>(1, (max_len + kGroup - 1) / kGroup);
-    const int64_t slots = std::min<int64_t>(kMaxSlots, units * ((groups + kWarps - 1) / kWarps));
-    return (size_t)slots * 8 * row_tiles(rows) * (8 + 4 * kD);
-}
+size_t one_pass_bytes(int64_t rows) { return (size_t)2 * kMaxClusters * 8 * row_tiles(rows) * (8 + 4 * kD); }
+
+// CTAs of a cluster: few units are cut into many partials, and clusters join
+// them on the chip; many units fill the GPU with CTAs of their own.
+int cluster_for(int64_t units) { return units <= 16 ? 8 : units <= 64 ? 4 : units < 152 ? 2 : 1; }
 
 template <int NQ>
 cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
     static std::mutex mu;
-    static bool done[64] = {false};
+    static int resident[64][4] = {};  // clusters of 1, 2, 4, 8 CTAs that the GPU holds at once
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    const int cs = cluster_for(units), at = cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem_bytes<NQ>;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     {
         std::lock_guard<std::mutex> lock(mu);
-        if (!done[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(fp4_attn_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NQ>());
+        if (!resident[dev][at]) {
+            cudaError_t e = cudaFuncSetAttribute(fp4_attn_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NQ>);
             if (e != cudaSuccess) return e;
-            done[dev] = true;
+            int n = 0;
+            cudaLaunchConfig_t probe = cfg;
+            cudaLaunchAttribute only = attr[1];
+            probe.gridDim = dim3((unsigned)cs, 1, 1);
+            probe.attrs = &only;
+            probe.numAttrs = 1;
+            e = cudaOccupancyMaxActiveClusters(&n, fp4_attn_kernel<NQ>, &probe);
+            if (e != cudaSuccess) return e;
+            if (n < 1) return cudaErrorInvalidConfiguration;
+            resident[dev][at] = std::min(n, kMaxClusters / cs);
         }
+        p.clusters = resident[dev][at];
     }
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)units, (unsigned)p.parts, 1);
-    cfg.blockDim = dim3(kThreads, 1, 1);
-    cfg.dynamicSmemBytes = smem_bytes<NQ>();
-    cfg.stream = s;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
+    p.least = 2 * cs * kWarps;
+    // (a unit more than the places need: the padded split counts on it)
+    const int64_t most = units * std::max<int64_t>(1, (p.max_len + kGroup - 1) / kGroup);
+    p.clusters = (int)std::min<int64_t>(p.clusters, (most + p.least - 1) / p.least + units);
+    cfg.gridDim = dim3((unsigned)(p.clusters * cs), 1, 1);
     return cudaLaunchKernelEx(&cfg, fp4_attn_kernel<NQ>, p);
 }
 
@@ -470,38 +715,33 @@ cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
 
 size_t fp4_attn_workspace_bytes(int H, int group, int batch, int t, int64_t max_len) {
     const int64_t heads = (int64_t)batch * H, rows = (int64_t)t * group;
-    const size_t few = one_pass_bytes(heads, std::min<int64_t>(rows, kFp4Rows), max_len);
+    const size_t few = one_pass_bytes(std::min<int64_t>(rows, kFp4Rows));
     return kCounterBytes + std::max(few, rows > kFp4Rows ? fp4_tiles_workspace_bytes(heads, rows, max_len) : 0);
 }
 
 cudaError_t launch_fp4_attn(cudaStream_t s, const Fp4Attn& a) {
     const int64_t rows = (int64_t)a.t * a.group;
     if (rows > kFp4Rows) return launch_fp4_tiles(s, a, static_cast<char*>(a.ws) + kCounterBytes);
-    const int64_t units = (int64_t)a.batch * a.map.H * row_blocks(rows);
-    const Split sp = split_for(units, std::min(a.max_len, a.cap));
     AttnParams p;
     p.rope = a.rope;
     p.q = a.q;
     p.map = a.map;
     p.seq_lens = a.seq_lens;
-    p.cap = a.cap;
-    p.max_len = std::min(a.max_len, a.cap);
+    p.max_len = (int)std::min(a.max_len, a.cap);
+    p.batch = a.batch;
     p.t = a.t;
     p.group = a.group;
     p.H = a.map.H;
-    p.parts = sp.parts;
-    p.part_groups = sp.part_groups;
     p.out = a.out;
     p.out_dtype = a.out_dtype;
     p.scale_log2 = a.scale * 1.4426950408889634f;
     p.status = a.status;
-    p.row_blocks = (int)row_blocks(rows);
     const int nq = row_tiles(rows);
     char* ws = static_cast<char*>(a.ws);
-    const int64_t slots = std::min<int64_t>(kMaxSlots, units * sp.parts);
     p.counters = reinterpret_cast<uint32_t*>(ws);
     p.part_o = reinterpret_cast<float*>(ws + kCounterBytes);
-    p.part_ml = reinterpret_cast<float2*>(ws + kCounterBytes + (size_t)slots * 8 * nq * 4 * kD);
+    p.part_ml = reinterpret_cast<float2*>(ws + kCounterBytes + (size_t)2 * kMaxClusters * 8 * nq * 4 * kD);
+    const int64_t units = (int64_t)a.batch * a.map.H;
     switch (nq) {
         case 1: return launch_one_pass<1>(s, p, units);
         case 2: return launch_one_pass<2>(s, p, units);
