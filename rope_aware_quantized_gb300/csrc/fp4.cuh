@@ -84,7 +84,7 @@ namespace {
 // Two neighbouring scale bytes (of `w`, at bytes lo and lo + 1) as two fp16.
 template <int kLo>
 __device__ __forceinline__ __half2 fp4_scales(uint32_t w) {
-    const uint32_t u = __byte_perm(w, 0u, kLo == 0 ? 0x1404 : 0x3424) >> 1;
+    const uint32_t u = __byte_perm(w, 0u, kLo == 0 ? 0x4140 : 0x4342) << 7;
     return *reinterpret_cast<const __half2*>(&u);
 }
 

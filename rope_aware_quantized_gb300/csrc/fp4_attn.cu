@@ -4,8 +4,8 @@
 //
 // out = sum_j softmax_j(scale q.k_j) v_j over the positions a row sees; split
 // over the positions, one running maximum and sum per warp, partials joined by
-// log-sum-exp.  A warp takes groups of 16 positions, brought to shared memory
-// by bulk copies of 2304 bytes, several in flight a warp:
+// log-sum-exp.  A warp takes pairs of groups (32 positions), brought to shared
+// memory by bulk copies, kStages pairs in flight a warp.  Of each group:
 //   S^T = K Q^T   (16 positions x 8 rows, K 16 dims a step): codes to fp16 by
 //                 the hardware's conversion, times the block's scale, exact;
 //                 the products are fp16 x fp16 in fp32
@@ -16,6 +16,8 @@
 // group is read with eight conflict-free loads a lane.  mma.sync, not tcgen05:
 // 8 to 32 rows a head leave a 128-row tile idle, and its operands would have
 // to pass through shared memory once more, decoded (4.5 -> 16 bits a value).
+// Two groups at a time: their chains of products and exponentials run side by
+// side, and the wait, the reference's check and the loop are paid once.
 // The reference m of a row's exponentials stays kLift below the largest logit
 // when set and moves only when a logit passes it by kRange, so that the two
 // parts keep 22 bits well above fp16's smallest numbers.
@@ -32,12 +34,12 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-template <int NQ>
-constexpr int kStagesOf = NQ == 4 ? 3 : 4;  // groups in flight a warp (four row tiles: what shared memory leaves)
+constexpr int kStages = 3;         // pairs of groups in flight a warp
 constexpr int kRowPad = 132;       // floats of a row of partial output in shared memory (keeps the warp's stores on 32 banks)
 constexpr float kLift = 8.0f, kRange = 15.0f;
 constexpr float kLow = -1.0e30f;   // "no position yet"
-constexpr int kUnitCost = 32;      // what a unit's start and end take of a CTA, in groups
+constexpr int kPair = 2 * kGroup, kPairBytes = 2 * kGroupBytes;
+constexpr int kUnitCost = 16;      // what a unit's start and end take of a CTA, in pairs of groups
 
 struct AttnParams {
     RopeParams rope;
@@ -47,7 +49,7 @@ struct AttnParams {
     int max_len;
     int batch, t, group, H;
     int clusters;        // of the launch
-    int least;           // groups that a cluster takes at least
+    int least;           // pairs that a cluster takes at least
     void* out;
     int out_dtype;
     float scale_log2;
@@ -83,21 +85,45 @@ struct State {
     float m[NQ][2], l[NQ][2];
 };
 
-// One group (`first`: of the warp's in this segment): img in shared memory, base its first position, lim the last
-// position each of the lane's rows sees; kEdge: some position is not seen by
-// every row (past n: its scales do not count).
+// The query's B operand: in registers, or (more row tiles, whose accumulators
+// need them) read again from shared memory, conflict-free by the rows' padding.
+constexpr int kQPad = 16;
+template <int NQ>
+struct Query {
+    const __half* at;
+    __device__ __forceinline__ void load(const __half (*rows)[kD + kQPad], int lane) { at = &rows[lane >> 2][4 * (lane & 3)]; }
+    __device__ __forceinline__ uint2 get(int j, int i) const { return *reinterpret_cast<const uint2*>(at + 8 * i * (kD + kQPad) + 16 * j); }
+};
+template <>
+struct Query<1> {
+    uint2 w[8];
+    __device__ __forceinline__ void load(const __half (*rows)[kD + kQPad], int lane) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = *reinterpret_cast<const uint2*>(&rows[lane >> 2][16 * j + 4 * (lane & 3)]);
+    }
+    __device__ __forceinline__ uint2 get(int j, int) const { return w[j]; }
+};
+
+// A pair of groups (`first`: of the warp's in this segment): img in shared
+// memory, base its first position, lim the last position each of the lane's
+// rows sees; kEdge: some position is not seen by every row (from n on: its
+// bytes do not count).
 template <int NQ, bool kEdge>
-__device__ __forceinline__ void attend(State<NQ>& st, bool first, const uint32_t (&q)[8][NQ][2], const uint8_t* img, int base, int n,
+__device__ __forceinline__ void attend(State<NQ>& st, bool first, const Query<NQ>& q, const uint8_t* img, int base, int n,
                                        const int (&lim)[NQ][2], float c, int lane) {
     const int g = lane >> 2, cl = lane & 3;
-    float s[NQ][4];
+    float s[2][NQ][4];
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.0f;
-    {
-        const uint4 ka = *reinterpret_cast<const uint4*>(img + 64 * g + 16 * cl);
-        const uint4 kb = *reinterpret_cast<const uint4*>(img + 64 * (g + 8) + 16 * cl);
-        const uint2 sa = *reinterpret_cast<const uint2*>(img + kGroupKs + 8 * g);
-        const uint2 sb = *reinterpret_cast<const uint2*>(img + kGroupKs + 8 * (g + 8));
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int i = 0; i < NQ; ++i) s[x][i][0] = s[x][i][1] = s[x][i][2] = s[x][i][3] = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const uint8_t* at = img + x * kGroupBytes;
+        const uint4 ka = *reinterpret_cast<const uint4*>(at + 64 * g + 16 * cl);
+        const uint4 kb = *reinterpret_cast<const uint4*>(at + 64 * (g + 8) + 16 * cl);
+        const uint2 sa = *reinterpret_cast<const uint2*>(at + kGroupKs + 8 * g);
+        const uint2 sb = *reinterpret_cast<const uint2*>(at + kGroupKs + 8 * (g + 8));
         const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
         for (int jj = 0; jj < 4; ++jj) {
@@ -112,37 +138,44 @@ __device__ __forceinline__ void attend(State<NQ>& st, bool first, const uint32_t
                 const uint32_t a0 = h2u(__hmul2(xa[2 * k], ma)), a1 = h2u(__hmul2(xb[2 * k], mb));
                 const uint32_t a2 = h2u(__hmul2(xa[2 * k + 1], ma)), a3 = h2u(__hmul2(xb[2 * k + 1], mb));
 #pragma unroll
-                for (int i = 0; i < NQ; ++i) mma16816(s[i], a0, a1, a2, a3, q[2 * jj + k][i][0], q[2 * jj + k][i][1]);
+                for (int i = 0; i < NQ; ++i) {
+                    const uint2 w = q.get(2 * jj + k, i);
+                    mma16816(s[x][i], a0, a1, a2, a3, w.x, w.y);
+                }
             }
         }
     }
-    // logits of positions g (0, 1) and g + 8 (2, 3), rows 2 cl (0, 2) and 2 cl + 1 (1, 3)
-    // (x: above the row's reference)
+    // logits above the row's reference: positions g (0, 1) and g + 8 (2, 3), rows 2 cl (0, 2) and 2 cl + 1 (1, 3)
     float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            s[i][e] = fmaf(s[i][e], c, -st.m[i][e & 1]);
-            if (kEdge && base + g + 8 * (e >> 1) > lim[i][e & 1]) s[i][e] = -INFINITY;
-            top = fmaxf(top, s[i][e]);
-        }
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[x][i][e] = fmaf(s[x][i][e], c, -st.m[i][e & 1]);
+                if (kEdge && base + kGroup * x + g + 8 * (e >> 1) > lim[i][e & 1]) s[x][i][e] = -INFINITY;
+                top = fmaxf(top, s[x][i][e]);
+            }
     if (first || __any_sync(0xffffffffu, top > kRange)) {
 #pragma unroll
         for (int i = 0; i < NQ; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float mt = fmaxf(s[i][e], s[i][e + 2]);
+                float mt = fmaxf(fmaxf(s[0][i][e], s[0][i][e + 2]), fmaxf(s[1][i][e], s[1][i][e + 2]));
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-                // (the first group sets the reference: a row that sees nothing of the warp's
+                // (the first pair sets the reference: a row that sees nothing of the warp's
                 // lowest positions sees none of its others)
                 if (mt > kRange || (first && mt != -INFINITY)) {
                     const float up = mt - kLift;
                     const float f = first ? 1.0f : ex2(-up);
                     st.m[i][e] += up;
-                    s[i][e] -= up;
-                    s[i][e + 2] -= up;
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        s[x][i][e] -= up;
+                        s[x][i][e + 2] -= up;
+                    }
                     st.l[i][e] *= f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
@@ -152,51 +185,60 @@ __device__ __forceinline__ void attend(State<NQ>& st, bool first, const uint32_t
                 }
             }
     }
-    uint32_t hi[NQ][2], lo[NQ][2];
+    uint32_t hi[2][NQ][2], lo[2][NQ][2];
 #pragma unroll
-    for (int i = 0; i < NQ; ++i)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const float p0 = ex2(s[i][2 * x]), p1 = ex2(s[i][2 * x + 1]);
-            st.l[i][0] += p0;
-            st.l[i][1] += p1;
-            const __half2 h = __floats2half2_rn(p0, p1);
-            const float2 b = __half22float2(h);
-            hi[i][x] = transpose8(h2u(h));
-            lo[i][x] = transpose8(h2u(__floats2half2_rn(p0 - b.x, p1 - b.y)));
+        for (int i = 0; i < NQ; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                const float p0 = ex2(s[x][i][2 * y]), p1 = ex2(s[x][i][2 * y + 1]);
+                st.l[i][0] += p0;
+                st.l[i][1] += p1;
+                const __half2 h = __floats2half2_rn(p0, p1);
+                const float2 b = __half22float2(h);
+                hi[x][i][y] = transpose8(h2u(h));
+                lo[x][i][y] = transpose8(h2u(__floats2half2_rn(p0 - b.x, p1 - b.y)));
+            }
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const uint8_t* at = img + x * kGroupBytes;
+        uint32_t dead = 0xffffffffu;  // scale bytes of positions past the sequence: their bits do not count
+        if (kEdge) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (base + kGroup * x + 2 * cl + (e & 1) + 8 * (e >> 1) >= n) dead &= ~(0xffu << (8 * e));
         }
-    uint32_t dead = 0xffffffffu;  // scale bytes of positions past the sequence: their bits do not count
-    if (kEdge) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (base + 2 * cl + (e & 1) + 8 * (e >> 1) >= n) dead &= ~(0xffu << (8 * e));
-    }
+        for (int jj = 0; jj < 2; ++jj) {
+            const uint4 v = *reinterpret_cast<const uint4*>(at + kGroupV + 512 * jj + 16 * lane);
+            const uint4 t = *reinterpret_cast<const uint4*>(at + kGroupVs + 32 * cl + 16 * jj);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w}, sc[4] = {t.x, t.y, t.z, t.w};
 #pragma unroll
-    for (int jj = 0; jj < 2; ++jj) {
-        const uint4 v = *reinterpret_cast<const uint4*>(img + kGroupV + 512 * jj + 16 * lane);
-        const uint4 t = *reinterpret_cast<const uint4*>(img + kGroupVs + 32 * cl + 16 * jj);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w}, sc[4] = {t.x, t.y, t.z, t.w};
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t u = kEdge ? sc[k] & dead : sc[k];
+                const __half2 f0 = fp4_scales<0>(u), f1 = fp4_scales<2>(u);
+                __half2 y[4];
+                fp4_numbers(w[k], y);
+                const uint32_t a0 = h2u(__hmul2(y[0], f0)), a1 = h2u(__hmul2(y[1], f0));
+                const uint32_t a2 = h2u(__hmul2(y[2], f1)), a3 = h2u(__hmul2(y[3], f1));
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t u = kEdge ? sc[k] & dead : sc[k];
-            const __half2 f0 = fp4_scales<0>(u), f1 = fp4_scales<2>(u);
-            __half2 x[4];
-            fp4_numbers(w[k], x);
-            const uint32_t a0 = h2u(__hmul2(x[0], f0)), a1 = h2u(__hmul2(x[1], f0));
-            const uint32_t a2 = h2u(__hmul2(x[2], f1)), a3 = h2u(__hmul2(x[3], f1));
-#pragma unroll
-            for (int i = 0; i < NQ; ++i) {
-                mma16816(st.o[4 * jj + k][i], a0, a1, a2, a3, hi[i][0], hi[i][1]);
-                mma16816(st.o[4 * jj + k][i], a0, a1, a2, a3, lo[i][0], lo[i][1]);
+                for (int i = 0; i < NQ; ++i) {
+                    mma16816(st.o[4 * jj + k][i], a0, a1, a2, a3, hi[x][i][0], hi[x][i][1]);
+                    mma16816(st.o[4 * jj + k][i], a0, a1, a2, a3, lo[x][i][0], lo[x][i][1]);
+                }
             }
         }
     }
 }
 
+// The copies' ring and, once a segment's copies are used up, the partials: the
+// warps' (kWarps x R padded rows), then those joined once (R rows).
+constexpr int kRingBytes = kWarps * kStages * kPairBytes;
 template <int NQ>
-constexpr int smem_ring = kWarps * kStagesOf<NQ> * kGroupBytes;
+constexpr int partial_bytes = 8 * NQ * (kWarps * kRowPad + kD) * 4;
 template <int NQ>
-constexpr int smem_bytes = smem_ring<NQ> + kWarps * 8 * NQ * kRowPad * 4;
+constexpr int smem_bytes = kRingBytes > partial_bytes<NQ> ? kRingBytes : partial_bytes<NQ>;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
     uint32_t r;
@@ -227,31 +269,31 @@ __device__ __forceinline__ float2 ld_cluster_v2(uint32_t a) {
     return v;
 }
 
-// The work is a list of groups, unit (sequence, KV head) after unit, cut into
+// The work is a list of pairs of groups, unit (sequence, KV head) after unit, cut into
 // equal ranges, one for each cluster of CTAs.  With few units a range is
-// ceil(groups / (clusters - units)) groups and every unit is padded to whole
+// ceil(pairs / (clusters - units)) pairs and every unit is padded to whole
 // ranges, so that a cluster has one unit and starts and ends once; with many,
 // a unit is followed by kUnitCost empty places (what its start and end take of
-// a CTA, in groups), and a range may hold several units and parts of two more.
+// a CTA), and a range may hold several units and parts of two more.
 // A unit in one cluster is finished there; one in several leaves a partial in
 // each (the first or a later unit of the range), which the last cluster to
 // arrive joins.  All of it follows from seq_lens, which every CTA sums up for
 // itself.
+constexpr int kTwoCtas = 1;  // row tiles up to which two CTAs share a SM (128 registers a thread)
 struct Share {
     int per;    // places of a cluster
     int total;  // places of all units
     bool pad;
-    __device__ __forceinline__ int places(int groups) const {
-        return pad ? (groups + per - 1) / per * per : groups + kUnitCost;
+    __device__ __forceinline__ int places(int pairs) const {
+        return pad ? (pairs + per - 1) / per * per : pairs + kUnitCost;
     }
 };
 
 template <int NQ>
-__global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int R = 8 * NQ, kStages = kStagesOf<NQ>;
+__global__ void __launch_bounds__(kThreads, NQ <= kTwoCtas ? 2 : 1) fp4_attn_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int R = 8 * NQ;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(16) __half s_q[R][kD + 8];
-    __shared__ __align__(16) float s_part[R][kD];
+    __shared__ __align__(16) __half s_q[R][kD + kQPad];
     __shared__ float2 s_part_ml[R], s_ml[kWarps][R];
     __shared__ int s_lim[R];
     __shared__ __align__(8) uint64_t s_bar[kWarps * kStages];
@@ -270,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
         const int n = p.seq_lens[b];
         return min(max(n, 0), p.max_len);
     };
-    // (a sequence without positions: one group, so that its zeros are written)
-    auto groups_of = [](int n) -> int { return max(1, (n + kGroup - 1) / kGroup); };
+    // (a sequence without positions: one pair, so that its zeros are written)
+    auto pairs_of = [](int n) -> int { return max(1, (n + kPair - 1) / kPair); };
     // ---- the cluster's range: where it begins
     Share sh;
     sh.pad = 2 * units <= p.clusters;
@@ -301,18 +343,18 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
         int sum = 0, before = 0;
         if (p.batch == 1) {
             n = seq_len(0);
-            sh.total = groups_of(n) * p.H;
+            sh.total = pairs_of(n) * p.H;
         } else {
-            for (int x = b0; x < b1; ++x) sum += groups_of(seq_len(x)) * p.H;
+            for (int x = b0; x < b1; ++x) sum += pairs_of(seq_len(x)) * p.H;
             sh.total = scan(sum, before);
         }
         if (sh.pad) {
             sh.per = max(p.least, (sh.total + p.clusters - units - 1) / (p.clusters - units));
             if (p.batch == 1) {
-                sh.total = sh.places(groups_of(n)) * p.H;
+                sh.total = sh.places(pairs_of(n)) * p.H;
             } else {
                 sum = 0;
-                for (int x = b0; x < b1; ++x) sum += sh.places(groups_of(seq_len(x))) * p.H;
+                for (int x = b0; x < b1; ++x) sum += sh.places(pairs_of(seq_len(x))) * p.H;
                 __syncthreads();
                 sh.total = scan(sum, before);
             }
@@ -327,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
             if (lo >= before && lo < before + sum) {
                 int at = before, x = b0;
                 for (;; ++x) {
-                    const int g = sh.places(groups_of(seq_len(x))) * p.H;
+                    const int g = sh.places(pairs_of(seq_len(x))) * p.H;
                     if (lo < at + g) break;
                     at += g;
                 }
@@ -344,23 +386,24 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
         }
     }
     const int lo = k * sh.per, hi = min(sh.total, lo + sh.per);
-    int h = (lo - start) / sh.places(groups_of(n));
-    start += h * sh.places(groups_of(n));
+    int h = (lo - start) / sh.places(pairs_of(n));
+    start += h * sh.places(pairs_of(n));
     __syncthreads();  // barriers initialised
 
-    uint8_t* ring = smem + warp * (kStages * kGroupBytes);
-    float* so = reinterpret_cast<float*>(smem + smem_ring<NQ>);
+    uint8_t* ring = smem + warp * (kStages * kPairBytes);
+    float* so = reinterpret_cast<float*>(smem);
+    float(*s_part)[kD] = reinterpret_cast<float(*)[kD]>(smem + kWarps * R * kRowPad * 4);
     const uint32_t ring_a = smem_u32(ring), bar_a = smem_u32(&s_bar[warp * kStages]);
     volatile int* abort_flag = &s_abort;
     const int g = lane >> 2, cl = lane & 3;
     int stage = 0;
     uint32_t parity = 0;
-    const int step = cs * kWarps;  // warps of the cluster take the groups in turn
+    const int step = cs * kWarps;  // warps of the cluster take the pairs in turn
     while (start < hi) {
-        // ---- unit (b, h): its groups [g0, g1) are the cluster's
-        const int unit_groups = groups_of(n), unit_end = start + unit_groups;
-        const int next_start = start + sh.places(unit_groups);
-        const int g0 = max(lo - start, 0), seg_end = min(unit_end, hi) - start, g1 = min(seg_end, (n + kGroup - 1) / kGroup);
+        // ---- unit (b, h): its pairs [g0, g1) are the cluster's
+        const int unit_pairs = pairs_of(n), unit_end = start + unit_pairs;
+        const int next_start = start + sh.places(unit_pairs);
+        const int g0 = max(lo - start, 0), seg_end = min(unit_end, hi) - start, g1 = min(seg_end, (n + kPair - 1) / kPair);
         if (g0 < seg_end) {
             const int gw = g0 + rank * kWarps + warp;
             // ---- the query rows (row r: token r / group, query head h group + r mod
@@ -386,20 +429,29 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
                     }
                 }
             }
+            // a pair's groups lie side by side, but for pages of one group and the last
+            // group of an odd number
             auto fetch = [&](int gi, int st) {
-                const uint8_t* src = p.map.group(b, h, gi);
-                if (!src) {
-                    if (p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
-                    src = p.map.base;  // (some group of the pool: the output is unspecified)
+                const bool both = 2 * gi + 1 < (n + kGroup - 1) / kGroup;
+                const bool one_copy = both && (!p.map.page_table || p.map.lg > 0);
+                mbar_expect_tx(bar_a + 8 * st, both ? kPairBytes : kGroupBytes);
+                for (int x = 0; x < (both && !one_copy ? 2 : 1); ++x) {
+                    const uint8_t* src = p.map.group(b, h, 2 * gi + x);
+                    uint32_t bytes = one_copy ? kPairBytes : kGroupBytes;
+                    if (!src) {
+                        if (p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
+                        src = p.map.base;  // (the pool's first groups: the output is unspecified)
+                    }
+                    bulk_copy(ring_a + st * kPairBytes + x * kGroupBytes, src, bytes, bar_a + 8 * st);
                 }
-                mbar_expect_tx(bar_a + 8 * st, kGroupBytes);
-                bulk_copy(ring_a + st * kGroupBytes, src, kGroupBytes, bar_a + 8 * st);
             };
-            if (lane == 0)
-                for (int s = 0, st = stage; s < kStages; ++s) {
-                    if (gw + s * step < g1) fetch(gw + s * step, st);
-                    if (++st == kStages) st = 0;
-                }
+            auto fetch_first = [&](int s0, int s1) {
+                for (int s = s0; s < s1; ++s)
+                    if (gw + s * step < g1) fetch(gw + s * step, (stage + s) % kStages);
+            };
+            // (one stage a warp before the query's cos and sin, the others after: those
+            // small loads would queue behind all the warps' copies)
+            if (lane == 0) fetch_first(0, 1);
             if (tid == 0 && rank == 0 && h == 0 && g0 == 0 && p.status && n != p.seq_lens[b])
                 atomicOr(p.status, BGTQ_STATUS_SEQLEN_CAPACITY);
 #pragma unroll
@@ -442,19 +494,16 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
                 *reinterpret_cast<uint2*>(&s_q[r][4 * lane]) = w;
                 if (lane == 0) s_lim[r] = q_lim[i];
             }
+            if (lane == 0) fetch_first(1, kStages);
             __syncthreads();
-            uint32_t q[8][NQ][2];
+            Query<NQ> q;
+            q.load(s_q, lane);
             int lim[NQ][2], lim_min = n - 1;
             State<NQ> st;
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(&s_q[8 * i + g][16 * j + 4 * cl]);
-                    q[j][i][0] = w.x;
-                    q[j][i][1] = w.y;
-                    st.o[j][i][0] = st.o[j][i][1] = st.o[j][i][2] = st.o[j][i][3] = 0.0f;
-                }
+                for (int j = 0; j < 8; ++j) st.o[j][i][0] = st.o[j][i][1] = st.o[j][i][2] = st.o[j][i][3] = 0.0f;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     lim[i][e] = s_lim[8 * i + 2 * cl + e];
@@ -464,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
                 }
             }
             lim_min = __reduce_min_sync(0xffffffffu, lim_min);
-            // ---- the groups
+            // ---- the pairs
             for (int gi = gw; gi < g1; gi += step) {
                 if (!__all_sync(0xffffffffu, mbar_wait(bar_a + 8 * stage, parity, abort_flag, p.status))) {
                     // gave up: the warp's own copies land (or time out once more) before the CTA ends
@@ -477,11 +526,11 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
                     }
                     break;
                 }
-                const uint8_t* img = ring + stage * kGroupBytes;
-                if (gi * kGroup + kGroup - 1 <= lim_min)
-                    attend<NQ, false>(st, gi == gw, q, img, gi * kGroup, n, lim, p.scale_log2, lane);
+                const uint8_t* img = ring + stage * kPairBytes;
+                if (gi * kPair + kPair - 1 <= lim_min)
+                    attend<NQ, false>(st, gi == gw, q, img, gi * kPair, n, lim, p.scale_log2, lane);
                 else
-                    attend<NQ, true>(st, gi == gw, q, img, gi * kGroup, n, lim, p.scale_log2, lane);
+                    attend<NQ, true>(st, gi == gw, q, img, gi * kPair, n, lim, p.scale_log2, lane);
                 __syncwarp();
                 if (lane == 0 && gi + kStages * step < g1) fetch(gi + kStages * step, stage);
                 if (++stage == kStages) {
@@ -489,7 +538,8 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
                     parity ^= 1u;
                 }
             }
-            // ---- the warps' partials, in shared memory
+            // ---- the warps' partials, in shared memory (every copy has been used)
+            __syncthreads();
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
 #pragma unroll
@@ -511,10 +561,10 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
                 __syncthreads();
             // ---- joined: rank x of the cluster has rows x, x + cs, ..; a warp joins the
             // partials that one CTA holds of one of them, then (cs > 1) the CTAs'
-            auto write_row = [&](int r, float4 o, float l) {
+            auto write_row = [&](int r, int d, float4 o, float l) {
                 const float inv = l > 0.0f ? 1.0f / l : l != l ? l : 0.0f;
                 const int x = r / p.group, a = r - x * p.group;
-                const int64_t at = (((int64_t)b * p.H * p.group + h * p.group + a) * p.t + x) * kD + 4 * lane;
+                const int64_t at = (((int64_t)b * p.H * p.group + h * p.group + a) * p.t + x) * kD + d;
                 if (p.out_dtype)
                     *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
                 else
@@ -523,12 +573,12 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
             };
             const bool whole = start >= lo && unit_end <= hi;
             const int64_t slot = 2 * (int64_t)k + (start > lo ? 1 : 0);
-            auto leave = [&](int r, float m, float4 o, float l) {
+            auto leave = [&](int r, int d, float m, float4 o, float l) {
                 if (whole) {
-                    write_row(r, o, l);
+                    write_row(r, d, o, l);
                 } else {
-                    *reinterpret_cast<float4*>(p.part_o + (slot * R + r) * kD + 4 * lane) = o;
-                    if (lane == 0) p.part_ml[slot * R + r] = make_float2(m, l);
+                    *reinterpret_cast<float4*>(p.part_o + (slot * R + r) * kD + d) = o;
+                    if (d == 0) p.part_ml[slot * R + r] = make_float2(m, l);
                 }
             };
             const int mine = (rows - rank + cs - 1) / cs;  // this rank's rows
@@ -553,49 +603,62 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
                     o.x += f * v[w].x, o.y += f * v[w].y, o.z += f * v[w].z, o.w += f * v[w].w;
                 }
                 if (cs == 1) {
-                    leave(r, m, o, l);
+                    leave(r, 4 * lane, m, o, l);
                 } else {
                     *reinterpret_cast<float4*>(&s_part[it][4 * lane]) = o;
                     if (lane == 0) s_part_ml[it] = make_float2(m, l);
                 }
             }
-            // the `count` partials of row r from s_part[first] on, joined
-            auto join = [&](int first, int count, auto&& done) {
-                float m = kLow, l = 0.0f;
-                for (int x = 0; x < count; ++x) m = fmaxf(m, s_part_ml[first + x].x);
-                float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int x = 0; x < count; ++x) {
-                    const float2 ml = s_part_ml[first + x];
-                    const float4 v = *reinterpret_cast<const float4*>(&s_part[first + x][4 * lane]);
+            // s_part[x count ..] (count <= 8), the partials of the rank's row x, joined by all
+            // warps: 16 dims a warp, a partial for four lanes
+            auto join = [&](int count, auto&& done) {
+                const int share = lane >> 2;
+                for (int it = warp; it < mine * 8; it += kWarps) {
+                    const int x = it >> 3, d = 16 * (it & 7) + 4 * (lane & 3);
+                    float2 ml = make_float2(kLow, 0.0f);
+                    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (share < count) {
+                        ml = s_part_ml[x * count + share];
+                        o = *reinterpret_cast<const float4*>(&s_part[x * count + share][d]);
+                    }
+                    float m = ml.x;
+#pragma unroll
+                    for (int y = 4; y < 32; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
                     const float f = ex2(ml.x - m);
-                    l += f * ml.y;
-                    o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+                    float l = f * ml.y;
+                    o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+                    for (int y = 4; y < 32; y <<= 1) {
+                        l += __shfl_xor_sync(0xffffffffu, l, y);
+                        o.x += __shfl_xor_sync(0xffffffffu, o.x, y);
+                        o.y += __shfl_xor_sync(0xffffffffu, o.y, y);
+                        o.z += __shfl_xor_sync(0xffffffffu, o.z, y);
+                        o.w += __shfl_xor_sync(0xffffffffu, o.w, y);
+                    }
+                    if (share == 0) done(rank + x * cs, d, m, o, l);
                 }
-                done(m, o, l);
             };
             if (cs > 1) {
                 __syncthreads();
-                for (int x = warp; x < mine; x += kWarps)
-                    join(x * cs, cs, [&](float m, float4 o, float l) { leave(rank + x * cs, m, o, l); });
+                join(cs, leave);
             }
             if (!whole) {
                 // ---- the last cluster to arrive joins the unit's partials (a rank its rows)
                 const int k0 = start / sh.per, k1 = (unit_end - 1) / sh.per;
-                __threadfence();
                 __syncthreads();
                 if (tid == 0) {
+                    __threadfence();  // (the CTA's writes, which the barrier ordered before)
                     uint32_t* count = p.counters + k0 * 8 + rank;
                     s_last = atomicAdd(count, 1u) == (uint32_t)(k1 - k0);
                     if (s_last) *count = 0;
+                    __threadfence();
                 }
                 __syncthreads();
                 if (s_last) {
-                    __threadfence();
                     // `each` warps a row, every one a share of the clusters
                     const int each = max(1, kWarps / max(mine, 1));
                     for (int it = warp; it < mine * each; it += kWarps) {
                         const int r = rank + it / each * cs;
-                        auto slot_of = [&](int x) { return (2 * (int64_t)x + (start > x * sh.per ? 1 : 0)) * R + r; };
                         float m = kLow, l = 0.0f;
                         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                         for (int x0 = k0 + it % each; x0 <= k1; x0 += 8 * each) {
@@ -604,13 +667,13 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
 #pragma unroll
                             for (int y = 0; y < 8; ++y) {
                                 const int x = x0 + y * each;
-                                if (x > k1) {
-                                    ml[y] = make_float2(kLow, 0.0f);
-                                    v[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                                    continue;
+                                ml[y] = make_float2(kLow, 0.0f);
+                                v[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                                if (x <= k1) {
+                                    const int64_t at = (2 * (int64_t)x + (start > x * sh.per ? 1 : 0)) * R + r;
+                                    ml[y] = __ldcg(&p.part_ml[at]);
+                                    v[y] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * kD + 4 * lane));
                                 }
-                                ml[y] = __ldcg(&p.part_ml[slot_of(x)]);
-                                v[y] = __ldcg(reinterpret_cast<const float4*>(p.part_o + slot_of(x) * kD + 4 * lane));
                             }
                             float top = m;
 #pragma unroll
@@ -627,7 +690,7 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
                             }
                         }
                         if (each == 1) {
-                            write_row(r, o, l);
+                            write_row(r, 4 * lane, o, l);
                         } else {
                             *reinterpret_cast<float4*>(&s_part[it][4 * lane]) = o;
                             if (lane == 0) s_part_ml[it] = make_float2(m, l);
@@ -635,11 +698,12 @@ __global__ void __launch_bounds__(kThreads, NQ == 1 ? 2 : 1) fp4_attn_kernel(con
                     }
                     if (each > 1) {
                         __syncthreads();
-                        for (int x = warp; x < mine; x += kWarps)
-                            join(x * each, each, [&](float, float4 o, float l) { write_row(rank + x * cs, o, l); });
+                        join(each, [&](int r, int d, float, float4 o, float l) { write_row(r, d, o, l); });
                     }
                 }
             }
+            // (the ring's memory goes back to the copies)
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             if (cs > 1)
                 cluster_sync();  // what other ranks read of this CTA is free, and nobody leaves before
             else
@@ -703,9 +767,9 @@ cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
         }
         p.clusters = resident[dev][at];
     }
-    p.least = 2 * cs * kWarps;
+    p.least = cs * kWarps;
     // (a unit more than the places need: the padded split counts on it)
-    const int64_t most = units * std::max<int64_t>(1, (p.max_len + kGroup - 1) / kGroup);
+    const int64_t most = units * std::max<int64_t>(1, (p.max_len + kPair - 1) / kPair);
     p.clusters = (int)std::min<int64_t>(p.clusters, (most + p.least - 1) / p.least + units);
     cfg.gridDim = dim3((unsigned)(p.clusters * cs), 1, 1);
     return cudaLaunchKernelEx(&cfg, fp4_attn_kernel<NQ>, p);

@@ -28,6 +28,11 @@ DTYPES = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 HALF_STEP = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 
 
+@pytest.fixture(autouse=True)
+def seeded():
+    torch.manual_seed(21)
+
+
 def tables(n, inv=INV):
     return bg.bgtq_rope_table(inv, n)
 
