@@ -8,14 +8,18 @@
 //                   block g, which is lane i of tensor memory; each brings in
 //                   its own query row first (rotated, to fp16)
 //   warp 8          issues the MMAs (one elected lane)
-//   warps 12-15     decode the tiles: a group of 16 positions is 2304
-//                   contiguous bytes (one bulk copy, kDqStages in flight a
-//                   warp); its values are exact in fp16
+//   warps 9-15      decode the tiles: a group of 16 positions is 2304
+//                   contiguous bytes (one bulk copy, kSlots of them in flight
+//                   or in use); its values are exact in fp16.  A tile is 16
+//                   pieces of work, the keys of its eight groups, then their
+//                   values, that the warps take in turn
 // Decoded tiles are K-major operands with the 128-byte swizzle.  Values are
 // stored transposed, [dim][position]: two neighbouring positions share a byte,
 // so the conversion of a byte gives a pair that lies side by side there, and
 // the stores of a warp fall on 32 distinct banks.  A tile is decoded once for
-// 256 rows: the decoders' 2200 warp-instructions a tile run beside the softmax's.
+// 256 rows; its 2000 warp-instructions run beside the softmax's 6700 in what
+// issue slots those leave, which is why seven warps share them (four took 2.1 us a
+// tile, longer than the softmax and the products).
 // Tensor memory: S_g at columns 128 g (P_g, fp16, over its first 64), O_g at
 // 256 + 128 g.  MMA order of tile j: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1).
 // fp16 outputs: probabilities are rounded to fp16 before they meet the values
@@ -41,11 +45,11 @@ constexpr int kRows = 128;                      // rows of a block
 constexpr int kKeys = 128;                      // positions of a tile
 constexpr int kTileGroups = kKeys / kGroup;
 constexpr int kTileThreads = 512;
-constexpr int kDqWarp0 = 12, kDqWarps = 4, kDqStages = 3;
+constexpr int kDqWarp0 = 9, kDqWarps = 7, kSlots = 12;  // decoding warps; groups in shared memory
 constexpr uint32_t kTile = kRows * kD * 2;      // one 128 x 128 fp16 tile
 constexpr uint32_t kBox = kTile / 2;            // 64 columns of it (128 rows x 128 B)
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffStage = 6 * kTile;
-constexpr uint32_t kTilesSmem = kOffStage + kDqWarps * kDqStages * kGroupBytes + 1024;
+constexpr uint32_t kTilesSmem = kOffStage + kSlots * kGroupBytes + 1024;
 constexpr uint32_t kTmemCols = 512;
 // a row's reference stays kLift below its largest logit when set and moves when
 // a logit passes it by kLift + kHeadroom: P up to 2^15, its small ones above
@@ -65,8 +69,9 @@ enum {
     kBarP = 12,
     kBarO = 14,
     kBarDrain = 16,
-    kBarStage = 17,
-    kNumBars = kBarStage + kDqWarps * kDqStages
+    kBarFull = 17,                // a slot's group has landed
+    kBarKeys = kBarFull + kSlots,  // a slot's keys are decoded
+    kNumBars = kBarKeys + kSlots
 };
 
 struct TileParams {
@@ -117,9 +122,6 @@ __device__ __forceinline__ uint32_t tile_at(int row, int col) {
 __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-__device__ __forceinline__ void st_shared_v2(uint32_t a, uint32_t x, uint32_t y) {
-    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(x), "r"(y) : "memory");
-}
 __device__ __forceinline__ void st_shared(uint32_t a, uint32_t x) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
 }
@@ -132,67 +134,105 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
-// Keys of group gr (0..7) of a tile: a lane takes 4 dims of every block of a
-// position, two positions in turn.  The positions of 8 lanes are an even and
-// an odd one, those of 16 lanes differ in bits 1-2, so that loads and stores
-// fall on distinct banks.
-__device__ __forceinline__ void decode_keys(uint32_t img, uint32_t tile, int gr, int lane) {
-    const int c = lane & 3, i = lane >> 2;
-    const int tp = i < 4 ? (i << 1) + (i & 1) : ((i - 4) << 1) + 1 - (i & 1);  // 0 3 4 7 1 2 5 6
+// What a lane's place in a warp says about where it reads and writes.
+struct Place {
+    uint32_t k_in, ks_in, k_out[4];  // keys: offsets of its codes and scales in a group, of its stores in a group's rows
+    uint32_t v_in, vs_in, v_out;     // values likewise; v_out without the group's columns
+    uint32_t g16;                    // (lane / 4) * 16
+    __device__ __forceinline__ explicit Place(int lane) {
+        // Keys: a lane takes 4 dims of every block of a position, two positions in
+        // turn.  The positions of 8 lanes are an even and an odd one, those of 16
+        // lanes differ in bits 1-2, so that loads and stores fall on distinct banks.
+        const int i = lane >> 2, c = lane & 3;
+        const int pos = i < 4 ? (i << 1) + (i & 1) : ((i - 4) << 1) + 1 - (i & 1);  // 0 3 4 7 1 2 5 6
+        k_in = 64 * pos + 16 * c;
+        ks_in = kGroupKs + 8 * pos;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k_out[j] = 128u * pos + 8u * (c & 1) + 16u * ((uint32_t)(2 * j + (c >> 1)) ^ (uint32_t)pos);
+        v_in = kGroupV + 16 * lane;
+        vs_in = kGroupVs + 32 * c;
+        v_out = 128u * i + 4u * c;
+        g16 = 16u * i;
+    }
+};
+
+template <int kAt>
+__device__ __forceinline__ void store2(uint32_t a, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.b32 [%0 + %3], {%1, %2};" ::"r"(a), "r"(x), "r"(y), "n"(kAt) : "memory");
+}
+template <int kAt>
+__device__ __forceinline__ void store1(uint32_t a, uint32_t x) {
+    asm volatile("st.shared.b32 [%0 + %2], %1;" ::"r"(a), "r"(x), "n"(kAt) : "memory");
+}
+
+// Blocks 2 kJJ and 2 kJJ + 1 of a position's keys (row 8 kIt + .. of the group's rows).
+template <int kIt, int kJJ>
+__device__ __forceinline__ void key_blocks(uint32_t w, uint32_t sw, const uint32_t (&out)[4]) {
+    const __half2 s = fp4_scales<(kJJ & 1) * 2>(sw), s0 = __low2half2(s), s1 = __high2half2(s);
+    __half2 x[4];
+    fp4_numbers(w, x);
+    constexpr int kAt = kIt * 1024 + (kJJ >> 1) * (int)kBox;
+    store2<kAt>(out[(2 * kJJ) & 3], u32(__hmul2(x[0], s0)), u32(__hmul2(x[1], s0)));
+    store2<kAt>(out[(2 * kJJ + 1) & 3], u32(__hmul2(x[2], s1)), u32(__hmul2(x[3], s1)));
+}
+
+// Keys of group gr (0..7) of a tile.
+__device__ __forceinline__ void decode_keys(const Place& at, uint32_t img, uint32_t tile, int gr) {
+    uint4 w[2];
+    uint32_t s[2][2];
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
-        const int pos = 8 * it + tp, row = kGroup * gr + pos;
-        const uint4 w4 = ld_shared_v4(img + 64 * pos + 16 * c);
-        uint32_t s0, s1;
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(s0), "=r"(s1) : "r"(img + kGroupKs + 8 * pos) : "memory");
-        const uint32_t w[4] = {w4.x, w4.y, w4.z, w4.w};
-        const uint32_t base = tile + (uint32_t)row * 128u + 8u * (c & 1);
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-            const uint32_t sw = jj < 2 ? s0 : s1;
-            const __half2 s = (jj & 1) ? fp4_scales<2>(sw) : fp4_scales<0>(sw);
-            __half2 x[4];
-            fp4_numbers(w[jj], x);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int j = 2 * jj + k;  // dims 16 j + 4 c ..
-                const __half2 m = k ? __high2half2(s) : __low2half2(s);
-                const uint32_t piece = (uint32_t)((2 * j + (c >> 1)) & 7) ^ (uint32_t)(row & 7);
-                st_shared_v2(base + (uint32_t)(j >> 2) * kBox + 16u * piece, u32(__hmul2(x[2 * k], m)), u32(__hmul2(x[2 * k + 1], m)));
-            }
-        }
+        w[it] = ld_shared_v4(img + at.k_in + 512 * it);
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(s[it][0]), "=r"(s[it][1]) : "r"(img + at.ks_in + 64 * it) : "memory");
     }
+    uint32_t out[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) out[j] = tile + 2048u * gr + at.k_out[j];
+    key_blocks<0, 0>(w[0].x, s[0][0], out);
+    key_blocks<0, 1>(w[0].y, s[0][0], out);
+    key_blocks<0, 2>(w[0].z, s[0][1], out);
+    key_blocks<0, 3>(w[0].w, s[0][1], out);
+    key_blocks<1, 0>(w[1].x, s[1][0], out);
+    key_blocks<1, 1>(w[1].y, s[1][0], out);
+    key_blocks<1, 2>(w[1].z, s[1][1], out);
+    key_blocks<1, 3>(w[1].w, s[1][1], out);
+}
+
+// Block kJ (dims 16 kJ ..) of the values of four positions.
+template <int kJ>
+__device__ __forceinline__ void value_block(uint32_t w, uint32_t sw, uint32_t a0, uint32_t a1) {
+    const __half2 f0 = fp4_scales<0>(sw), f1 = fp4_scales<2>(sw);
+    __half2 x[4];
+    fp4_numbers(w, x);
+    store1<2048 * kJ>(a0, u32(__hmul2(x[0], f0)));
+    store1<2048 * kJ + 1024>(a0, u32(__hmul2(x[1], f0)));
+    store1<2048 * kJ>(a1, u32(__hmul2(x[2], f1)));
+    store1<2048 * kJ + 1024>(a1, u32(__hmul2(x[3], f1)));
 }
 
 // Values of group gr, transposed; `live`: positions of the group that exist (the others become zeros).
-__device__ __forceinline__ void decode_values(uint32_t img, uint32_t tile, int gr, int live, int lane) {
-    const int g = lane >> 2, c = lane & 3;
-    uint32_t keep = 0xffffffffu;
+__device__ __forceinline__ void decode_values(const Place& at, uint32_t img, uint32_t tile, int gr, int live, int lane) {
+    const uint4 w0 = ld_shared_v4(img + at.v_in), w1 = ld_shared_v4(img + at.v_in + 512);
+    uint4 s0 = ld_shared_v4(img + at.vs_in), s1 = ld_shared_v4(img + at.vs_in + 16);
     if (live < kGroup) {
+        uint32_t keep = 0xffffffffu;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            if (2 * c + (e & 1) + 8 * (e >> 1) >= live) keep &= ~(0xffu << (8 * e));
+            if (2 * (lane & 3) + (e & 1) + 8 * (e >> 1) >= live) keep &= ~(0xffu << (8 * e));
+        s0.x &= keep, s0.y &= keep, s0.z &= keep, s0.w &= keep;
+        s1.x &= keep, s1.y &= keep, s1.z &= keep, s1.w &= keep;
     }
     // positions 16 gr + 2 c (+ 1) and + 8: columns of the transposed tile
-    const uint32_t box = tile + (uint32_t)(gr >> 2) * kBox + 4u * c;
-    const uint32_t p0 = ((uint32_t)(2 * (gr & 3)) ^ (uint32_t)g) * 16u, p1 = ((uint32_t)(2 * (gr & 3) + 1) ^ (uint32_t)g) * 16u;
-#pragma unroll
-    for (int jj = 0; jj < 2; ++jj) {
-        const uint4 v = ld_shared_v4(img + kGroupV + 512 * jj + 16 * lane), t = ld_shared_v4(img + kGroupVs + 32 * c + 16 * jj);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w}, sc[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const uint32_t u = sc[k] & keep;
-            const __half2 f0 = fp4_scales<0>(u), f1 = fp4_scales<2>(u);
-            __half2 x[4];
-            fp4_numbers(w[k], x);
-            const uint32_t row = box + (uint32_t)(16 * (4 * jj + k) + g) * 128u;  // dims 16 j + g and + 8
-            st_shared(row + p0, u32(__hmul2(x[0], f0)));
-            st_shared(row + 1024u + p0, u32(__hmul2(x[1], f0)));
-            st_shared(row + p1, u32(__hmul2(x[2], f1)));
-            st_shared(row + 1024u + p1, u32(__hmul2(x[3], f1)));
-        }
-    }
+    const uint32_t box = tile + (uint32_t)(gr >> 2) * kBox + at.v_out;
+    const uint32_t a0 = box + ((uint32_t)(32 * (gr & 3)) ^ at.g16), a1 = box + ((uint32_t)(32 * (gr & 3) + 16) ^ at.g16);
+    value_block<0>(w0.x, s0.x, a0, a1);
+    value_block<1>(w0.y, s0.y, a0, a1);
+    value_block<2>(w0.z, s0.z, a0, a1);
+    value_block<3>(w0.w, s0.w, a0, a1);
+    value_block<4>(w1.x, s1.x, a0, a1);
+    value_block<5>(w1.y, s1.y, a0, a1);
+    value_block<6>(w1.z, s1.z, a0, a1);
+    value_block<7>(w1.w, s1.w, a0, a1);
 }
 __device__ __forceinline__ void zero_values(uint32_t tile, int gr, int lane) {
     const int g = lane >> 2, c = lane & 3;
@@ -262,7 +302,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_bar[kNumBars];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort;
+    __shared__ int s_abort, s_issued[kSlots];
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // units with the most tiles (a head's last rows) first; of split units all first parts, then all second ones
@@ -292,8 +332,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
 
     if (tid == 0) {
         s_abort = 0;
+        for (int i = 0; i < kSlots; ++i) s_issued[i] = 0;
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(BAR(i), i < kBarKFull ? 4 : (i >= kBarKFull && i < kBarKEmpty) ? kDqWarps : (i == kBarP || i == kBarP + 1) ? kRows : 1);
+            mbar_init(BAR(i), i < kBarKFull ? 4 : (i >= kBarKFull && i < kBarKEmpty) ? kTileGroups : (i == kBarP || i == kBarP + 1) ? kRows : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) {
@@ -361,70 +402,56 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             mma_commit_warp(BAR(kBarDrain));
             mbar_wait(BAR(kBarDrain), 0, abort_flag, p.status, false);
         } else if (warp >= kDqWarp0) {
-            // ---- decoding: warp w takes groups w and w + 4 of every tile
-            const int w = warp - kDqWarp0;
-            const int n_groups = (n + kGroup - 1) / kGroup;
-            const uint32_t ring = sbase + kOffStage + w * (kDqStages * kGroupBytes), rbar = BAR(kBarStage + w * kDqStages);
-            const int first = j0 * kTileGroups + w;         // the warp's groups: first + 4 x, x = 0, 1, ...
-            const int count = max(0, min(2 * nkt, (n_groups - first + 3) / 4));
+            // ---- decoding: piece u = 16 j + (0..7 keys, 8..15 values of group u mod 8 of tile j)
+            const int n_groups = (n + kGroup - 1) / kGroup, first = j0 * kTileGroups;
+            const int count = max(0, min(kTileGroups * nkt, n_groups - first));  // groups of the CTA's tiles
+            const Place at(lane);
             auto fetch = [&](int x) {
-                const int gi = first + 4 * x, st = x % kDqStages;
-                const uint8_t* src = p.map.group(b, h, gi);
+                const int st = x % kSlots;
+                const uint8_t* src = p.map.group(b, h, first + x);
                 if (!src) {
                     if (p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
                     src = p.map.base;  // (some group of the pool: the output is unspecified)
                 }
-                mbar_expect_tx(rbar + 8 * st, kGroupBytes);
+                s_issued[st] = x / kSlots + 1;
+                mbar_expect_tx(BAR(kBarFull + st), kGroupBytes);
                 asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                 ring + st * kGroupBytes),
-                             "l"(src), "r"((uint32_t)kGroupBytes), "r"(rbar + 8 * st)
+                                 sbase + kOffStage + st * kGroupBytes),
+                             "l"(src), "r"((uint32_t)kGroupBytes), "r"(BAR(kBarFull + st))
                              : "memory");
             };
-            int issued = 0;  // (lane 0)
-            if (lane == 0)
-                for (; issued < min(count, kDqStages); ++issued) fetch(issued);
-            bool ok = true;
             auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag, p.status));
             };
-            int landed = 0;  // groups whose copies this warp has waited for
-            for (int j = 0; ok && j < nkt; ++j) {
-                const int s = j & 1;
-                const uint32_t par = (uint32_t)((j >> 1) - 1) & 1u;
-                if (j >= 2 && !(ok = wait(BAR(kBarKEmpty + s), par))) break;
-                for (int e = 0; e < 2 && ok; ++e) {
-                    const int x = 2 * j + e;
-                    if (x >= count) continue;
-                    if (x >= landed) {
-                        ok = wait(rbar + 8 * (x % kDqStages), (uint32_t)(x / kDqStages));
-                        landed = x + 1;
-                    }
-                    if (ok) decode_keys(ring + (x % kDqStages) * kGroupBytes, sbase + kOffK + s * kTile, w + 4 * e, lane);
-                }
-                if (!ok) break;
-                fence_to_async();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(kBarKFull + s));
-                if (j >= 2 && !(ok = wait(BAR(kBarVEmpty + s), par))) break;
-                for (int e = 0; e < 2; ++e) {
-                    const int x = 2 * j + e;
-                    if (x < count) {
-                        decode_values(ring + (x % kDqStages) * kGroupBytes, sbase + kOffV + s * kTile, w + 4 * e,
-                                      n - (first + 4 * x) * kGroup, lane);
-                        __syncwarp();
-                        if (lane == 0 && issued < count) fetch(issued++);
-                    } else {
-                        zero_values(sbase + kOffV + s * kTile, w + 4 * e, lane);
-                    }
+            if (warp == kDqWarp0 && lane == 0)
+                for (int x = 0; x < min(count, kSlots); ++x) fetch(x);
+            for (int u = warp - kDqWarp0; u < 16 * nkt; u += kDqWarps) {
+                const int j = u >> 4, gr = u & 7, s = j & 1, x = kTileGroups * j + gr;
+                const uint32_t slot = (uint32_t)(x % kSlots), round = (uint32_t)(x / kSlots);
+                const uint32_t img = sbase + kOffStage + slot * kGroupBytes;
+                const bool keys = !(u & 8);
+                // the tile's buffer is free, the group has landed
+                if (j >= 2 && !wait(BAR((keys ? kBarKEmpty : kBarVEmpty) + s), (uint32_t)((j >> 1) - 1))) break;
+                if (x < count && !wait(BAR(kBarFull + slot), round)) break;
+                if (keys) {
+                    if (x < count) decode_keys(at, img, sbase + kOffK + s * kTile, gr);
+                } else if (x < count) {
+                    decode_values(at, img, sbase + kOffV + s * kTile, gr, n - (first + x) * kGroup, lane);
+                } else {
+                    zero_values(sbase + kOffV + s * kTile, gr, lane);
                 }
                 fence_to_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(BAR(kBarVFull + s));
+                if (lane == 0) {
+                    mbar_arrive(BAR((keys ? kBarKFull : kBarVFull) + s));
+                    if (keys) {
+                        if (x < count) mbar_arrive(BAR(kBarKeys + slot));
+                    } else if (x + kSlots < count && mbar_wait(BAR(kBarKeys + slot), round & 1u, abort_flag, p.status)) {
+                        fetch(x + kSlots);  // the slot's next group
+                    }
+                }
+                __syncwarp();
             }
-            // every copy issued has landed before the CTA ends
-            issued = __shfl_sync(0xffffffffu, issued, 0);
-            for (int x = landed; x < issued; ++x)
-                mbar_wait(rbar + 8 * (x % kDqStages), (uint32_t)(x / kDqStages) & 1u, abort_flag, p.status, false);
         }
         __syncwarp();
     } else {
@@ -556,22 +583,29 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             }
         }
     }
-#undef BAR
     tc_fence_before();
     __syncthreads();
+    // (after a wait that gave up: every copy issued lands, or times out once more, before the CTA ends)
+    if (s_abort && tid < kSlots && s_issued[tid])
+        mbar_wait(BAR(kBarFull + tid), (uint32_t)(s_issued[tid] - 1) & 1u, abort_flag, p.status, false);
+#undef BAR
     if (warp == 8) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols));
     }
 }
 
-// Joins the splits' rows: a warp a row, four dims a lane.
+// Joins the splits' rows: kWide, many splits: a block of eight warps a row, a
+// warp every eighth split; else a warp a row.  Four dims a lane.
+template <bool kWide>
 __global__ void __launch_bounds__(256) fp4_join_kernel(const __grid_constant__ TileParams p) {
+    __shared__ __align__(16) float s_o[8][kD];
+    __shared__ float2 s_ml[8];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int64_t total = (int64_t)p.n_split * (2 * kRows);
-    const int64_t slot_row = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t slot_row = kWide ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
     const int unit = p.n_whole + (int)(slot_row / (2 * kRows));
     const int pb = p.blocks - 1 - unit / p.heads, head = unit % p.heads;
     const int r = pb * 2 * kRows + (int)(slot_row % (2 * kRows));
@@ -580,21 +614,65 @@ __global__ void __launch_bounds__(256) fp4_join_kernel(const __grid_constant__ T
     const int tiles = block_tiles(p, pb, clamp_len(p, b));
     const int active = (tiles + p.part_tiles - 1) / p.part_tiles;
     if (active <= 1) return;  // (written by its CTA)
-    float m = kLow;
-    for (int x = 0; x < active; ++x) m = fmaxf(m, p.part_ml[x * total + slot_row].x);
-    float l = 0.0f;
+    constexpr int kStep = kWide ? 8 : 1, kAhead = kWide ? 8 : 4;
+    float m = kLow, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int x = 0; x < active; ++x) {
-        const float2 ml = p.part_ml[x * total + slot_row];
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + (x * total + slot_row) * kD + 4 * lane);
+    for (int x0 = kWide ? warp : 0; x0 < active; x0 += kStep * kAhead) {
+        float2 ml[kAhead];
+        float4 v[kAhead];
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const int x = x0 + kStep * y;
+            ml[y] = make_float2(kLow, 0.0f);
+            v[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (x < active) {
+                ml[y] = p.part_ml[x * total + slot_row];
+                v[y] = *reinterpret_cast<const float4*>(p.part_o + (x * total + slot_row) * kD + 4 * lane);
+            }
+        }
+        float top = m;
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) top = fmaxf(top, ml[y].x);
+        const float f0 = ex2(m - top);
+        m = top;
+        l *= f0;
+        o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+        for (int y = 0; y < kAhead; ++y) {
+            const float f = ex2(ml[y].x - m);
+            l += f * ml[y].y;
+            o.x += f * v[y].x, o.y += f * v[y].y, o.z += f * v[y].z, o.w += f * v[y].w;
+        }
+    }
+    int d = 4 * lane;
+    if constexpr (kWide) {
+        // 16 dims a warp, a warp's partial for four lanes
+        *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = o;
+        if (lane == 0) s_ml[warp] = make_float2(m, l);
+        __syncthreads();
+        const int share = lane >> 2;
+        d = 16 * warp + 4 * (lane & 3);
+        const float2 ml = s_ml[share];
+        o = *reinterpret_cast<const float4*>(&s_o[share][d]);
+        m = ml.x;
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, y));
         const float f = ex2(ml.x - m);
-        l += f * ml.y;
-        o.x += f * v.x, o.y += f * v.y, o.z += f * v.z, o.w += f * v.w;
+        l = f * ml.y;
+        o.x *= f, o.y *= f, o.z *= f, o.w *= f;
+#pragma unroll
+        for (int y = 4; y < 32; y <<= 1) {
+            l += __shfl_xor_sync(0xffffffffu, l, y);
+            o.x += __shfl_xor_sync(0xffffffffu, o.x, y);
+            o.y += __shfl_xor_sync(0xffffffffu, o.y, y);
+            o.z += __shfl_xor_sync(0xffffffffu, o.z, y);
+            o.w += __shfl_xor_sync(0xffffffffu, o.w, y);
+        }
+        if (share != 0) return;
     }
     const float inv = l > 0.0f ? 1.0f / l : l != l ? l : 0.0f;
     const int i = r / p.group, a = r - i * p.group;
-    const int64_t at = (((int64_t)b * p.H * p.group + h * p.group + a) * p.t + i) * kD + 4 * lane;
+    const int64_t at = (((int64_t)b * p.H * p.group + h * p.group + a) * p.t + i) * kD + d;
     if (p.out_dtype)
         *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     else
@@ -700,10 +778,11 @@ cudaError_t launch_fp4_tiles(cudaStream_t s, const Fp4Attn& a, void* ws) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, a.out_dtype ? fp4_tiles_kernel<true> : fp4_tiles_kernel<false>, p);
     if (e != cudaSuccess || sp.n_split == 0) return e;
-    cfg.gridDim = dim3((unsigned)(sp.n_split * 2 * kRows / 8), 1, 1);
+    const bool wide = sp.parts >= 8;
+    cfg.gridDim = dim3((unsigned)(sp.n_split * 2 * kRows / (wide ? 1 : 8)), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, fp4_join_kernel, p);
+    return cudaLaunchKernelEx(&cfg, wide ? fp4_join_kernel<true> : fp4_join_kernel<false>, p);
 }
 
 }  // namespace bgtq
