@@ -178,43 +178,22 @@ __device__ __forceinline__ float half_scale_norm(float (&z)[64], int n, const fl
 template <int BK, class P>
 __device__ __forceinline__ void bulk_key_half(const P& p, int nc, int hf, const int* s_end, const float2* pw,
                                               const float* is, const uint4* cp, const uint32_t* pk, uint32_t* row,
-                                              uint32_t* rec, uint4 (&w4)[8], bool act, size_t unit, int64_t pos,
-                                              int64_t end, int64_t sl, const int (&rp)[kMaxAxes]) {
-    // 16-byte pieces w4[0..3] and w4[4..7] of the row start at q0 and q1
-    int q0 = 8 * hf, q1 = 8 * hf + 4;
-    if constexpr (kRotates<P>) {
-        // this half's 32 blocks, eight at a time; rounded to fp16 as the cached key is
-        auto turn = [&](int m, uint4& wa, uint4& wb) {
-            uint32_t a[4] = {wa.x, wa.y, wa.z, wa.w}, b[4] = {wb.x, wb.y, wb.z, wb.w};
-            rope_rotate8(p.rope, rp, 32 * hf + 8 * m, a, b);
-            wa = make_uint4(a[0], a[1], a[2], a[3]);
-            wb = make_uint4(b[0], b[1], b[2], b[3]);
-        };
-        if (act && p.rope.layout == 0) {
+                                              uint32_t* rec, const uint4 (&w4)[8], bool act, size_t unit, int64_t pos,
+                                              int64_t end, int64_t sl) {
+    if constexpr (!kRotates<P>) {  // (rotated rows are in shared memory already, see rotate_rows)
+        if (act && p.recent > 0 && pos >= end - p.recent) {
+            // fp16 recent-key ring: the key as given, slot pos mod W
+            uint4* rdst = reinterpret_cast<uint4*>(p.k_recent + (unit * p.recent + pos % p.recent) * kD) + 8 * hf;
 #pragma unroll
-            for (int m = 0; m < 4; ++m) turn(m, w4[m], w4[4 + m]);
-        } else if (act) {
-#pragma unroll
-            for (int m = 0; m < 4; ++m) turn(m, w4[2 * m], w4[2 * m + 1]);
+            for (int i = 0; i < 8; ++i) rdst[i] = w4[i];
         }
-        if (p.rope.layout == 0) {
-            q0 = 4 * hf;
-            q1 = 8 + 4 * hf;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            row[32 * hf + 4 * i] = w4[i].x;
+            row[32 * hf + 4 * i + 1] = w4[i].y;
+            row[32 * hf + 4 * i + 2] = w4[i].z;
+            row[32 * hf + 4 * i + 3] = w4[i].w;
         }
-    }
-    if (act && p.recent > 0 && pos >= end - p.recent) {
-        // fp16 recent-key ring: the key as given, slot pos mod W
-        uint4* rdst = reinterpret_cast<uint4*>(p.k_recent + (unit * p.recent + pos % p.recent) * kD);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) rdst[(i < 4 ? q0 : q1 - 4) + i] = w4[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        uint32_t* dst = row + 4 * ((i < 4 ? q0 : q1 - 4) + i);
-        dst[0] = w4[i].x;
-        dst[1] = w4[i].y;
-        dst[2] = w4[i].z;
-        dst[3] = w4[i].w;
     }
 #pragma unroll
     for (int i = 0; i < 2 * BK; ++i) rec[2 * BK * hf + i] = 0;
@@ -365,6 +344,67 @@ __device__ __forceinline__ void bulk_value_half(const P& p, int hf, int par, con
     }
 }
 
+// Keys that are rotated on the way.  The rows of the block's 64 tokens are
+// loaded, turned and put into shared memory by eight threads a token (16
+// tokens in turn), so that neighbouring threads read neighbouring bytes of
+// rows and tables: with the two threads a token of the encoder every load
+// touched 32 lines, and the tables cost 41 us of 131072 tokens' 165 against
+// the plain append's 123.  Thread i of a token has the dims of blocks 8 i ..
+// 8 i + 7; w4[2 k], w4[2 k + 1]: its two pieces of token 16 k + tid / 8.
+template <class P>
+__device__ __forceinline__ void rotate_pieces(const P& p, int i, int& qa, int& qb) {
+    qa = p.rope.layout ? 2 * i : i;
+    qb = p.rope.layout ? 2 * i + 1 : 8 + i;
+}
+template <class P>
+__device__ __forceinline__ void rotate_load(const P& p, int b, int h, int ps, int64_t end, int64_t pos0, uint4 (&w4)[8]) {
+    if constexpr (kRotates<P>) {
+        int qa, qb;
+        rotate_pieces(p, threadIdx.x & 7, qa, qb);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int64_t pos = pos0 + 16 * k + (threadIdx.x >> 3);
+            w4[2 * k] = w4[2 * k + 1] = make_uint4(0u, 0u, 0u, 0u);
+            if (pos >= ps && pos < end) {
+                const uint4* src = reinterpret_cast<const uint4*>(new_key(p, b, h, pos - ps));
+                w4[2 * k] = __ldg(src + qa);
+                w4[2 * k + 1] = __ldg(src + qb);
+            }
+        }
+    }
+}
+template <class P>
+__device__ __forceinline__ void rotate_rows(const P& p, int b, size_t unit, int ps, int64_t end, int64_t pos0, uint4 (&w4)[8],
+                                            uint32_t* s_rows) {
+    if constexpr (kRotates<P>) {
+        int qa, qb;
+        rotate_pieces(p, threadIdx.x & 7, qa, qb);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int tok = 16 * k + (threadIdx.x >> 3);
+            const int64_t pos = pos0 + tok;
+            int rp[kMaxAxes];
+            uint32_t x[4] = {w4[2 * k].x, w4[2 * k].y, w4[2 * k].z, w4[2 * k].w};
+            uint32_t y[4] = {w4[2 * k + 1].x, w4[2 * k + 1].y, w4[2 * k + 1].z, w4[2 * k + 1].w};
+            if (pos >= ps && pos < end && rope_positions(p.rope, (int64_t)b * p.t_new + (pos - ps), pos, rp)) {
+                rope_rotate8(p.rope, rp, 8 * (threadIdx.x & 7), x, y);
+                if (p.recent > 0 && pos >= end - p.recent) {
+                    // fp16 recent-key ring: the rotated key, slot pos mod W
+                    uint4* rdst = reinterpret_cast<uint4*>(p.k_recent + (unit * p.recent + pos % p.recent) * kD);
+                    rdst[qa] = make_uint4(x[0], x[1], x[2], x[3]);
+                    rdst[qb] = make_uint4(y[0], y[1], y[2], y[3]);
+                }
+            }
+            uint32_t* row = s_rows + tok * kRowWords;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                row[4 * qa + e] = x[e];
+                row[4 * qb + e] = y[e];
+            }
+        }
+    }
+}
+
 template <int BK, int BV, class P>
 __global__ void __launch_bounds__(kBulkThreads, kBulkMinBlocks) quantize_append_bulk_kernel(P p) {
     __shared__ float2 s_pw[2 * kPwRow];  // keys: (whitening x sign, source dim) per codec coordinate (0 past n_coded)
@@ -399,8 +439,8 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkMinBlocks) quantize_append_
     const int64_t pos = (int64_t)(ps & ~1) + (int64_t)blockIdx.x * kBulkTok + tk;
     bool act = pos >= ps && pos < end;
     const size_t unit = (size_t)b * p.H + h;
-    int rp[kMaxAxes] = {};
     if constexpr (kRotates<P>) {
+        int rp[kMaxAxes];
         if (act && !rope_positions(p.rope, (int64_t)b * p.t_new + (pos - ps), pos, rp)) {
             act = false;
             if (hf == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_ROPE_RANGE);
@@ -409,18 +449,12 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkMinBlocks) quantize_append_
     // this half of the token's fp16 row (zeros for an inactive token): issued
     // first, so that the plan-static set-up below runs while it is in flight
     uint4 w4[8];
-    if (act) {
-        const uint4* src = reinterpret_cast<const uint4*>(is_v ? new_value(p, b, h, pos - ps) : new_key(p, b, h, pos - ps));
-        int q0 = 8 * hf, q1 = 8 * hf + 4;
-        if constexpr (kRotates<P>) {
-            // (keys of layout 0: both dims of this half's blocks)
-            if (!is_v && p.rope.layout == 0) {
-                q0 = 4 * hf;
-                q1 = 8 + 4 * hf;
-            }
-        }
+    if (kRotates<P> && !is_v) {
+        rotate_load(p, b, h, ps, end, (int64_t)(ps & ~1) + (int64_t)blockIdx.x * kBulkTok, w4);
+    } else if (act) {
+        const uint4* src = reinterpret_cast<const uint4*>(is_v ? new_value(p, b, h, pos - ps) : new_key(p, b, h, pos - ps)) + 8 * hf;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w4[i] = __ldg(src + (i < 4 ? q0 : q1 - 4) + i);
+        for (int i = 0; i < 8; ++i) w4[i] = __ldg(src + i);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w4[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -474,11 +508,14 @@ __global__ void __launch_bounds__(kBulkThreads, kBulkMinBlocks) quantize_append_
         const uint32_t bit = ht->pair_bit[m];  // the pair's 2w-bit field starts here
         s_pk[mk] = 4u * (bit >> 5) | (bit & 31u) << 8 | (uint32_t)w << 16 | (uint32_t)((bit & 31u) + 2u * w > 32u) << 31;
     }
+    if constexpr (kRotates<P>) {
+        if (!is_v) rotate_rows(p, b, unit, ps, end, (int64_t)(ps & ~1) + (int64_t)blockIdx.x * kBulkTok, w4, s_dyn);
+    }
     __syncthreads();
     if (sl < 0 && p.status && hf == 0) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
     if (!is_v)
         bulk_key_half<BK>(p, nc, hf, s_end, s_pw + hf * kPwRow, s_is + hf * kFRow, s_cp + hf * kCpRow, s_pk + hf * kPkRow,
-                          s_dyn + tk * kRowWords, s_rec + tk * (4 * BK + 1), w4, act, unit, pos, end, sl, rp);
+                          s_dyn + tk * kRowWords, s_rec + tk * (4 * BK + 1), w4, act, unit, pos, end, sl);
     else
         bulk_value_half<BV>(p, hf, tk & 1, s_sv + hf * kFRow, s_cell, cell_base, w4, act, ps, pos, end, sl);
 }

@@ -100,43 +100,57 @@ __device__ __forceinline__ void fp4_numbers(uint32_t w, __half2 (&x)[4]) {
 }
 
 // Byte of the scale of a block whose largest magnitude is amax: amax / 6 to
-// four significant bits, ties to even, steps of 2^-17 below 2^-14.
+// four significant bits, ties to even, steps of 2^-17 below 2^-14.  The
+// quotient comes from 1/6 in two parts, the first of 12 bits, whose product
+// with amax (11 bits) is exact: a quotient that is a tie (five bits) comes out
+// as that tie, and any other is at least 2^-12 of itself away from one.
 __device__ __forceinline__ uint32_t fp4_scale_byte(float amax) {
-    const float y = __fdiv_rn(amax, 6.0f);
+    constexpr float kHi = 0.1666259765625f, kLo = (float)(1.0 / 6.0 - 0.1666259765625);
+    const float y = __fmaf_rn(amax, kLo, __fmul_rn(amax, kHi));
     const uint32_t u = __float_as_uint(y);
     const uint32_t norm = ((u + 0x7ffffu + ((u >> 20) & 1u)) >> 20) - (112u << 3);
     const uint32_t sub = (uint32_t)__float2int_rn(__fmul_rn(y, 131072.0f));
     return min(y < 6.103515625e-5f ? sub : norm, (uint32_t)kScaleMax);
 }
 
-// 16 fp16 values (8 words) -> 16 codes in dim order (2 words) and the scale
-// byte.  The quotient x/s is correctly rounded where it has to be: one
-// correction of x r with the exact remainder makes a quotient that is a
-// midpoint of two codes come out as that midpoint, and any other is at least
-// 2^-18 of itself away from one (x has 11 bits, s four, a midpoint three).
-__device__ __forceinline__ uint32_t fp4_encode(const uint32_t (&w)[8], uint32_t (&code)[2]) {
-    __half2 m = __habs2(*reinterpret_cast<const __half2*>(&w[0]));
-#pragma unroll
-    for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&w[i])));
-    const uint32_t byte = fp4_scale_byte(fmaxf(__low2float(m), __high2float(m)));
-    const float s = __half2float(__ushort_as_half((unsigned short)(byte << 7)));
-    const float r = byte ? __frcp_rn(s) : 0.0f;
-#pragma unroll
-    for (int hw = 0; hw < 2; ++hw) {
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&w[4 * hw + i]));
-            const float a = __fmul_rn(x.x, r), b = __fmul_rn(x.y, r);
-            const float qa = __fmaf_rn(__fmaf_rn(-a, s, x.x), r, a), qb = __fmaf_rn(__fmaf_rn(-b, s, x.y), r, b);
-            uint32_t e;
-            asm("{\n .reg .b8 t;\n cvt.rn.satfinite.e2m1x2.f32 t, %1, %2;\n cvt.u32.u8 %0, t;\n}\n" : "=r"(e) : "f"(qb), "f"(qa));
-            // (the correction turns a quotient -0 into +0: the sign is x's own)
-            c |= (e | ((w[4 * hw + i] >> 12) & 0x8u) | ((w[4 * hw + i] >> 24) & 0x80u)) << (8 * i);
-        }
-        code[hw] = c;
+__device__ __forceinline__ float fp4_amax(const uint32_t (&w)[4]) {
+    const __half2 m = __hmax2(__hmax2(__habs2(*reinterpret_cast<const __half2*>(&w[0])), __habs2(*reinterpret_cast<const __half2*>(&w[1]))),
+                              __hmax2(__habs2(*reinterpret_cast<const __half2*>(&w[2])), __habs2(*reinterpret_cast<const __half2*>(&w[3]))));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+// A block's reciprocal scale in two parts, the first of 12 bits (0 for scale 0).
+struct Fp4Recip {
+    uint64_t hi, lo;  // each twice
+    __device__ __forceinline__ explicit Fp4Recip(uint32_t byte) {
+        const float s = __half2float(__ushort_as_half((unsigned short)(byte << 7)));
+        const float r = byte ? __frcp_rn(s) : 0.0f;
+        const float h = __uint_as_float(__float_as_uint(r) & 0xfffff000u);
+        const float l = byte ? __fmul_rn(__fmaf_rn(-h, s, 1.0f), r) : 0.0f;
+        hi = pair2(h, h);
+        lo = pair2(l, l);
     }
-    return byte;
+};
+
+// Half a block, 8 fp16 values (4 words) -> 8 codes in dim order.  x/s = x hi +
+// x lo: the first product is exact (11 and 12 bits), so the sum is the quotient
+// to 2^-36 rounded once to fp32.  A quotient that is a midpoint of two codes
+// comes out as that midpoint, and any other is at least 2^-18 of itself away
+// from one (x has 11 bits, s four, a midpoint three).  A zero keeps its sign.
+__device__ __forceinline__ uint32_t fp4_encode8(const uint32_t (&w)[4], const Fp4Recip& r) {
+    float2 q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = rope_f2(w[i]);
+        const uint64_t p = pair2(x.x, x.y);
+        q[i] = halves2(fma_pair(p, r.lo, mul_pair(p, r.hi)));
+    }
+    uint32_t c;
+    asm("{\n .reg .b8 a, b, c, d;\n cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n mov.b32 %0, {a, b, c, d};\n}\n"
+        : "=r"(c)
+        : "f"(q[0].x), "f"(q[0].y), "f"(q[1].x), "f"(q[1].y), "f"(q[2].x), "f"(q[2].y), "f"(q[3].x), "f"(q[3].y));
+    return c;
 }
 
 }  // namespace

@@ -1,14 +1,17 @@
 // Appending keys and values to the 4-bit cache, the keys rotated on the way,
 // and the cache's inspection.
 //
-// One warp writes one group: 16 positions of a head, keys and values.  Its
-// image is put together in shared memory and stored as whole 16-byte pieces;
-// of a group that is not new all through, the pieces that a new position
-// touches are read first and the rest left alone, so no atomics and no other
-// position's bytes change.  Heads run fastest over the blocks, so that the
-// heads of a token find its cos and sin in L2.
-// Bound by HBM: 512 bytes in and 144 out for a token and head (and 512 of
-// tables a token), about 60 warp-instructions.
+// A group's image is put together in shared memory and stored as whole 16-byte
+// pieces; of a group that is not new all through, the pieces that a new
+// position touches are read first and the rest left alone, so no atomics and
+// no other position's bytes change.  Heads run fastest over the blocks, so
+// that the heads of a token find its cos and sin in L2.  Two kernels:
+//   few groups   a block a group: eight threads a position for its keys, eight
+//                for two positions' values (they share bytes), so that a thread
+//                waits for its loads once (one token of 32 x 8 heads 3.4 us,
+//                the other kernel 5.9)
+//   many         a warp a group, its rows' loads all on their way at once
+// Floor: 512 bytes in and 144 out for a token and head, 512 of tables a token.
 #include <cuda_fp16.h>
 
 #include "fp4.cuh"
@@ -16,7 +19,7 @@
 namespace bgtq {
 namespace {
 
-constexpr int kApWarps = 4;
+constexpr int kKeyThreads = 8 * kGroup, kApThreads = kKeyThreads + 4 * kGroup;
 
 struct Fp4AppendParams {
     RopeParams rope;
@@ -36,14 +39,159 @@ __device__ __forceinline__ uint32_t piece_positions(int i) {
     return 0x303u << (2 * ((i - 136) >> 1));
 }
 
-__device__ __forceinline__ void load16(const __half* row, int d, uint32_t (&w)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(row + d), b = *reinterpret_cast<const uint4*>(row + d + 8);
-    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+__device__ __forceinline__ void load8(const __half* row, int d, uint32_t (&w)[4]) {
+    const uint4 a = *reinterpret_cast<const uint4*>(row + d);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
 }
 
-__global__ void __launch_bounds__(32 * kApWarps) fp4_append_kernel(const __grid_constant__ Fp4AppendParams p) {
-    __shared__ __align__(16) uint8_t s_img[kApWarps][kGroupBytes];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+// Codes of a piece of 8 key values (dims d .. d + 7 of position t) and, with the
+// block's first half, its scale byte.
+__device__ __forceinline__ void put_keys(uint8_t* img, int t, int d, const uint32_t (&x)[4], uint32_t byte, const Fp4Recip& r) {
+    const uint32_t code = fp4_encode8(x, r);
+    uint16_t* dst = reinterpret_cast<uint16_t*>(img + 64 * t + 32 * (d >> 3 & 1) + 2 * (d >> 4));
+    dst[0] = (uint16_t)code;
+    dst[8] = (uint16_t)(code >> 16);
+    if (!(d & 8)) img[kGroupKs + 8 * t + (d >> 4)] = (uint8_t)byte;
+}
+
+// Block j of the values of positions t and t + 1 (t even; x: 16 values of each)
+// of which those in `two` are new.
+__device__ __forceinline__ void put_values(uint8_t* img, int t, int j, uint32_t two, const uint32_t (&x)[2][2][4]) {
+    const int pc = (t >> 1) & 3, th = t >> 3;
+    uint32_t code[2][2], s[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        s[e] = fp4_scale_byte(fmaxf(fp4_amax(x[e][0]), fp4_amax(x[e][1])));
+        const Fp4Recip r(s[e]);
+        code[e][0] = fp4_encode8(x[e][0], r);
+        code[e][1] = fp4_encode8(x[e][1], r);
+    }
+    uint16_t* dst = reinterpret_cast<uint16_t*>(img + kGroupV + 512 * (j >> 2) + 16 * pc + 4 * (j & 3) + 2 * th);
+    // byte of dim g of either half of the block: the two positions' codes
+    constexpr uint32_t kEven = 0x0f0f0f0fu;
+    uint32_t even[2], odd[2];  // dims 0 2 4 6 and 1 3 5 7 of both halves
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+        even[hh] = (code[0][hh] & kEven) | ((code[1][hh] & kEven) << 4);
+        odd[hh] = ((code[0][hh] >> 4) & kEven) | (code[1][hh] & ~kEven);
+    }
+    uint8_t* sd = img + kGroupVs + 32 * pc + 4 * j + 2 * th;
+    if (two == 3u) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t(&y)[2] = (i & 1) ? odd : even;
+            dst[32 * i] = (uint16_t)__byte_perm(y[0], y[1], (i >> 1) | (4 + (i >> 1)) << 4 | 0x4400u);
+        }
+        *reinterpret_cast<uint16_t*>(sd) = (uint16_t)(s[0] | s[1] << 8);
+    } else {
+        const uint32_t keep = two == 1u ? 0xf0f0u : 0x0f0fu;  // nibbles of the other position
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t(&y)[2] = (i & 1) ? odd : even;
+            const uint32_t u = __byte_perm(y[0], y[1], (i >> 1) | (4 + (i >> 1)) << 4 | 0x4400u);
+            dst[32 * i] = (uint16_t)((u & ~keep) | (dst[32 * i] & keep));
+        }
+        if (two & 1u) sd[0] = (uint8_t)s[0];
+        if (two & 2u) sd[1] = (uint8_t)s[1];
+    }
+}
+
+__global__ void __launch_bounds__(kApThreads, 7) fp4_append_kernel(const __grid_constant__ Fp4AppendParams p) {
+    __shared__ __align__(16) uint8_t img[kGroupBytes];
+    __shared__ uint32_t s_fresh[kKeyThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int h = (int)(blockIdx.x % (unsigned)p.map.H), b = blockIdx.y;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int ps = p.pos_start[b];
+    if (ps < 0 || (int64_t)ps + p.t_new > p.cap) {
+        if (blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_APPEND_CAPACITY);
+        return;
+    }
+    const int64_t end = (int64_t)ps + p.t_new;
+    const int64_t gi = (ps >> 4) + (int64_t)(blockIdx.x / (unsigned)p.map.H);
+    if (gi * kGroup >= end) return;
+    const int row0 = (int)(gi * kGroup - ps);  // row of the group's first position (may be negative)
+    uint8_t* g = p.map.group(b, h, gi);
+    if (!g) {
+        if (tid == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
+        return;
+    }
+    // positions of the group that are given (bit i: position 16 gi + i)
+    const int given_lo = max(0, -row0), given_hi = min(kGroup, p.t_new - row0);
+    const uint32_t given = ((1u << given_hi) - 1u) & ~((1u << given_lo) - 1u);
+    // ---- loads, pieces of 8 values.  Keys: thread i of a position has both dims of
+    // blocks 8 i .. 8 i + 7; values: thread i has dims 16 i .. of two positions.
+    const bool values = tid >= kKeyThreads;
+    const bool halves = !p.rope.cos || p.rope.layout == 0;
+    const int i8 = tid & 7, t = values ? 2 * ((tid - kKeyThreads) >> 3) : tid >> 3;
+    const int da = values ? 16 * i8 : halves ? 8 * i8 : 16 * i8, db = values || !halves ? da + 8 : 64 + 8 * i8;
+    uint32_t x[2][2][4] = {};
+    int rp[2][kMaxAxes];
+    uint32_t two = (given >> t) & (values ? 3u : 1u);  // which of the thread's positions are new
+    {
+        const RowsView& v = values ? p.v : p.k;
+        const __half* base = static_cast<const __half*>(v.p) + b * v.sb + h * v.sh;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if ((two >> e) & 1u) {
+                load8(base + (int64_t)(row0 + t + e) * v.st, da, x[e][0]);
+                load8(base + (int64_t)(row0 + t + e) * v.st, db, x[e][1]);
+            }
+    }
+    uint4 old = make_uint4(0u, 0u, 0u, 0u);
+    const bool keeps = given != 0xffffu && tid < kGroupBytes / 16 && (given & piece_positions(tid));
+    if (keeps) old = reinterpret_cast<const uint4*>(g)[tid];
+    if (p.rope.cos) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            if (((two >> e) & 1u) && !rope_positions(p.rope, (int64_t)b * p.t_new + row0 + t + e, ps + (int64_t)row0 + t + e, rp[e])) {
+                two &= ~(1u << e);
+                if (h == 0 && !values && i8 == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_ROPE_RANGE);
+            }
+        if (!values && (two & 1u)) rope_rotate8(p.rope, rp[0], 8 * i8, x[0][0], x[0][1]);
+    }
+    if (!values) {
+        const uint32_t m = __ballot_sync(0xffffffffu, two & 1u);
+        if (lane == 0) s_fresh[tid >> 5] = (m & 1u) | (m >> 7 & 2u) | (m >> 14 & 4u) | (m >> 21 & 8u);
+    }
+    if (keeps) reinterpret_cast<uint4*>(img)[tid] = old;
+    __syncthreads();
+    const uint32_t fresh = s_fresh[0] | s_fresh[1] << 4 | s_fresh[2] << 8 | s_fresh[3] << 12;
+    if (given == 0xffffu && fresh != 0xffffu) {
+        // (a whole group of which some position is skipped: what is kept, read now)
+        if (tid < kGroupBytes / 16) reinterpret_cast<uint4*>(img)[tid] = reinterpret_cast<const uint4*>(g)[tid];
+        __syncthreads();
+    }
+    // ---- codes into the image
+    if (!values) {
+        // a block's other half is the next lane's, or (neighbouring dims) this lane's own
+        float ma = fp4_amax(x[0][0]), mb = fp4_amax(x[0][1]);
+        if (halves) {
+            ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
+            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+        } else {
+            ma = mb = fmaxf(ma, mb);
+        }
+        if (two & 1u) {
+            const uint32_t sa = fp4_scale_byte(ma), sb = halves ? fp4_scale_byte(mb) : sa;
+            put_keys(img, t, da, x[0][0], sa, Fp4Recip(sa));
+            put_keys(img, t, db, x[0][1], sb, Fp4Recip(sb));
+        }
+    } else if (two) {
+        put_values(img, t, i8, two, x);
+    }
+    __syncthreads();
+    if (tid < kGroupBytes / 16 && (fresh & piece_positions(tid)))
+        reinterpret_cast<uint4*>(g)[tid] = reinterpret_cast<const uint4*>(img)[tid];
+}
+
+constexpr int kBulkWarps = 4;
+
+template <bool kRope, bool kHalves>  // kHalves: both dims of a rotary block are 64 apart (layout 0), or there is none
+__global__ void __launch_bounds__(32 * kBulkWarps) fp4_append_bulk_kernel(const __grid_constant__ Fp4AppendParams p) {
+    __shared__ __align__(16) uint8_t s_img[kBulkWarps][kGroupBytes];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i8 = lane & 7;
     const int h = (int)(blockIdx.x % (unsigned)p.map.H), b = blockIdx.y;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -53,105 +201,109 @@ __global__ void __launch_bounds__(32 * kApWarps) fp4_append_kernel(const __grid_
         return;
     }
     const int64_t end = (int64_t)ps + p.t_new;
-    const int64_t gi = (ps >> 4) + (int64_t)(blockIdx.x / (unsigned)p.map.H) * kApWarps + warp;
+    const int64_t gi = (ps >> 4) + (int64_t)(blockIdx.x / (unsigned)p.map.H) * kBulkWarps + warp;
     if (gi * kGroup >= end) return;
-    // which of the group's positions are new (bit i: position 16 gi + i)
-    int rp[kMaxAxes] = {};
-    bool mine = false;
-    if (lane < kGroup) {
-        const int64_t pos = gi * kGroup + lane;
-        mine = pos >= ps && pos < end;
-        if (mine && p.rope.cos && !rope_positions(p.rope, (int64_t)b * p.t_new + (pos - ps), pos, rp)) {
-            mine = false;
-            if (h == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_ROPE_RANGE);
+    const int row0 = (int)(gi * kGroup - ps);  // row of the group's first position (may be negative)
+    const int given_lo = max(0, -row0), given_hi = min(kGroup, p.t_new - row0);
+    const uint32_t given = ((1u << given_hi) - 1u) & ~((1u << given_lo) - 1u);
+    // ---- loads.  Keys: lanes 8 x .. 8 x + 7 have position 4 it + x, lane i both dims of
+    // its blocks 8 i ..; values: lane (x, i) dims 16 i .. of positions 2 x + 8 it (+ 1)
+    const int ka = kHalves ? 8 * i8 : 16 * i8, kb = kHalves ? 64 + 8 * i8 : 16 * i8 + 8;
+    const __half* kp = static_cast<const __half*>(p.k.p) + b * p.k.sb + h * p.k.sh + (int64_t)row0 * p.k.st;
+    const __half* vp = static_cast<const __half*>(p.v.p) + b * p.v.sb + h * p.v.sh + (int64_t)row0 * p.v.st;
+    uint32_t kx[4][2][4], vx[2][2][2][4];
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+        const int t = 4 * it + (lane >> 3);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) kx[it][0][e] = kx[it][1][e] = 0u;
+        if ((given >> t) & 1u) {
+            load8(kp + t * p.k.st, ka, kx[it][0]);
+            load8(kp + t * p.k.st, kb, kx[it][1]);
         }
     }
-    const uint32_t fresh = __ballot_sync(0xffffffffu, mine);
-    if (fresh == 0) return;
+    // a position's row in the tables, by the lane of that number
+    int rp[kMaxAxes] = {};
+    bool mine = lane < kGroup && ((given >> lane) & 1u);
+    if (kRope && mine && !rope_positions(p.rope, (int64_t)b * p.t_new + row0 + lane, (int64_t)ps + row0 + lane, rp)) {
+        mine = false;
+        rp[0] = rp[1] = rp[2] = rp[3] = 0;  // (loaded, not used)
+        if (h == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_ROPE_RANGE);
+    }
+    // cos and sin of a pass, one pass ahead
+    auto tables = [&](RopeTurn& turn, int it) {
+        const int t = 4 * it + (lane >> 3);
+        int tp[kMaxAxes];
+        tp[0] = tp[1] = tp[2] = tp[3] = __shfl_sync(0xffffffffu, rp[0], t);
+        if (p.rope.axes > 1) {
+#pragma unroll
+            for (int e = 1; e < kMaxAxes; ++e) tp[e] = __shfl_sync(0xffffffffu, rp[e], t);
+        }
+        turn.load(p.rope, tp, 8 * i8);
+    };
+    RopeTurn turn;
+    if constexpr (kRope) tables(turn, 0);
+#pragma unroll
+    for (int it = 0; it < 2; ++it)
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int t = 2 * (lane >> 3) + 8 * it + n;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) vx[it][n][0][e] = vx[it][n][1][e] = 0u;
+            if ((given >> t) & 1u) {
+                load8(vp + t * p.v.st, 16 * i8, vx[it][n][0]);
+                load8(vp + t * p.v.st, 16 * i8 + 8, vx[it][n][1]);
+            }
+        }
     uint8_t* g = p.map.group(b, h, gi);
     if (!g) {
         if (lane == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
         return;
     }
+    const uint32_t fresh = __ballot_sync(0xffffffffu, mine);
     uint8_t* img = s_img[warp];
     if (fresh != 0xffffu) {
         for (int i = lane; i < kGroupBytes / 16; i += 32)
             if (fresh & piece_positions(i)) reinterpret_cast<uint4*>(img)[i] = reinterpret_cast<const uint4*>(g)[i];
         __syncwarp();
     }
-    const int64_t row0 = gi * kGroup - ps;  // row of the group's first position
-    // ---- keys: a lane takes blocks j and j + 4 of a token (both dims of a
-    // rotary block in either layout)
-    const __half* kb = static_cast<const __half*>(p.k.p) + b * p.k.sb + h * p.k.sh;
 #pragma unroll
-    for (int it = 0; it < 2; ++it) {
-        const int t = 8 * it + (lane >> 2), j = lane & 3;
-        int tp[kMaxAxes];
-        if (p.rope.cos) {
-#pragma unroll
-            for (int a = 0; a < kMaxAxes; ++a) tp[a] = __shfl_sync(0xffffffffu, rp[a], t);
+    for (int it = 0; it < 4; ++it) {
+        const int t = 4 * it + (lane >> 3);
+        const bool is_new = (fresh >> t) & 1u;
+        if constexpr (kRope) {
+            RopeTurn next;
+            if (it < 3) tables(next, it + 1);
+            rope_turn8(turn, kHalves, kx[it][0], kx[it][1]);
+            turn = next;
         }
-        if (!((fresh >> t) & 1u)) continue;
-        const __half* row = kb + (row0 + t) * p.k.st;
-        uint32_t a[8], c[8];
-        load16(row, 16 * j, a);
-        load16(row, 64 + 16 * j, c);
-        if (p.rope.cos) {
-            uint32_t(&a0)[4] = *reinterpret_cast<uint32_t(*)[4]>(&a[0]);
-            uint32_t(&a1)[4] = *reinterpret_cast<uint32_t(*)[4]>(&a[4]);
-            uint32_t(&c0)[4] = *reinterpret_cast<uint32_t(*)[4]>(&c[0]);
-            uint32_t(&c1)[4] = *reinterpret_cast<uint32_t(*)[4]>(&c[4]);
-            if (p.rope.layout == 0) {
-                rope_rotate8(p.rope, tp, 16 * j, a0, c0);
-                rope_rotate8(p.rope, tp, 16 * j + 8, a1, c1);
-            } else {
-                rope_rotate8(p.rope, tp, 8 * j, a0, a1);
-                rope_rotate8(p.rope, tp, 32 + 8 * j, c0, c1);
-            }
+        // a block's other half is the next lane's, or (neighbouring dims) this lane's own
+        float ma = fp4_amax(kx[it][0]), mb = fp4_amax(kx[it][1]);
+        if constexpr (kHalves) {
+            ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1));
+            mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+        } else {
+            ma = mb = fmaxf(ma, mb);
         }
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t code[2];
-            const uint32_t s = fp4_encode(half ? c : a, code);
-            uint16_t* dst = reinterpret_cast<uint16_t*>(img + 64 * t + 2 * (j + 4 * half));
-            dst[0] = (uint16_t)code[0];
-            dst[8] = (uint16_t)(code[0] >> 16);
-            dst[16] = (uint16_t)code[1];
-            dst[24] = (uint16_t)(code[1] >> 16);
-            img[kGroupKs + 8 * t + j + 4 * half] = (uint8_t)s;
+        if (is_new) {
+            const uint32_t sa = fp4_scale_byte(ma), sb = kHalves ? fp4_scale_byte(mb) : sa;
+            put_keys(img, t, ka, kx[it][0], sa, Fp4Recip(sa));
+            put_keys(img, t, kb, kx[it][1], sb, Fp4Recip(sb));
         }
     }
-    // ---- values: a lane takes block j of two neighbouring tokens, which share bytes
-    const __half* vb = static_cast<const __half*>(p.v.p) + b * p.v.sb + h * p.v.sh;
 #pragma unroll
     for (int it = 0; it < 2; ++it) {
-        const int pc = lane >> 3, j = lane & 7, t = 2 * pc + 8 * it;
+        const int t = 2 * (lane >> 3) + 8 * it;
         const uint32_t two = (fresh >> t) & 3u;
-        if (two == 0) continue;
-        uint32_t code[2][2] = {}, s[2] = {};
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            if (!((two >> n) & 1u)) continue;
-            uint32_t w[8];
-            load16(vb + (row0 + t + n) * p.v.st, 16 * j, w);
-            s[n] = fp4_encode(w, code[n]);
-        }
-        uint16_t* dst = reinterpret_cast<uint16_t*>(img + kGroupV + 512 * (j >> 2) + 16 * pc + 4 * (j & 3) + 2 * it);
-        const uint32_t keep = two == 3u ? 0u : two == 1u ? 0xf0f0u : 0x0f0fu;  // nibbles of the other token
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint32_t u = ((code[0][0] >> (4 * i)) & 15u) | ((code[1][0] >> (4 * i)) & 15u) << 4 |
-                         ((code[0][1] >> (4 * i)) & 15u) << 8 | ((code[1][1] >> (4 * i)) & 15u) << 12;
-            if (keep) u |= dst[32 * i] & keep;
-            dst[32 * i] = (uint16_t)u;
-        }
-        uint8_t* sd = img + kGroupVs + 32 * pc + 4 * j + 2 * it;
-        if (two & 1u) sd[0] = (uint8_t)s[0];
-        if (two & 2u) sd[1] = (uint8_t)s[1];
+        if (two) put_values(img, t, i8, two, vx[it]);
     }
     __syncwarp();
-    for (int i = lane; i < kGroupBytes / 16; i += 32)
-        if (fresh & piece_positions(i)) reinterpret_cast<uint4*>(g)[i] = reinterpret_cast<const uint4*>(img)[i];
+#pragma unroll
+    for (int i = 0; i < (kGroupBytes / 16 + 31) / 32; ++i) {
+        const int at = lane + 32 * i;
+        if (at < kGroupBytes / 16 && (fresh & piece_positions(at)))
+            reinterpret_cast<uint4*>(g)[at] = reinterpret_cast<const uint4*>(img)[at];
+    }
 }
 
 // One thread a dim of a position.
@@ -194,17 +346,24 @@ cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsVie
     p.pos_start = pos_start;
     p.status = status;
     const int64_t groups = ((int64_t)t_new + 14) / kGroup + 1;  // that t_new positions can touch
-    const int64_t blocks = (groups + kApWarps - 1) / kApWarps * c.n_heads;
+    // Up to two waves of blocks (8 x 152): the block-a-group kernel's short chain of
+    // waits; beyond, the work counts (131043 tokens x 2 heads: 64 us with a block
+    // a group, whose six warps each pay for the set-up).
+    const bool bulk = groups * c.n_heads * batch > 16 * 152;
+    const int64_t blocks = (bulk ? (groups + kBulkWarps - 1) / kBulkWarps : groups) * c.n_heads;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, (unsigned)batch, 1);
-    cfg.blockDim = dim3(32 * kApWarps, 1, 1);
+    cfg.blockDim = dim3(bulk ? 32 * kBulkWarps : kApThreads, 1, 1);
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fp4_append_kernel, p);
+    if (!bulk) return cudaLaunchKernelEx(&cfg, fp4_append_kernel, p);
+    if (!r.cos) return cudaLaunchKernelEx(&cfg, fp4_append_bulk_kernel<false, true>, p);
+    return r.layout == 0 ? cudaLaunchKernelEx(&cfg, fp4_append_bulk_kernel<true, true>, p)
+                         : cudaLaunchKernelEx(&cfg, fp4_append_bulk_kernel<true, false>, p);
 }
 
 cudaError_t launch_fp4_dequant(cudaStream_t s, const bgtq_fp4_cache& c, int b, int head, int64_t t0, int64_t t1, float* k_out,

@@ -7,8 +7,10 @@
 //
 // rope_rows: bound by HBM (each row read and written once, 3 flops an
 // element).  A thread takes 8 blocks of one token (16 elements of a row), reads
-// their cos and sin once and turns them in a share of the token's heads, four
+// their cos and sin once and turns them in a share of the token's heads, two
 // rows in flight; few tokens are shared out over more threads, head by head.
+// 32768 tokens x 18 heads: 49.6 us, 0.95 of measured HBM (four rows in flight:
+// 52.8, their registers halve the warps; 256 threads: 55.6).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -95,9 +97,9 @@ struct RowsParams {
     int32_t* status;
 };
 
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
 constexpr int kRowLanes = 8;  // threads of a token and share
-constexpr int kRowBatch = 4;  // rows a thread has in flight
+constexpr int kRowBatch = 2;  // rows a thread has in flight
 
 template <class In, class Out>
 __global__ void __launch_bounds__(kRowThreads) rope_rows_kernel(const __grid_constant__ RowsParams p) {

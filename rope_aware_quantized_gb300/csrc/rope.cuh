@@ -9,6 +9,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <limits.h>
 
 #include "bgtq_internal.h"
 
@@ -59,15 +60,43 @@ int check_rows(const bgtq_rows* r, const char* name, int batch, int heads, int64
 #ifdef __CUDACC__
 namespace {
 
+// Two floats as one operand: each operation rounds both as its scalar does.
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 halves2(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
 // The row's position on each axis; false when one lies outside the tables.
 __device__ __forceinline__ bool rope_positions(const RopeParams& r, int64_t row, int64_t own, int (&pos)[kMaxAxes]) {
+    if (!r.pos || r.axes == 1) {
+        // (one axis, or the row's own position on all of them)
+        const int v = r.pos ? r.pos[row] : own < INT_MAX ? (int)own : -1;
+#pragma unroll
+        for (int a = 0; a < kMaxAxes; ++a) pos[a] = v;
+        return (uint32_t)v < (uint32_t)r.n_pos;
+    }
     bool ok = true;
 #pragma unroll
     for (int a = 0; a < kMaxAxes; ++a) {
-        int64_t v = own;
-        if (r.pos) v = a < r.axes ? r.pos[a * r.pos_rows + row] : r.pos[row];
-        ok = ok && v >= 0 && v < r.n_pos;
-        pos[a] = (int)v;
+        const int v = r.pos[a < r.axes ? a * r.pos_rows + row : row];
+        ok = ok && (uint32_t)v < (uint32_t)r.n_pos;
+        pos[a] = v;
     }
     return ok;
 }
@@ -79,7 +108,7 @@ __device__ __forceinline__ int rope_pick(const int (&pos)[kMaxAxes], uint32_t a)
 // cos and sin of blocks i0 .. i0 + 3 (i0 a multiple of 4) at the row's
 // positions: one 16-byte load each when the four lie on one axis.
 __device__ __forceinline__ void rope_load4(const RopeParams& r, const int (&pos)[kMaxAxes], int i0, float (&c)[4], float (&s)[4]) {
-    const uint32_t ax = (r.axis2[i0 >> 4] >> (2 * (i0 & 15))) & 0xffu;
+    const uint32_t ax = r.axes == 1 ? 0u : (r.axis2[i0 >> 4] >> (2 * (i0 & 15))) & 0xffu;
     if (ax == (ax & 3u) * 0x55u) {
         const int64_t at = (int64_t)rope_pick(pos, ax & 3u) * kNB + i0;
         const float4 cv = __ldg(reinterpret_cast<const float4*>(r.cos + at));
@@ -119,32 +148,49 @@ __device__ __forceinline__ uint32_t rope_h2(float a, float b) {
 }
 __device__ __forceinline__ float2 rope_f2(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
 
-// Rotate blocks i0 .. i0 + 7 of an fp16 row held as 8 words: layout 0, a =
-// dims i0 .. i0 + 7 and b = dims 64 + i0 ..; layout 1, a and b = dims 2 i0 .. 2 i0 + 15.
-__device__ __forceinline__ void rope_rotate8(const RopeParams& r, const int (&pos)[kMaxAxes], int i0, uint32_t (&a)[4], uint32_t (&b)[4]) {
+// cos and sin of blocks i0 .. i0 + 7.
+struct RopeTurn {
+    float c[8], s[8];
+    __device__ __forceinline__ void load(const RopeParams& r, const int (&pos)[kMaxAxes], int i0) {
+        rope_load4(r, pos, i0, *reinterpret_cast<float(*)[4]>(&c[0]), *reinterpret_cast<float(*)[4]>(&s[0]));
+        rope_load4(r, pos, i0 + 4, *reinterpret_cast<float(*)[4]>(&c[4]), *reinterpret_cast<float(*)[4]>(&s[4]));
+    }
+};
+
+// Turn blocks i0 .. i0 + 7 of an fp16 row held as 8 words: halves, a = dims i0
+// .. i0 + 7 and b = dims 64 + i0 .. (layout 0); else a and b = dims 2 i0 .. 2 i0 + 15.
+__device__ __forceinline__ void rope_turn8(const RopeTurn& t, bool halves, uint32_t (&a)[4], uint32_t (&b)[4]) {
+    if (halves) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        float c[4], s[4];
-        rope_load4(r, pos, i0 + 4 * k, c, s);
-        if (r.layout == 0) {
+        for (int m = 0; m < 4; ++m) {
+            const float2 x = rope_f2(a[m]), y = rope_f2(b[m]);
+            const uint64_t lo = pair2(x.x, x.y), hi = pair2(y.x, y.y);
+            const uint64_t cc = pair2(t.c[2 * m], t.c[2 * m + 1]), ss = pair2(t.s[2 * m], t.s[2 * m + 1]);
+            // (the sums one by one: a packed product and a packed sum came out as one
+            // rounding where the compiler may contract them)
+            const float2 lc = halves2(mul_pair(lo, cc)), hs = halves2(mul_pair(hi, ss));
+            const float2 hc = halves2(mul_pair(hi, cc)), ls = halves2(mul_pair(lo, ss));
+            a[m] = rope_h2(__fsub_rn(lc.x, hs.x), __fsub_rn(lc.y, hs.y));
+            b[m] = rope_h2(__fadd_rn(hc.x, ls.x), __fadd_rn(hc.y, ls.y));
+        }
+    } else {
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-                float2 lo = rope_f2(a[2 * k + m]), hi = rope_f2(b[2 * k + m]);
-                rope_pair(lo.x, hi.x, c[2 * m], s[2 * m]);
-                rope_pair(lo.y, hi.y, c[2 * m + 1], s[2 * m + 1]);
-                a[2 * k + m] = rope_h2(lo.x, lo.y);
-                b[2 * k + m] = rope_h2(hi.x, hi.y);
-            }
-        } else {
+        for (int k = 0; k < 2; ++k) {
             uint32_t(&w)[4] = k ? b : a;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 float2 x = rope_f2(w[m]);
-                rope_pair(x.x, x.y, c[m], s[m]);
+                rope_pair(x.x, x.y, t.c[4 * k + m], t.s[4 * k + m]);
                 w[m] = rope_h2(x.x, x.y);
             }
         }
     }
+}
+
+__device__ __forceinline__ void rope_rotate8(const RopeParams& r, const int (&pos)[kMaxAxes], int i0, uint32_t (&a)[4], uint32_t (&b)[4]) {
+    RopeTurn t;
+    t.load(r, pos, i0);
+    rope_turn8(t, r.layout == 0, a, b);
 }
 
 }  // namespace

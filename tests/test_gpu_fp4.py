@@ -179,6 +179,21 @@ def test_append_skips():
     c.page_table.copy_(table)
 
 
+def test_append_skips_inside_whole_groups():
+    rng = np.random.default_rng(6)
+    c = new_cache(2, 1, 96, 0, seed=8)
+    before = c.groups.cpu().numpy()
+    k, v = (rng.standard_normal((1, 2, 70, 128)).astype(np.float16) for _ in range(2))
+    rope = bg.Rope(*bg.bgtq_rope_table(np.zeros(64), 70))
+    pos = np.arange(70)[None]
+    bad = [10, 11, 12, 40, 61]  # a position of one group, neighbours that share bytes; cache positions 13 .. 64
+    pos[0, bad] = [70, -1, 1 << 30, 71, -9]
+    st = status()
+    bg.bgtq_fp4_append(torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), i32([3]), c, rope=rope, pos=i32(pos), status=st)
+    assert st.item() == bg.STATUS_ROPE_RANGE
+    check_bytes(before, c, k, v, [3], lambda b, t: t not in bad)
+
+
 def test_dequant():
     c = new_cache(2, 2, 64, 16, seed=3)
     c.groups.view(-1, F.GROUP_BYTES)[:, 2048:] %= 227
