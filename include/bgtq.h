@@ -717,10 +717,13 @@ int bgtq_fp4_attn_workspace(int n_kv_heads, int group, int batch, int t, int64_t
  *              (1), 16-byte aligned
  *   workspace  device, 256-byte aligned, bgtq_fp4_attn_workspace bytes; two
  *              calls that may overlap on the GPU need two
- * Logits are fp16 products summed in fp32, probabilities taken in 22 bits.
+ * Logits are fp16 products summed in fp32, probabilities taken in 22 bits (two
+ * fp16 parts); with more than 16 rows a KV head (t * group) and an fp16 output
+ * they may be rounded to fp16, as in bgtq_prefill_attn.
  * Positions from n on, and their bytes, do not matter.
  * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (more than 65535 sequences,
- * batch * H > 65535, sizes past 2^31 rows), CUDA.
+ * batch * H > 65535, batch * H * max_len >=
+ * 2^34, sizes past 2^31 rows), CUDA.
  */
 int bgtq_fp4_attn(void* stream, const bgtq_rope* rope, const int32_t* pos, const bgtq_rows* q, int group, int batch,
                   int t, const bgtq_fp4_cache* cache, const int32_t* seq_lens, int64_t max_len, void* out,

@@ -603,33 +603,50 @@ class Rope:
         self.axis = None if axis is None else np.ascontiguousarray(axis, dtype=np.uint8)
         self.device = cos.get_device()
         self.desc = BgtqRope(cos.data_ptr(), sin.data_ptr(), cos.shape[0], self.axes, _ptr(self.axis), layout)
+        self.address = C.addressof(self.desc)
 
 
 def _rope_args(rope, pos, batch: int, t: int, dev: int):
-    """The descriptor and the positions' pointer; pos [axes][B][T] int32 (one axis: also [B][T]) or None."""
-    import torch
+    """The addresses of the descriptor and of the positions; pos [axes][B][T] int32 (one axis: also [B][T]) or None."""
     if rope is None:
         if pos is not None:
             raise ValueError("pos without rope")
         return None, None
     if rope.device != dev:
         raise ValueError(f"the rope's tables are on cuda:{rope.device}, the current device is cuda:{dev}")
-    if pos is not None and not (rope.axes == 1 and pos.shape == (batch, t) and pos.dtype == torch.int32 and pos.is_contiguous()
-                                and pos.get_device() == dev):
-        _need(pos, "pos", torch.int32, (rope.axes, batch, t), dev)
-    return C.byref(rope.desc), _ptr(pos)
+    if pos is None:
+        return rope.address, None
+    if (pos.shape == (rope.axes, batch, t) or rope.axes == 1 and pos.shape == (batch, t)) and pos.dtype is _types()[3] \
+            and pos.is_contiguous() and pos.get_device() == dev:
+        return rope.address, pos.data_ptr()
+    _need(pos, "pos", _types()[3], (rope.axes, batch, t), dev)
+    return rope.address, pos.data_ptr()
+
+
+_TYPES = None
+
+
+def _types():
+    """(float16, float32, bfloat16, int32) of torch: the first three in the order of the library's numbers for them."""
+    global _TYPES
+    if _TYPES is None:
+        import torch
+        _TYPES = (torch.float16, torch.float32, torch.bfloat16, torch.int32)
+    return _TYPES
 
 
 def _rows(x, name: str, dtype, shape, dev: int) -> BgtqRows:
     """Rows of a [B][heads][T][128] tensor of any strides but the innermost."""
-    if (dtype is not None and x.dtype != dtype) or x.shape != shape:
-        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)}")
+    sb, sh, st, inner = x.stride() if x.dim() == 4 else (0, 0, 0, 0)
+    if x.dtype is dtype and x.shape == shape and inner == 1 and x.get_device() == dev:
+        return BgtqRows(x.data_ptr(), sb, sh, st)
+    if x.dtype != dtype or tuple(x.shape) != shape:
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {shape}")
     if x.get_device() != dev:
         raise ValueError(f"{name} must be a CUDA tensor on the current device")
-    st = x.stride()
-    if st[3] != 1 and x.numel():
+    if x.numel():
         raise ValueError(f"{name}: the 128 elements of a row must be contiguous")
-    return BgtqRows(x.data_ptr(), st[0], st[1], st[2])
+    return BgtqRows(x.data_ptr(), sb, sh, st)
 
 
 def bgtq_rope_table(inv_freq, n_pos: int, scale: float = 1.0, device="cuda", stream=None):
@@ -653,11 +670,14 @@ def _device_is_current(x, name: str):
 
 
 def _row_dtype(x) -> int:
-    import torch
-    try:
-        return {torch.float16: 0, torch.float32: 1, torch.bfloat16: 2}[x.dtype]
-    except KeyError:
-        raise ValueError("rows must be float16, float32 or bfloat16") from None
+    f16, f32, bf16, _ = _types()
+    if x.dtype is f16:
+        return 0
+    if x.dtype is f32:
+        return 1
+    if x.dtype is bf16:
+        return 2
+    raise ValueError("rows must be float16, float32 or bfloat16")
 
 
 def bgtq_rope_rows(rope: Rope, pos, q, q_out, k=None, k_out=None, inverse: bool = False, status=None, stream=None):
@@ -667,22 +687,28 @@ def bgtq_rope_rows(rope: Rope, pos, q, q_out, k=None, k_out=None, inverse: bool 
     one for q_out and k_out, which may be q and k themselves.  pos: [axes][B][T] int32, or [B][T] with
     one axis; a row with a position outside the tables is not written.  inverse: rotate back (the
     gradient of the rotation)."""
-    b, nq, t, _ = q.shape
-    dev = _device(q)
-    rd, pp = _rope_args(rope, pos, b, t, dev)
     if rope is None or pos is None:
         raise ValueError("rope and pos are needed")
     if (k is None) != (k_out is None):
         raise ValueError("k and k_out are given together or not at all")
-    qi, qo = _rows(q, "q", None, (b, nq, t, HEAD_DIM), dev), _rows(q_out, "q_out", None, (b, nq, t, HEAD_DIM), dev)
-    nk, ki, ko = 0, None, None
-    if k is not None:
+    b, nq, t, _ = q.shape
+    dev = _device(q)
+    rd, pp = _rope_args(rope, pos, b, t, dev)
+    shape = (b, nq, t, HEAD_DIM)
+    qi, qo = _rows(q, "q", q.dtype, shape, dev), _rows(q_out, "q_out", q_out.dtype, shape, dev)
+    if k is None:
+        nk, ki, ko = 0, None, None
+    else:
         nk = k.shape[1]
-        ki, ko = _rows(k, "k", q.dtype, (b, nk, t, HEAD_DIM), dev), _rows(k_out, "k_out", q_out.dtype, (b, nk, t, HEAD_DIM), dev)
-    _on_device(None, status, dev)
-    _check(lib().bgtq_rope_rows(_stream(stream, dev), rd, pp, b, t, C.byref(qi), C.byref(qo), nq,
-                                None if ki is None else C.byref(ki), None if ko is None else C.byref(ko), nk,
-                                _row_dtype(q), _row_dtype(q_out), 1 if inverse else 0, _ptr(status)))
+        shape = (b, nk, t, HEAD_DIM)
+        kr, kro = _rows(k, "k", q.dtype, shape, dev), _rows(k_out, "k_out", q_out.dtype, shape, dev)
+        ki, ko = C.addressof(kr), C.addressof(kro)
+    if status is not None:
+        _on_device(None, status, dev)
+    rc = lib().bgtq_rope_rows(_stream(stream, dev), rd, pp, b, t, C.addressof(qi), C.addressof(qo), nq, ki, ko, nk, _row_dtype(q),
+                              _row_dtype(q_out), 1 if inverse else 0, _ptr(status))
+    if rc:
+        _check(rc)
 
 
 def bgtq_rope_append(plan: Plan, rope: Rope, pos, k, v, pos_start, cache: Cache, status=None, stream=None):
@@ -690,20 +716,20 @@ def bgtq_rope_append(plan: Plan, rope: Rope, pos, k, v, pos_start, cache: Cache,
     strides but the innermost): rotated by pos ([axes][B][T_new] int32, [B][T_new] with one axis, None:
     pos_start[b] + i) to float16 on the way, the same records as the two calls.  A token with a
     position outside the tables is not appended."""
-    import torch
-    b, h, t, _ = k.shape
-    dev = _device(k)
-    shape = (b, plan.n_kv_heads, t, HEAD_DIM)
-    kr, vr = _rows(k, "k", torch.float16, shape, dev), _rows(v, "v", torch.float16, shape, dev)
     if rope is None:
         raise ValueError("rope is needed")
+    f16, _, _, i32 = _types()
+    b, _, t, _ = k.shape
+    dev = _device(k)
+    shape = (b, plan.n_kv_heads, t, HEAD_DIM)
+    kr, vr = _rows(k, "k", f16, shape, dev), _rows(v, "v", f16, shape, dev)
     rd, pp = _rope_args(rope, pos, b, t, dev)
-    _need(pos_start, "pos_start", torch.int32, (b,), dev)
+    _need(pos_start, "pos_start", i32, (b,), dev)
     _on_device(cache, status, dev)
     if cache.batch < b:
         raise ValueError("the cache holds fewer sequences than k")
-    _check(lib().bgtq_rope_append(plan.handle, _stream(stream, dev), rd, pp, C.byref(kr), C.byref(vr), b, t, _ptr(pos_start),
-                                  C.byref(cache.desc), _ptr(status)))
+    _check(lib().bgtq_rope_append(plan.handle, _stream(stream, dev), rd, pp, C.addressof(kr), C.addressof(vr), b, t,
+                                  pos_start.data_ptr(), C.byref(cache.desc), _ptr(status)))
 
 
 # ----------------------------------------------------------------------------- the 4-bit cache
@@ -739,6 +765,7 @@ class Fp4Cache:
         self.groups = torch.zeros(n, dtype=torch.uint8, device=device)
         self.desc = BgtqFp4Cache(self.groups.data_ptr(), capacity, n_kv_heads, _ptr(self.page_table), self.max_pages,
                                  page_tokens, self.n_pages)
+        self.address = C.addressof(self.desc)
 
     def nbytes(self) -> int:
         return self.groups.numel()
@@ -749,22 +776,23 @@ def _on_fp4(cache: Fp4Cache, batch: int, status, dev: int):
         raise ValueError(f"the cache is on {cache.groups.device}, the current device is cuda:{dev}")
     if cache.batch < batch:
         raise ValueError("the cache holds fewer sequences than the call")
-    _on_device(None, status, dev)
+    if status is not None:
+        _on_device(None, status, dev)
 
 
 def bgtq_fp4_append(k, v, pos_start, cache: Fp4Cache, rope: Rope | None = None, pos=None, status=None, stream=None):
     """Encode and store new tokens (k, v [B][H][T_new][128] float16 of any strides but the innermost) at
     positions pos_start[b] ..; with rope the keys are rotated on the way, pos as in bgtq_rope_append."""
-    import torch
-    b, h, t, _ = k.shape
+    f16, _, _, i32 = _types()
+    b, _, t, _ = k.shape
     dev = _device(k)
     shape = (b, cache.n_kv_heads, t, HEAD_DIM)
-    kr, vr = _rows(k, "k", torch.float16, shape, dev), _rows(v, "v", torch.float16, shape, dev)
+    kr, vr = _rows(k, "k", f16, shape, dev), _rows(v, "v", f16, shape, dev)
     rd, pp = _rope_args(rope, pos, b, t, dev)
-    _need(pos_start, "pos_start", torch.int32, (b,), dev)
+    _need(pos_start, "pos_start", i32, (b,), dev)
     _on_fp4(cache, b, status, dev)
-    _check(lib().bgtq_fp4_append(_stream(stream, dev), rd, pp, C.byref(kr), C.byref(vr), b, t, _ptr(pos_start),
-                                 C.byref(cache.desc), _ptr(status)))
+    _check(lib().bgtq_fp4_append(_stream(stream, dev), rd, pp, C.addressof(kr), C.addressof(vr), b, t, pos_start.data_ptr(),
+                                 cache.address, _ptr(status)))
 
 
 def bgtq_fp4_attn_workspace(n_kv_heads: int, group: int, batch: int, t: int, max_len: int) -> int:
@@ -781,21 +809,23 @@ def bgtq_fp4_attn(q, cache: Fp4Cache, seq_lens, max_len: int, out, workspace, ro
     seq_len - T + i, sees the positions up to its own.  With rope the queries are rotated on the way, by
     pos ([axes][B][T] int32, [B][T] with one axis) or their own positions.  workspace: a uint8 CUDA
     tensor of bgtq_fp4_attn_workspace bytes, zeroed before its first use."""
-    import torch
+    f16, _, _, i32 = _types()
     if q.dim() == 3:
         q, out = q.unsqueeze(2), out.unsqueeze(2)
     b, hq, t, _ = q.shape
     dev = _device(q)
-    if hq % cache.n_kv_heads or not 1 <= hq // cache.n_kv_heads <= 8:
+    group = hq // cache.n_kv_heads
+    if hq % cache.n_kv_heads or not 1 <= group <= 8:
         raise ValueError("q must have 1 to 8 query heads for each KV head")
-    qr = _rows(q, "q", torch.float16, (b, hq, t, HEAD_DIM), dev)
-    _need(out, "out", out.dtype, (b, hq, t, HEAD_DIM), dev)
+    shape = (b, hq, t, HEAD_DIM)
+    qr = _rows(q, "q", f16, shape, dev)
+    _need(out, "out", out.dtype, shape, dev)
     rd, pp = _rope_args(rope, pos, b, t, dev)
-    _need(seq_lens, "seq_lens", torch.int32, (b,), dev)
+    _need(seq_lens, "seq_lens", i32, (b,), dev)
     _on_fp4(cache, b, status, dev)
     scale = (1.0 / HEAD_DIM ** 0.5) if softmax_scale is None else softmax_scale
-    _check(lib().bgtq_fp4_attn(_stream(stream, dev), rd, pp, C.byref(qr), hq // cache.n_kv_heads, b, t, C.byref(cache.desc),
-                               _ptr(seq_lens), max_len, _ptr(out), _out_dtype(out), scale, _ptr(workspace),
+    _check(lib().bgtq_fp4_attn(_stream(stream, dev), rd, pp, C.addressof(qr), group, b, t, cache.address, seq_lens.data_ptr(),
+                               max_len, out.data_ptr(), _out_dtype(out), scale, workspace.data_ptr(),
                                _scratch(workspace, "workspace", dev), _ptr(status)))
 
 

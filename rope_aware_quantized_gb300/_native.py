@@ -92,19 +92,20 @@ EXPORTS = {
                              C.c_int64, C.c_int64, C.c_int64, C.POINTER(BgtqCache), C.c_void_p, C.c_void_p, C.c_void_p,
                              C.c_void_p]),
     "bgtq_rope_table": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int64, C.c_double, C.c_void_p, C.c_void_p]),
-    "bgtq_rope_rows": (C.c_int, [C.c_void_p, C.POINTER(BgtqRope), C.c_void_p, C.c_int, C.c_int, C.POINTER(BgtqRows),
-                                 C.POINTER(BgtqRows), C.c_int, C.POINTER(BgtqRows), C.POINTER(BgtqRows), C.c_int, C.c_int,
+    # (descriptors as addresses: a small call's conversions cost as much as its checks)
+    "bgtq_rope_rows": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_void_p,
+                                 C.c_void_p, C.c_int, C.c_void_p, C.c_void_p, C.c_int, C.c_int,
                                  C.c_int, C.c_int, C.c_void_p]),
-    "bgtq_rope_append": (C.c_int, [C.c_void_p, C.c_void_p, C.POINTER(BgtqRope), C.c_void_p, C.POINTER(BgtqRows),
-                                   C.POINTER(BgtqRows), C.c_int, C.c_int, C.c_void_p, C.POINTER(BgtqCache), C.c_void_p]),
+    "bgtq_rope_append": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                   C.c_void_p, C.c_int, C.c_int, C.c_void_p, C.POINTER(BgtqCache), C.c_void_p]),
     "bgtq_fp4_cache_bytes": (C.c_int, [C.c_int, C.c_int, C.c_int64, C.POINTER(C.c_size_t)]),
-    "bgtq_fp4_append": (C.c_int, [C.c_void_p, C.POINTER(BgtqRope), C.c_void_p, C.POINTER(BgtqRows), C.POINTER(BgtqRows),
-                                  C.c_int, C.c_int, C.c_void_p, C.POINTER(BgtqFp4Cache), C.c_void_p]),
+    "bgtq_fp4_append": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p,
+                                  C.c_int, C.c_int, C.c_void_p, C.c_void_p, C.c_void_p]),
     "bgtq_fp4_attn_workspace": (C.c_int, [C.c_int, C.c_int, C.c_int, C.c_int, C.c_int64, C.POINTER(C.c_size_t)]),
-    "bgtq_fp4_attn": (C.c_int, [C.c_void_p, C.POINTER(BgtqRope), C.c_void_p, C.POINTER(BgtqRows), C.c_int, C.c_int, C.c_int,
-                                C.POINTER(BgtqFp4Cache), C.c_void_p, C.c_int64, C.c_void_p, C.c_int, C.c_float, C.c_void_p,
+    "bgtq_fp4_attn": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int,
+                                C.c_void_p, C.c_void_p, C.c_int64, C.c_void_p, C.c_int, C.c_float, C.c_void_p,
                                 C.c_size_t, C.c_void_p]),
-    "bgtq_fp4_dequant": (C.c_int, [C.c_void_p, C.POINTER(BgtqFp4Cache), C.c_int, C.c_int, C.c_int, C.c_int64, C.c_int64,
+    "bgtq_fp4_dequant": (C.c_int, [C.c_void_p, C.c_void_p, C.c_int, C.c_int, C.c_int, C.c_int64, C.c_int64,
                                    C.c_void_p, C.c_void_p]),
     "bgtq_logit_mae": (C.c_int, [C.c_void_p, C.c_void_p, C.c_void_p, C.c_void_p, C.POINTER(BgtqCache), C.c_int64,
                                  C.c_int, C.c_float, C.c_void_p]),

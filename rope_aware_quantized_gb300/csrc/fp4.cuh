@@ -52,9 +52,10 @@ inline Fp4Map make_fp4_map(const bgtq_fp4_cache& c) {
     return m;
 }
 
-// What bgtq_fp4_attn runs: the one-pass kernel for up to kFp4Rows query rows
-// of a KV head, or the tensor-core tiles over a decoded copy.
-constexpr int kFp4Rows = 32;
+// What bgtq_fp4_attn runs: the one-pass kernel (fp4_attn.cu) for up to
+// kFp4RowsLeast query rows of a KV head and, where there is work enough, up to
+// kFp4Rows; else the tensor cores' tiles (fp4_tiles.cu).
+constexpr int kFp4RowsLeast = 16, kFp4Rows = 32;
 struct Fp4Attn {
     RopeParams rope;
     RowsView q;

@@ -50,6 +50,7 @@ struct AttnParams {
     int batch, t, group, H;
     int clusters;        // of the launch
     int least;           // pairs that a cluster takes at least
+    bool pad;            // few units: each in whole ranges (see Share)
     void* out;
     int out_dtype;
     float scale_log2;
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, NQ <= kTwoCtas ? 2 : 1) fp4_attn_ker
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cs = (int)cluster_size(), rank = (int)cluster_rank();
     const int k = (int)blockIdx.x / cs;
-    const int rows = p.t * p.group, units = p.batch * p.H;
+    const int rows = p.t * p.group, units = p.batch * p.H;  // (pad: units < clusters)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (tid < kWarps * kStages) mbar_init(smem_u32(&s_bar[tid]), 1);
     if (tid == 0) s_abort = 0;
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, NQ <= kTwoCtas ? 2 : 1) fp4_attn_ker
     auto pairs_of = [](int n) -> int { return max(1, (n + kPair - 1) / kPair); };
     // ---- the cluster's range: where it begins
     Share sh;
-    sh.pad = 2 * units <= p.clusters;
+    sh.pad = p.pad;
     int b = 0, start = 0, n = 0;  // start: places before sequence b
     {
         const int each = (p.batch + kThreads - 1) / kThreads;
@@ -725,51 +726,67 @@ constexpr size_t kCounterBytes = (size_t)kMaxClusters * 8 * 4;
 
 size_t one_pass_bytes(int64_t rows) { return (size_t)2 * kMaxClusters * 8 * row_tiles(rows) * (8 + 4 * kD); }
 
-// CTAs of a cluster: few units are cut into many partials, and clusters join
-// them on the chip; many units fill the GPU with CTAs of their own.
-int cluster_for(int64_t units) { return units <= 16 ? 8 : units <= 64 ? 4 : units < 152 ? 2 : 1; }
-
+// Clusters of cs CTAs (1, 2, 4, 8) that the GPU holds at once.
 template <int NQ>
-cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
+cudaError_t resident_clusters(int cs, const cudaLaunchConfig_t& cfg, int& n) {
     static std::mutex mu;
-    static int resident[64][4] = {};  // clusters of 1, 2, 4, 8 CTAs that the GPU holds at once
+    static int known[64][4] = {};
     int dev = 0;
     cudaGetDevice(&dev);
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    const int cs = cluster_for(units), at = cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3;
+    std::lock_guard<std::mutex> lock(mu);
+    int& at = known[dev][cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3];
+    if (!at) {
+        cudaError_t e = cudaFuncSetAttribute(fp4_attn_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NQ>);
+        if (e != cudaSuccess) return e;
+        cudaLaunchAttribute shape;
+        shape.id = cudaLaunchAttributeClusterDimension;
+        shape.val.clusterDim.x = cs;
+        shape.val.clusterDim.y = shape.val.clusterDim.z = 1;
+        cudaLaunchConfig_t probe = cfg;
+        probe.gridDim = dim3((unsigned)cs, 1, 1);
+        probe.attrs = &shape;
+        probe.numAttrs = 1;
+        int most = 0;
+        e = cudaOccupancyMaxActiveClusters(&most, fp4_attn_kernel<NQ>, &probe);
+        if (e != cudaSuccess) return e;
+        if (most < 1) return cudaErrorInvalidConfiguration;
+        at = std::min(most, kMaxClusters / cs);
+    }
+    n = at;
+    return cudaSuccess;
+}
+
+template <int NQ>
+cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cs;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = smem_bytes<NQ>;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    {
-        std::lock_guard<std::mutex> lock(mu);
-        if (!resident[dev][at]) {
-            cudaError_t e = cudaFuncSetAttribute(fp4_attn_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NQ>);
-            if (e != cudaSuccess) return e;
-            int n = 0;
-            cudaLaunchConfig_t probe = cfg;
-            cudaLaunchAttribute only = attr[1];
-            probe.gridDim = dim3((unsigned)cs, 1, 1);
-            probe.attrs = &only;
-            probe.numAttrs = 1;
-            e = cudaOccupancyMaxActiveClusters(&n, fp4_attn_kernel<NQ>, &probe);
-            if (e != cudaSuccess) return e;
-            if (n < 1) return cudaErrorInvalidConfiguration;
-            resident[dev][at] = std::min(n, kMaxClusters / cs);
-        }
-        p.clusters = resident[dev][at];
+    // Few units: the largest clusters of which every unit can have two (they join
+    // on the chip what would be partials in memory), and units in whole ranges.
+    // Many: CTAs of their own.
+    int cs = 8;
+    for (;; cs >>= 1) {
+        const cudaError_t e = resident_clusters<NQ>(cs, cfg, p.clusters);
+        if (e != cudaSuccess) return e;
+        p.pad = 2 * units <= p.clusters;
+        if (p.pad || cs == 1) break;
     }
-    p.least = cs * kWarps;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cs;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    // Few units: one of up to four pairs a warp stays in one cluster, as the join of
+    // several through memory takes longer (2.8 us) than the pairs (0.6 us each).
+    const int64_t unit_pairs = std::max<int64_t>(1, (p.max_len + kPair - 1) / kPair);
+    p.least = (p.pad && unit_pairs <= 4 * cs * kWarps ? 4 : 1) * cs * kWarps;
     // (a unit more than the places need: the padded split counts on it)
-    const int64_t most = units * std::max<int64_t>(1, (p.max_len + kPair - 1) / kPair);
+    const int64_t most = units * unit_pairs;
     p.clusters = (int)std::min<int64_t>(p.clusters, (most + p.least - 1) / p.least + units);
     cfg.gridDim = dim3((unsigned)(p.clusters * cs), 1, 1);
     return cudaLaunchKernelEx(&cfg, fp4_attn_kernel<NQ>, p);
@@ -780,12 +797,18 @@ cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
 size_t fp4_attn_workspace_bytes(int H, int group, int batch, int t, int64_t max_len) {
     const int64_t heads = (int64_t)batch * H, rows = (int64_t)t * group;
     const size_t few = one_pass_bytes(std::min<int64_t>(rows, kFp4Rows));
-    return kCounterBytes + std::max(few, rows > kFp4Rows ? fp4_tiles_workspace_bytes(heads, rows, max_len) : 0);
+    return kCounterBytes + std::max(few, rows > kFp4RowsLeast ? fp4_tiles_workspace_bytes(heads, rows, max_len) : 0);
 }
 
 cudaError_t launch_fp4_attn(cudaStream_t s, const Fp4Attn& a) {
     const int64_t rows = (int64_t)a.t * a.group;
-    if (rows > kFp4Rows) return launch_fp4_tiles(s, a, static_cast<char*>(a.ws) + kCounterBytes);
+    // 17 to 32 rows: the tiles, while they are few (32 rows, in us, one pass and
+    // tiles: 1 head of 16384 18.8 and 13.7, 8 heads of 8192 35 and 20, 2 heads of
+    // 131072 45 and 38; 256 heads of 8192 175 and 231).  16 rows: 12.7 and 13.7,
+    // 2 heads of 131072 28 and 37.
+    const int64_t tiles = (int64_t)a.batch * a.map.H * ((std::min(a.max_len, a.cap) + 127) / 128);
+    if (rows > kFp4Rows || (rows > kFp4RowsLeast && tiles <= 4096))
+        return launch_fp4_tiles(s, a, static_cast<char*>(a.ws) + kCounterBytes);
     AttnParams p;
     p.rope = a.rope;
     p.q = a.q;

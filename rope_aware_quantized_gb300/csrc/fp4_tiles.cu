@@ -680,30 +680,31 @@ __global__ void __launch_bounds__(256) fp4_join_kernel(const __grid_constant__ T
             make_uint2(pack_h2(o.x * inv, o.y * inv), pack_h2(o.z * inv, o.w * inv));
 }
 
-constexpr int kSms = 152;
+constexpr int kSms = 152, kLeastTiles = 2;
 
 // Units (pair blocks of all heads) onto the GPU's 152 SMs, one CTA each.  More
 // units than SMs: whole ones for the full rounds, the rest split over the SMs.
 // Fewer: p equal parts and one smaller one, of which an SM that has no large
 // part takes k in turn while the large ones run: k s = m, p m + s = tiles
-// (128 units of 272 tiles: 233 + 39).  Parts of eight tiles at least: a CTA's
-// own start and end take as long as about three.
+// (128 units of 272 tiles: 233 + 39).  Parts of kLeastTiles at least: a CTA's
+// own start and end take as long as about three tiles, but CTAs of few units
+// would be idle; a smaller part of eight at least.
 struct TileSplit {
     int64_t n_whole, n_split;
     int parts, part_tiles;
 };
 TileSplit tile_split(int64_t units, int64_t max_len) {
-    const int64_t tiles = std::max<int64_t>(1, (max_len + kKeys - 1) / kKeys), least = 8;
+    const int64_t tiles = std::max<int64_t>(1, (max_len + kKeys - 1) / kKeys), small = 8;
     const int64_t n_split = units % kSms, n_whole = units - n_split;
-    if (n_split == 0 || tiles < 2 * least) return {units, 0, 1, (int)tiles};
+    if (n_split == 0 || tiles < 2 * kLeastTiles) return {units, 0, 1, (int)tiles};
     const int64_t p = kSms / n_split, free = kSms - p * n_split;
     int64_t m = (tiles + p - 1) / p;
     if (free > 0 && n_whole == 0) {
         const int64_t k = (n_split + free - 1) / free;
         const int64_t m2 = (k * tiles + p * k) / (p * k + 1);  // rounded up
-        if (m2 + least < m && tiles - p * m2 >= least) m = m2;
+        if (m2 + small < m && tiles - p * m2 >= small) m = m2;
     }
-    m = std::max(m, least);
+    m = std::max<int64_t>(m, kLeastTiles);
     const int64_t parts = (tiles + m - 1) / m;
     if (parts == 1) return {units, 0, 1, (int)tiles};
     return {n_whole, n_split, (int)parts, (int)m};
@@ -714,10 +715,10 @@ int64_t pair_blocks(int64_t rows) { return (rows + 2 * kRows - 1) / (2 * kRows);
 }  // namespace
 
 // Room for the splits' rows of any shape up to this one: at most kSms of equal
-// parts and kSms smaller ones, none of less than eight tiles but the last.
+// parts and kSms smaller ones, none of less than kLeastTiles but the last.
 size_t fp4_tiles_workspace_bytes(int64_t heads, int64_t rows, int64_t max_len) {
     const int64_t tiles = std::max<int64_t>(1, (max_len + kKeys - 1) / kKeys);
-    const int64_t slots = std::min<int64_t>(2 * kSms, heads * pair_blocks(rows) * ((tiles + 7) / 8));
+    const int64_t slots = std::min<int64_t>(2 * kSms, heads * pair_blocks(rows) * ((tiles + kLeastTiles - 1) / kLeastTiles));
     return (size_t)slots * 2 * kRows * (8 + 4 * kD);
 }
 
@@ -778,7 +779,9 @@ cudaError_t launch_fp4_tiles(cudaStream_t s, const Fp4Attn& a, void* ws) {
     cfg.numAttrs = 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, a.out_dtype ? fp4_tiles_kernel<true> : fp4_tiles_kernel<false>, p);
     if (e != cudaSuccess || sp.n_split == 0) return e;
-    const bool wide = sp.parts >= 8;
+    // a block a row while the rows alone do not fill the GPU (256 rows of 16 parts:
+    // 12.7 us in all against 14.7; 2048 rows of 8: 27 against 20)
+    const bool wide = sp.parts >= 8 && sp.n_split * 2 * kRows <= 8 * kSms;
     cfg.gridDim = dim3((unsigned)(sp.n_split * 2 * kRows / (wide ? 1 : 8)), 1, 1);
     cfg.blockDim = dim3(256, 1, 1);
     cfg.dynamicSmemBytes = 0;

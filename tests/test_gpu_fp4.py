@@ -10,10 +10,13 @@ weight, whichever is more (the parts' smallest step is 2^-24, half of it
 2^-25, and the largest weight is 2^8 or more when the reference is set); an
 output's sums, in chains of
 at most n / 8 + 64 steps of fp32, by 2^-24 a step (rounded towards zero by the
-tensor cores: 2^-23) of sum w |v|.  Tiles of the tensor cores round a weight to
-fp16, 2^-11 (below fp16's normal range 2^-25 of the largest, 2^-17 of a
-weight's share over 256 positions).  An fp16 output adds half a step, 2^-11.
+tensor cores: 2^-23) of sum w |v|.  With more than 16 rows a KV head an fp16
+output may come from the tiles, which round a weight to fp16, 2^-11 (below
+fp16's normal range 2^-25 of the largest, 2^-17 of a weight's share over 256
+positions).  An fp16 output adds half a step, 2^-11.
 """
+
+import ctypes
 
 import numpy as np
 import pytest
@@ -221,6 +224,7 @@ class Case:
                 one.__dict__.update(self.cache.__dict__)
                 one.batch = 1
                 one.desc = type(self.cache.desc).from_buffer_copy(self.cache.desc)
+                one.address = ctypes.addressof(one.desc)
                 if page:
                     one.desc.page_table += 4 * b * self.cache.max_pages
                 else:
@@ -259,7 +263,7 @@ class Case:
                     rel = np.expm1(2 * d) + 2.0 ** -21 + 2.0 ** -22 + (n / 8 + 64) * 2.0 ** -23
                     top = w.max(-1, keepdims=True, initial=0.0)
                     tol = rel * mag + 2.0 ** -33 * top * np.abs(v).sum(0)
-                    if tiles:
+                    if tiles and half:
                         tol = tol + 2.0 ** -11 * mag + 2.0 ** -17 * np.abs(v).max(initial=0.0)
                     if half:
                         tol = tol + 2.0 ** -11 * np.abs(want) + 2.0 ** -25
@@ -275,7 +279,7 @@ class Case:
 @pytest.mark.parametrize("half", [False, True])
 def test_attention_few_rows(H, G, t, lens, cap, page, half):
     c = Case(H, G, t, lens, cap, page, seed=cap + t, spread=1.5)
-    c.check(c.run(half), half)
+    c.check(c.run(half), half, tiles=t * G > 16)
 
 
 @pytest.mark.parametrize("H,G,t,lens,cap,page", [
@@ -297,7 +301,7 @@ def test_attention_rotates_the_queries(t, layout, axis):
     q = torch.empty(c.q.shape, dtype=torch.float16, device="cuda")
     bg.bgtq_rope_rows(rope, pos, c.q, q)
     out = c.run(False, rope=rope, pos=pos)
-    c.check(out, False, tiles=t * 4 > 32, q=q)
+    c.check(out, False, tiles=t * 4 > 16, q=q)
     plain = Case.run(type("C", (), dict(c.__dict__, q=q)), False)
     assert torch.equal(out, plain)  # the same bits as the two calls
     if axis is None:  # positions left out: the rows' own
@@ -438,7 +442,7 @@ def test_a_run_from_an_empty_cache():
         pos = i32(start[:, None] + np.arange(t))
         c.q = torch.empty((B, H * G, t, 128), dtype=torch.float16, device="cuda")
         bg.bgtq_rope_rows(rope, pos, q, c.q)
-        c.check(out, half, tiles=t * G > 32)
+        c.check(out, half, tiles=t * G > 16)
 
 
 def test_a_captured_step_replayed():
