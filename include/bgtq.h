@@ -717,9 +717,9 @@ int bgtq_fp4_attn_workspace(int n_kv_heads, int group, int batch, int t, int64_t
  *              (1), 16-byte aligned
  *   workspace  device, 256-byte aligned, bgtq_fp4_attn_workspace bytes; two
  *              calls that may overlap on the GPU need two
- * Logits are fp16 products summed in fp32, probabilities taken in 22 bits (two
- * fp16 parts); with more than 16 rows a KV head (t * group) and an fp16 output
- * they may be rounded to fp16, as in bgtq_prefill_attn.
+ * Logits are fp16 products summed in fp32.  Probabilities meet the values
+ * rounded to fp16 for a half output, as in bgtq_prefill_attn, and in 22 bits
+ * (two fp16 parts) for a float one; their sum is taken before.
  * Positions from n on, and their bytes, do not matter.
  * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (more than 65535 sequences,
  * batch * H > 65535, batch * H * max_len >=

@@ -9,9 +9,13 @@
 //   S^T = K Q^T   (16 positions x 8 rows, K 16 dims a step): codes to fp16 by
 //                 the hardware's conversion, times the block's scale, exact;
 //                 the products are fp16 x fp16 in fp32
-//   P^T           exp2(scaled S - m) in fp32, split into two fp16 parts (22
-//                 bits), transposed from accumulator to operand by movmatrix
-//   O^T += V^T P^T  (16 dims x 8 rows, 16 positions a step), twice (two parts)
+//   P^T           exp2(scaled S - m) in fp32, summed, then rounded to fp16 (fp16
+//                 outputs) or split into two fp16 parts, 22 bits (fp32 outputs),
+//                 transposed from accumulator to operand by movmatrix
+//   O^T += V^T P^T  (16 dims x 8 rows, 16 positions a step), for each part
+// One part where the output is rounded to fp16 itself: an output is then off
+// by 2.6e-4 (2-norm) instead of 2.1e-4, and 32 x 8 heads of up to 16384 take
+// 69 us instead of 76.
 // A lane's operands are contiguous in a group (that is its layout), so a
 // group is read with eight conflict-free loads a lane.  mma.sync, not tcgen05:
 // 8 to 32 rows a head leave a 128-row tile idle, and its operands would have
@@ -19,8 +23,8 @@
 // Two groups at a time: their chains of products and exponentials run side by
 // side, and the wait, the reference's check and the loop are paid once.
 // The reference m of a row's exponentials stays kLift below the largest logit
-// when set and moves only when a logit passes it by kRange, so that the two
-// parts keep 22 bits well above fp16's smallest numbers.
+// when set and moves only when a logit passes it by kRange, so that the parts
+// keep their bits well above fp16's smallest numbers.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -109,7 +113,7 @@ struct Query<1> {
 // memory, base its first position, lim the last position each of the lane's
 // rows sees; kEdge: some position is not seen by every row (from n on: its
 // bytes do not count).
-template <int NQ, bool kEdge>
+template <int NQ, bool kTwo, bool kEdge>
 __device__ __forceinline__ void attend(State<NQ>& st, bool first, const Query<NQ>& q, const uint8_t* img, int base, int n,
                                        const int (&lim)[NQ][2], float c, int lane) {
     const int g = lane >> 2, cl = lane & 3;
@@ -186,7 +190,7 @@ __device__ __forceinline__ void attend(State<NQ>& st, bool first, const Query<NQ
                 }
             }
     }
-    uint32_t hi[2][NQ][2], lo[2][NQ][2];
+    uint32_t hi[2][NQ][2], lo[2][NQ][2];  // lo: with kTwo
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -197,9 +201,11 @@ __device__ __forceinline__ void attend(State<NQ>& st, bool first, const Query<NQ
                 st.l[i][0] += p0;
                 st.l[i][1] += p1;
                 const __half2 h = __floats2half2_rn(p0, p1);
-                const float2 b = __half22float2(h);
                 hi[x][i][y] = transpose8(h2u(h));
-                lo[x][i][y] = transpose8(h2u(__floats2half2_rn(p0 - b.x, p1 - b.y)));
+                if constexpr (kTwo) {
+                    const float2 b = __half22float2(h);
+                    lo[x][i][y] = transpose8(h2u(__floats2half2_rn(p0 - b.x, p1 - b.y)));
+                }
             }
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -226,7 +232,7 @@ __device__ __forceinline__ void attend(State<NQ>& st, bool first, const Query<NQ
 #pragma unroll
                 for (int i = 0; i < NQ; ++i) {
                     mma16816(st.o[4 * jj + k][i], a0, a1, a2, a3, hi[x][i][0], hi[x][i][1]);
-                    mma16816(st.o[4 * jj + k][i], a0, a1, a2, a3, lo[x][i][0], lo[x][i][1]);
+                    if constexpr (kTwo) mma16816(st.o[4 * jj + k][i], a0, a1, a2, a3, lo[x][i][0], lo[x][i][1]);
                 }
             }
         }
@@ -290,7 +296,7 @@ struct Share {
     }
 };
 
-template <int NQ>
+template <int NQ, bool kTwo>
 __global__ void __launch_bounds__(kThreads, NQ <= kTwoCtas ? 2 : 1) fp4_attn_kernel(const __grid_constant__ AttnParams p) {
     constexpr int R = 8 * NQ;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -529,9 +535,9 @@ __global__ void __launch_bounds__(kThreads, NQ <= kTwoCtas ? 2 : 1) fp4_attn_ker
                 }
                 const uint8_t* img = ring + stage * kPairBytes;
                 if (gi * kPair + kPair - 1 <= lim_min)
-                    attend<NQ, false>(st, gi == gw, q, img, gi * kPair, n, lim, p.scale_log2, lane);
+                    attend<NQ, kTwo, false>(st, gi == gw, q, img, gi * kPair, n, lim, p.scale_log2, lane);
                 else
-                    attend<NQ, true>(st, gi == gw, q, img, gi * kPair, n, lim, p.scale_log2, lane);
+                    attend<NQ, kTwo, true>(st, gi == gw, q, img, gi * kPair, n, lim, p.scale_log2, lane);
                 __syncwarp();
                 if (lane == 0 && gi + kStages * step < g1) fetch(gi + kStages * step, stage);
                 if (++stage == kStages) {
@@ -727,7 +733,7 @@ constexpr size_t kCounterBytes = (size_t)kMaxClusters * 8 * 4;
 size_t one_pass_bytes(int64_t rows) { return (size_t)2 * kMaxClusters * 8 * row_tiles(rows) * (8 + 4 * kD); }
 
 // Clusters of cs CTAs (1, 2, 4, 8) that the GPU holds at once.
-template <int NQ>
+template <int NQ, bool kTwo>
 cudaError_t resident_clusters(int cs, const cudaLaunchConfig_t& cfg, int& n) {
     static std::mutex mu;
     static int known[64][4] = {};
@@ -737,7 +743,7 @@ cudaError_t resident_clusters(int cs, const cudaLaunchConfig_t& cfg, int& n) {
     std::lock_guard<std::mutex> lock(mu);
     int& at = known[dev][cs == 1 ? 0 : cs == 2 ? 1 : cs == 4 ? 2 : 3];
     if (!at) {
-        cudaError_t e = cudaFuncSetAttribute(fp4_attn_kernel<NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NQ>);
+        cudaError_t e = cudaFuncSetAttribute(fp4_attn_kernel<NQ, kTwo>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<NQ>);
         if (e != cudaSuccess) return e;
         cudaLaunchAttribute shape;
         shape.id = cudaLaunchAttributeClusterDimension;
@@ -748,7 +754,7 @@ cudaError_t resident_clusters(int cs, const cudaLaunchConfig_t& cfg, int& n) {
         probe.attrs = &shape;
         probe.numAttrs = 1;
         int most = 0;
-        e = cudaOccupancyMaxActiveClusters(&most, fp4_attn_kernel<NQ>, &probe);
+        e = cudaOccupancyMaxActiveClusters(&most, fp4_attn_kernel<NQ, kTwo>, &probe);
         if (e != cudaSuccess) return e;
         if (most < 1) return cudaErrorInvalidConfiguration;
         at = std::min(most, kMaxClusters / cs);
@@ -757,7 +763,7 @@ cudaError_t resident_clusters(int cs, const cudaLaunchConfig_t& cfg, int& n) {
     return cudaSuccess;
 }
 
-template <int NQ>
+template <int NQ, bool kTwo>
 cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -773,7 +779,7 @@ cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
     // Many: CTAs of their own.
     int cs = 8;
     for (;; cs >>= 1) {
-        const cudaError_t e = resident_clusters<NQ>(cs, cfg, p.clusters);
+        const cudaError_t e = resident_clusters<NQ, kTwo>(cs, cfg, p.clusters);
         if (e != cudaSuccess) return e;
         p.pad = 2 * units <= p.clusters;
         if (p.pad || cs == 1) break;
@@ -789,7 +795,7 @@ cudaError_t launch_one_pass(cudaStream_t s, AttnParams& p, int64_t units) {
     const int64_t most = units * unit_pairs;
     p.clusters = (int)std::min<int64_t>(p.clusters, (most + p.least - 1) / p.least + units);
     cfg.gridDim = dim3((unsigned)(p.clusters * cs), 1, 1);
-    return cudaLaunchKernelEx(&cfg, fp4_attn_kernel<NQ>, p);
+    return cudaLaunchKernelEx(&cfg, fp4_attn_kernel<NQ, kTwo>, p);
 }
 
 }  // namespace
@@ -830,9 +836,9 @@ cudaError_t launch_fp4_attn(cudaStream_t s, const Fp4Attn& a) {
     p.part_ml = reinterpret_cast<float2*>(ws + kCounterBytes + (size_t)2 * kMaxClusters * 8 * nq * 4 * kD);
     const int64_t units = (int64_t)a.batch * a.map.H;
     switch (nq) {
-        case 1: return launch_one_pass<1>(s, p, units);
-        case 2: return launch_one_pass<2>(s, p, units);
-        default: return launch_one_pass<4>(s, p, units);
+        case 1: return a.out_dtype ? launch_one_pass<1, true>(s, p, units) : launch_one_pass<1, false>(s, p, units);
+        case 2: return a.out_dtype ? launch_one_pass<2, true>(s, p, units) : launch_one_pass<2, false>(s, p, units);
+        default: return a.out_dtype ? launch_one_pass<4, true>(s, p, units) : launch_one_pass<4, false>(s, p, units);
     }
 }
 

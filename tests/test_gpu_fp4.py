@@ -10,10 +10,9 @@ weight, whichever is more (the parts' smallest step is 2^-24, half of it
 2^-25, and the largest weight is 2^8 or more when the reference is set); an
 output's sums, in chains of
 at most n / 8 + 64 steps of fp32, by 2^-24 a step (rounded towards zero by the
-tensor cores: 2^-23) of sum w |v|.  With more than 16 rows a KV head an fp16
-output may come from the tiles, which round a weight to fp16, 2^-11 (below
-fp16's normal range 2^-25 of the largest, 2^-17 of a weight's share over 256
-positions).  An fp16 output adds half a step, 2^-11.
+tensor cores: 2^-23) of sum w |v|.  For an fp16 output weights are rounded to
+fp16, 2^-11 (below fp16's normal range 2^-25 of the largest, 2^-17 of a weight's
+share over 256 positions), and the output adds half a step, 2^-11.
 """
 
 import ctypes
@@ -245,7 +244,7 @@ class Case:
         bg.bgtq_fp4_attn(self.q, self.cache, self.seq, max_len, out, ws, **kw)
         return out
 
-    def check(self, out, half, tiles=False, q=None, lens=None, scale=SCALE, units=None):
+    def check(self, out, half, q=None, lens=None, scale=SCALE, units=None):
         q = (self.q if q is None else q).cpu().numpy().astype(np.float64)
         got = out.double().cpu().numpy()
         assert np.isfinite(got).all()
@@ -263,9 +262,8 @@ class Case:
                     rel = np.expm1(2 * d) + 2.0 ** -21 + 2.0 ** -22 + (n / 8 + 64) * 2.0 ** -23
                     top = w.max(-1, keepdims=True, initial=0.0)
                     tol = rel * mag + 2.0 ** -33 * top * np.abs(v).sum(0)
-                    if tiles and half:
-                        tol = tol + 2.0 ** -11 * mag + 2.0 ** -17 * np.abs(v).max(initial=0.0)
                     if half:
+                        tol = tol + 2.0 ** -11 * mag + 2.0 ** -17 * np.abs(v).max(initial=0.0)
                         tol = tol + 2.0 ** -11 * np.abs(want) + 2.0 ** -25
                     assert (np.abs(got[b, a] - want) <= tol).all(), (b, a, np.abs(got[b, a] - want).max(), tol.min())
 
@@ -279,7 +277,7 @@ class Case:
 @pytest.mark.parametrize("half", [False, True])
 def test_attention_few_rows(H, G, t, lens, cap, page, half):
     c = Case(H, G, t, lens, cap, page, seed=cap + t, spread=1.5)
-    c.check(c.run(half), half, tiles=t * G > 16)
+    c.check(c.run(half), half)
 
 
 @pytest.mark.parametrize("H,G,t,lens,cap,page", [
@@ -289,7 +287,7 @@ def test_attention_few_rows(H, G, t, lens, cap, page, half):
 @pytest.mark.parametrize("half", [False, True])
 def test_attention_many_rows(H, G, t, lens, cap, page, half):
     c = Case(H, G, t, lens, cap, page, seed=cap + t, spread=1.5)
-    c.check(c.run(half), half, tiles=True)
+    c.check(c.run(half), half)
 
 
 @pytest.mark.parametrize("t", [1, 3, 40])
@@ -301,7 +299,7 @@ def test_attention_rotates_the_queries(t, layout, axis):
     q = torch.empty(c.q.shape, dtype=torch.float16, device="cuda")
     bg.bgtq_rope_rows(rope, pos, c.q, q)
     out = c.run(False, rope=rope, pos=pos)
-    c.check(out, False, tiles=t * 4 > 16, q=q)
+    c.check(out, False, q=q)
     plain = Case.run(type("C", (), dict(c.__dict__, q=q)), False)
     assert torch.equal(out, plain)  # the same bits as the two calls
     if axis is None:  # positions left out: the rows' own
@@ -333,7 +331,7 @@ def test_lengths_outside_the_bounds(t):
     st = status()
     out = c.run(False, max_len=64, status=st)
     assert st.item() == bg.STATUS_SEQLEN_CAPACITY
-    c.check(out, False, tiles=t > 16, lens=[64, 64, 0])
+    c.check(out, False, lens=[64, 64, 0])
     st.zero_()
     c.seq = i32([100, 64, 0])
     c.run(False, max_len=1 << 20, ws=torch.zeros(bg.bgtq_fp4_attn_workspace(1, 2, 3, t, 112), dtype=torch.uint8, device="cuda"), status=st)
@@ -367,14 +365,14 @@ def test_bytes_past_the_sequence_do_not_matter(t):
 def test_large_logits_and_one_sided_rows(t):
     """Logits of hundreds: one position takes nearly all the weight; a maximum that keeps moving up."""
     c = Case(1, 4, t, [700], 704, 0, seed=8, spread=40.0)
-    c.check(c.run(False, softmax_scale=0.05), False, tiles=t > 8, scale=0.05)
+    c.check(c.run(False, softmax_scale=0.05), False, scale=0.05)
     n = 700
     ramp = torch.linspace(0.1, 20, n, device="cuda").view(1, 1, n, 1).expand(1, 1, n, 128).half()
     bg.bgtq_fp4_append(ramp, torch.randn((1, 1, n, 128), device="cuda").half(), i32([0]), c.cache)
     c.q = torch.full((1, 4, t, 128), 0.5, device="cuda").half()
-    c.check(c.run(False), False, tiles=t > 8)
+    c.check(c.run(False), False)
     c.q.neg_()
-    c.check(c.run(False), False, tiles=t > 8)
+    c.check(c.run(False), False)
 
 
 def test_tiny_values():
@@ -442,7 +440,7 @@ def test_a_run_from_an_empty_cache():
         pos = i32(start[:, None] + np.arange(t))
         c.q = torch.empty((B, H * G, t, 128), dtype=torch.float16, device="cuda")
         bg.bgtq_rope_rows(rope, pos, q, c.q)
-        c.check(out, half, tiles=t * G > 16)
+        c.check(out, half)
 
 
 def test_a_captured_step_replayed():
