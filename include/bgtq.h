@@ -684,9 +684,11 @@ int bgtq_fp4_cache_bytes(int n_kv_heads, int batch, int64_t capacity, size_t* by
  *   pos_start  device, [batch] int32: first cache position of each sequence; a
  *              sequence with pos_start < 0 or pos_start + t_new > capacity is
  *              skipped (BGTQ_STATUS_APPEND_CAPACITY)
- * Other positions of the cache keep their bytes.  An unmapped page: those
- * tokens are skipped (BGTQ_STATUS_PAGE_RANGE).  Inputs are finite: one that is
- * not gives unspecified codes of its own block.
+ * Other positions of the cache keep their bytes (their 16-byte pieces may be
+ * written again as they are: two appends to one group of 16 positions are
+ * ordered by the caller).  An unmapped page: those tokens are skipped
+ * (BGTQ_STATUS_PAGE_RANGE).  Inputs are finite: one that is not gives
+ * unspecified codes of its own block.
  * Errors: INVALID_ARG, UNSUPPORTED (more than 65535 sequences), CUDA.
  */
 int bgtq_fp4_append(void* stream, const bgtq_rope* rope, const int32_t* pos, const bgtq_rows* k, const bgtq_rows* v,

@@ -14,6 +14,8 @@
 // Floor: 512 bytes in and 144 out for a token and head, 512 of tables a token.
 #include <cuda_fp16.h>
 
+#include <algorithm>
+
 #include "fp4.cuh"
 
 namespace bgtq {
@@ -345,7 +347,9 @@ cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsVie
     p.cap = c.capacity;
     p.pos_start = pos_start;
     p.status = status;
-    const int64_t groups = ((int64_t)t_new + 14) / kGroup + 1;  // that t_new positions can touch
+    // groups that t_new positions can touch (more than the capacity: no sequence takes
+    // them, and the kernels' first blocks say so)
+    const int64_t groups = (std::min<int64_t>(t_new, c.capacity) + 14) / kGroup + 1;
     // Up to two waves of blocks (8 x 152): the block-a-group kernel's short chain of
     // waits; beyond, the work counts (131043 tokens x 2 heads: 64 us with a block
     // a group, whose six warps each pay for the set-up).

@@ -181,6 +181,31 @@ def test_append_skips():
     c.page_table.copy_(table)
 
 
+def test_more_new_tokens_than_the_capacity():
+    c = new_cache(1, 2, 32, 0, seed=9)
+    before = c.groups.clone()
+    k = torch.randn((2, 1, 40, 128), device="cuda").half()
+    st = status()
+    bg.bgtq_fp4_append(k, k, i32([0, 5]), c, status=st)
+    assert st.item() == bg.STATUS_APPEND_CAPACITY and torch.equal(before, c.groups)
+
+
+def test_append_of_one_call_equals_many():
+    """A prompt in one call (the kernel for many groups) and the same in uneven pieces."""
+    H, B, T = 8, 2, 3000
+    k, v = (torch.randn((B, H, T, 128), device="cuda").half() for _ in range(2))
+    rope = bg.Rope(*bg.bgtq_rope_table(INV, 4000), 1, MIXED)
+    pos = i32(np.random.default_rng(0).integers(0, 4000, (3, B, T)))
+    a, b = new_cache(H, B, 3008, 0, seed=5), new_cache(H, B, 3008, 0, seed=5)
+    bg.bgtq_fp4_append(k, v, i32([0, 8]), a, rope=rope, pos=pos)
+    t = 0
+    for n in (1, 15, 16, 17, 3, 100, 2000, T):
+        n = min(n, T - t)
+        bg.bgtq_fp4_append(k[:, :, t:t + n], v[:, :, t:t + n], i32([t, 8 + t]), b, rope=rope, pos=pos[:, :, t:t + n].contiguous())
+        t += n
+    assert t == T and torch.equal(a.groups, b.groups)
+
+
 def test_append_skips_inside_whole_groups():
     rng = np.random.default_rng(6)
     c = new_cache(2, 1, 96, 0, seed=8)
@@ -288,6 +313,36 @@ def test_attention_few_rows(H, G, t, lens, cap, page, half):
 def test_attention_many_rows(H, G, t, lens, cap, page, half):
     c = Case(H, G, t, lens, cap, page, seed=cap + t, spread=1.5)
     c.check(c.run(half), half)
+
+
+def many(B, H, G, t, top, page, seed, half, some):
+    """A large ragged batch, of which the units (sequence, query head) in `some` are checked."""
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, top + 1, B)
+    lens[rng.integers(0, B)] = top
+    cap = -(-top // max(page, 16)) * max(page, 16)
+    c = Case.__new__(Case)
+    c.H, c.G, c.t, c.lens, c.seq = H, G, t, lens.tolist(), i32(lens)
+    c.cache = new_cache(H, B, cap, page, spare=2, seed=seed)
+    k, v = (torch.randn((B, H, cap, 128), generator=gen(seed + i), device="cuda").half() for i in (1, 2))
+    bg.bgtq_fp4_append(k, v, i32(np.zeros(B)), c.cache)
+    c.q = torch.randn((B, H * G, t, 128), generator=gen(seed + 3), device="cuda").half()
+    out = c.run(half)
+    c.check(out, half, units={(int(b), int(a)) for b, a in zip(rng.integers(0, B, some), rng.integers(0, H * G, some))})
+    return c, out
+
+
+@pytest.mark.parametrize("B,H,G,t,top,page", [
+    (300, 2, 4, 1, 200, 16),     # more sequences than threads of a block sum up at once; several whole units a CTA
+    (40, 8, 4, 1, 3000, 64),     # units that begin in one CTA's share and end in another's
+    (150, 1, 8, 1, 700, 0), (20, 4, 8, 2, 900, 32), (7, 8, 5, 3, 1500, 0),
+    (64, 8, 4, 5, 1100, 16), (64, 8, 8, 4, 1100, 0),  # 20 and 32 rows with work enough for one pass
+    (20, 8, 1, 40, 2000, 64), (20, 8, 3, 120, 600, 16),  # more pair blocks than SMs, on the tiles
+])
+@pytest.mark.parametrize("half", [False, True])
+def test_attention_large_batches(B, H, G, t, top, page, half):
+    c, out = many(B, H, G, t, top, page, B + t, half, 40)
+    assert torch.equal(out, c.run(half))  # the same bits on every run
 
 
 @pytest.mark.parametrize("t", [1, 3, 40])

@@ -311,6 +311,52 @@ def test_append_past_the_capacity_and_unmapped_pages():
     same(a, b)
 
 
+def test_a_run_on_the_packed_cache():
+    """A prompt rotated and prefilled, the cache cut, then steps whose rotary positions run on
+    while the slots start again behind the cut: the records and outputs of steps on keys and
+    queries rotated beforehand."""
+    H, G, T, keep = 2, 2, 200, 64
+    plan = layer(9, H, 384, 3, 0)
+    rope = bg.Rope(*tables(400))
+    x = torch.randn((1, T, H * G + 2 * H, 128), device="cuda").half()
+    q, k, v = (x[:, :, a:b].transpose(1, 2) for a, b in ((0, H * G), (H * G, H * G + H), (H * G + H, H * G + 2 * H)))
+    pos = torch.arange(T, dtype=torch.int32, device="cuda").view(1, T)
+    qr, kr = torch.empty(q.shape, dtype=q.dtype, device="cuda"), torch.empty(k.shape, dtype=k.dtype, device="cuda")
+    bg.bgtq_rope_rows(rope, pos, q, qr, k, kr)
+    full, out = bg.Cache(plan, 1, T), torch.empty_like(qr)
+    lse = torch.empty((1, H * G, T), device="cuda")
+    bg.bgtq_prefill_window_attn(plan, qr, kr, v.contiguous(), full, 0, T, out, lse=lse)
+    other = bg.Cache(plan, 1, T)
+    bg.bgtq_rope_append(plan, rope, pos, k, v, i32([0]), other)
+    same(full, other)
+    scores = torch.empty((1, H, T), device="cuda")
+    bg.bgtq_prefill_score(plan, qr, kr, lse, scores, torch.zeros(max(16, bg.bgtq_prefill_score_workspace(plan, 1, T)), dtype=torch.uint8, device="cuda"))
+    caches = []
+    for _ in range(2):
+        c = bg.Cache(plan, 1, 128)
+        lens = i32([0])
+        bg.bgtq_evict(plan, full, scores, i32([T]), T, keep, 2, 10, c, torch.zeros((1, H, 128), device="cuda"), lens,
+                      torch.empty((1, H, keep), dtype=torch.int32, device="cuda"))
+        assert lens.item() == keep
+        caches.append(c)
+    a, b = caches
+    ws = [torch.zeros(bg.bgtq_decode_attn_workspace(plan, 1, 128), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    oa, ob = (torch.empty((1, H * G, 128), device="cuda") for _ in range(2))
+    for i in range(5):
+        q, k, v = (torch.randn((1, n, 1, 128), device="cuda").half() for n in (H * G, H, H))
+        pos, slot, n = i32([[T + i]]), i32([keep + i]), i32([keep + i + 1])
+        qr, kr = torch.empty_like(q), torch.empty_like(k)
+        bg.bgtq_rope_rows(rope, pos, q, qr)
+        bg.bgtq_rope_append(plan, rope, pos, k, v, slot, a)
+        bg.bgtq_decode_attn(plan, qr.squeeze(2), a, n, 128, oa, ws[0])
+        c, s = rope.cos.cpu().numpy(), rope.sin.cpu().numpy()
+        kr = expected(k.float().cpu().numpy(), c, s, np.array([[[T + i]]]), 0, None, False, "f16").cuda()
+        qn = expected(q.float().cpu().numpy(), c, s, np.array([[[T + i]]]), 0, None, False, "f16").cuda()
+        bg.bgtq_decode_step(plan, qn.squeeze(2), kr.squeeze(2), v.squeeze(2), slot, b, n, 128, ob, ws[1])
+        assert torch.equal(oa, ob)
+        same(a, b)
+
+
 def test_rotation_captured_replayed_and_on_another_stream():
     plan = layer(6, 2, 384, 3, 0)
     rope = bg.Rope(*tables(200))
