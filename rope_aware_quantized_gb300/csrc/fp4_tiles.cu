@@ -46,6 +46,13 @@ constexpr int kKeys = 128;                      // positions of a tile
 constexpr int kTileGroups = kKeys / kGroup;
 constexpr int kTileThreads = 512;
 constexpr int kDqWarp0 = 9, kDqWarps = 7, kSlots = 12;  // decoding warps; groups in shared memory
+// A slot's copies arrive at two barriers in turn: a warp may ask for a copy that
+// has not been started, while the slot's last one is still under way (another
+// warp waits for that), and with one barrier the phase before would answer it.
+// With two, that phase is of a group 2 kSlots before, of a tile whose keys the
+// products have had; and a warp has a piece of every tile's keys and values, so
+// it has seen each phase of a tile's buffers.
+static_assert(2 * kSlots >= 2 * kTileGroups && kDqWarps <= kTileGroups, "phases of the barriers stay apart");
 constexpr uint32_t kTile = kRows * kD * 2;      // one 128 x 128 fp16 tile
 constexpr uint32_t kBox = kTile / 2;            // 64 columns of it (128 rows x 128 B)
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffStage = 6 * kTile;
@@ -69,8 +76,8 @@ enum {
     kBarP = 12,
     kBarO = 14,
     kBarDrain = 16,
-    kBarFull = 17,                // a slot's group has landed
-    kBarKeys = kBarFull + kSlots,  // a slot's keys are decoded
+    kBarFull = 17,                // a slot's group has landed (two: of even and of odd rounds)
+    kBarKeys = kBarFull + 2 * kSlots,  // a slot's keys are decoded
     kNumBars = kBarKeys + kSlots
 };
 
@@ -407,17 +414,17 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             const int count = max(0, min(kTileGroups * nkt, n_groups - first));  // groups of the CTA's tiles
             const Place at(lane);
             auto fetch = [&](int x) {
-                const int st = x % kSlots;
+                const int st = x % kSlots, full = kBarFull + 2 * st + (x / kSlots & 1);
                 const uint8_t* src = p.map.group(b, h, first + x);
                 if (!src) {
                     if (p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
                     src = p.map.base;  // (some group of the pool: the output is unspecified)
                 }
                 s_issued[st] = x / kSlots + 1;
-                mbar_expect_tx(BAR(kBarFull + st), kGroupBytes);
+                mbar_expect_tx(BAR(full), kGroupBytes);
                 asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                                  sbase + kOffStage + st * kGroupBytes),
-                             "l"(src), "r"((uint32_t)kGroupBytes), "r"(BAR(kBarFull + st))
+                             "l"(src), "r"((uint32_t)kGroupBytes), "r"(BAR(full))
                              : "memory");
             };
             auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -432,7 +439,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                 const bool keys = !(u & 8);
                 // the tile's buffer is free, the group has landed
                 if (j >= 2 && !wait(BAR((keys ? kBarKEmpty : kBarVEmpty) + s), (uint32_t)((j >> 1) - 1))) break;
-                if (x < count && !wait(BAR(kBarFull + slot), round)) break;
+                if (x < count && !wait(BAR(kBarFull + 2 * slot + (round & 1u)), round >> 1)) break;
                 if (keys) {
                     if (x < count) decode_keys(at, img, sbase + kOffK + s * kTile, gr);
                 } else if (x < count) {
@@ -586,8 +593,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
     tc_fence_before();
     __syncthreads();
     // (after a wait that gave up: every copy issued lands, or times out once more, before the CTA ends)
-    if (s_abort && tid < kSlots && s_issued[tid])
-        mbar_wait(BAR(kBarFull + tid), (uint32_t)(s_issued[tid] - 1) & 1u, abort_flag, p.status, false);
+    if (s_abort && tid < kSlots && s_issued[tid]) {
+        const uint32_t round = (uint32_t)(s_issued[tid] - 1);
+        mbar_wait(BAR(kBarFull + 2 * tid + (round & 1u)), (round >> 1) & 1u, abort_flag, p.status, false);
+    }
 #undef BAR
     if (warp == 8) {
         tc_fence_after();
