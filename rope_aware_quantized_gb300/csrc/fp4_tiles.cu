@@ -8,11 +8,10 @@
 //                   block g, which is lane i of tensor memory; each brings in
 //                   its own query row first (rotated, to fp16)
 //   warp 8          issues the MMAs (one elected lane)
-//   warps 9-15      decode the tiles: a group of 16 positions is 2304
-//                   contiguous bytes (one bulk copy, kSlots of them in flight
-//                   or in use); its values are exact in fp16.  A tile is 16
-//                   pieces of work, the keys of its eight groups, then their
-//                   values, that the warps take in turn
+//   warps 9-15      decode the tiles (a value is exact in fp16).  A tile is 16
+//                   pieces of work, the keys of its eight groups of 16
+//                   positions, then their values, 1152 bytes each, that the
+//                   warps take in turn
 // Decoded tiles are K-major operands with the 128-byte swizzle.  Values are
 // stored transposed, [dim][position]: two neighbouring positions share a byte,
 // so the conversion of a byte gives a pair that lies side by side there, and
@@ -45,18 +44,14 @@ constexpr int kRows = 128;                      // rows of a block
 constexpr int kKeys = 128;                      // positions of a tile
 constexpr int kTileGroups = kKeys / kGroup;
 constexpr int kTileThreads = 512;
-constexpr int kDqWarp0 = 9, kDqWarps = 7, kSlots = 12;  // decoding warps; groups in shared memory
-// A slot's copies arrive at two barriers in turn: a warp may ask for a copy that
-// has not been started, while the slot's last one is still under way (another
-// warp waits for that), and with one barrier the phase before would answer it.
-// With two, that phase is of a group 2 kSlots before, of a tile whose keys the
-// products have had; and a warp has a piece of every tile's keys and values, so
-// it has seen each phase of a tile's buffers.
-static_assert(2 * kSlots >= 2 * kTileGroups && kDqWarps <= kTileGroups, "phases of the barriers stay apart");
+constexpr int kDqWarp0 = 9, kDqWarps = 7, kRing = 4;  // decoding warps; pieces of a warp in shared memory
+constexpr uint32_t kPieceScales = kGroupV, kPieceBytes = kPieceScales + kGroup * kD / 16;  // codes, then scales
+// (a decoding warp has a piece of every tile's keys and values, so it sees every phase of their buffers)
+static_assert(kDqWarps <= kTileGroups, "");
 constexpr uint32_t kTile = kRows * kD * 2;      // one 128 x 128 fp16 tile
 constexpr uint32_t kBox = kTile / 2;            // 64 columns of it (128 rows x 128 B)
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffStage = 6 * kTile;
-constexpr uint32_t kTilesSmem = kOffStage + kSlots * kGroupBytes + 1024;
+constexpr uint32_t kTilesSmem = kOffStage + kDqWarps * kRing * kPieceBytes + 1024;
 constexpr uint32_t kTmemCols = 512;
 // a row's reference stays kLift below its largest logit when set and moves when
 // a logit passes it by kLift + kHeadroom: P up to 2^15, its small ones above
@@ -76,9 +71,8 @@ enum {
     kBarP = 12,
     kBarO = 14,
     kBarDrain = 16,
-    kBarFull = 17,                // a slot's group has landed (two: of even and of odd rounds)
-    kBarKeys = kBarFull + 2 * kSlots,  // a slot's keys are decoded
-    kNumBars = kBarKeys + kSlots
+    kBarPv = 17,                  // (one row block) PV of a tile has completed
+    kNumBars
 };
 
 struct TileParams {
@@ -137,13 +131,16 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 // Writes of this thread become visible to the tensor cores (asynchronous proxy).
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); }
 
 // What a lane's place in a warp says about where it reads and writes.
 struct Place {
-    uint32_t k_in, ks_in, k_out[4];  // keys: offsets of its codes and scales in a group, of its stores in a group's rows
+    uint32_t k_in, ks_in, k_out[4];  // keys: offsets of its codes and scales in a piece, of its stores in a group's rows
     uint32_t v_in, vs_in, v_out;     // values likewise; v_out without the group's columns
     uint32_t g16;                    // (lane / 4) * 16
     __device__ __forceinline__ explicit Place(int lane) {
@@ -153,11 +150,11 @@ struct Place {
         const int i = lane >> 2, c = lane & 3;
         const int pos = i < 4 ? (i << 1) + (i & 1) : ((i - 4) << 1) + 1 - (i & 1);  // 0 3 4 7 1 2 5 6
         k_in = 64 * pos + 16 * c;
-        ks_in = kGroupKs + 8 * pos;
+        ks_in = kPieceScales + 8 * pos;
 #pragma unroll
         for (int j = 0; j < 4; ++j) k_out[j] = 128u * pos + 8u * (c & 1) + 16u * ((uint32_t)(2 * j + (c >> 1)) ^ (uint32_t)pos);
-        v_in = kGroupV + 16 * lane;
-        vs_in = kGroupVs + 32 * c;
+        v_in = 16 * lane;
+        vs_in = kPieceScales + 32 * c;
         v_out = 128u * i + 4u * c;
         g16 = 16u * i;
     }
@@ -309,7 +306,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_bar[kNumBars];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_abort, s_issued[kSlots];
+    __shared__ int s_abort;
     const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // units with the most tiles (a head's last rows) first; of split units all first parts, then all second ones
@@ -339,9 +336,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
 
     if (tid == 0) {
         s_abort = 0;
-        for (int i = 0; i < kSlots; ++i) s_issued[i] = 0;
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(BAR(i), i < kBarKFull ? 4 : (i >= kBarKFull && i < kBarKEmpty) ? kTileGroups : (i == kBarP || i == kBarP + 1) ? kRows : 1);
+            mbar_init(BAR(i), i < kBarKFull ? 4 : i < kBarKEmpty ? kTileGroups : (i == kBarP || i == kBarP + 1) ? kRows : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) {
@@ -364,39 +360,55 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                 return __all_sync(0xffffffffu, mbar_wait(BAR(bar), parity & 1u, abort_flag, p.status));
             };
             auto step = [](int k) { return (uint32_t)(k >> 2) * kBox + (uint32_t)(k & 3) * 32u; };
-            auto issue_s = [&](int g, int j) {
+            // S of row block g at tensor-memory column 128 to (one row block: its tiles in turn)
+            auto issue_s = [&](int g, int to, int j) {
                 const uint32_t qa = sbase + kOffQ + g * kTile, ka = sbase + kOffK + (j & 1) * kTile;
 #pragma unroll
                 for (int k = 0; k < kD / 16; ++k)
-                    mma_ss_warp(tm + 128u * g, smem_desc(qa + step(k), 16, 1024), smem_desc(ka + step(k), 16, 1024), id, k > 0);
-                mma_commit_warp(BAR(kBarS + g));
+                    mma_ss_warp(tm + 128u * to, smem_desc(qa + step(k), 16, 1024), smem_desc(ka + step(k), 16, 1024), id, k > 0);
+                mma_commit_warp(BAR(kBarS + to));
             };
-            auto issue_pv = [&](int g, int j) {
+            auto issue_pv = [&](int g, int from, int j) {
                 const uint32_t va = sbase + kOffV + (j & 1) * kTile;
 #pragma unroll
                 for (int k = 0; k < kKeys / 16; ++k) {
-                    mma_ts_warp(tm + 256u + 128u * g, tm + 128u * g + 8u * k, smem_desc(va + step(k), 16, 1024), id,
+                    mma_ts_warp(tm + 256u + 128u * g, tm + 128u * from + 8u * k, smem_desc(va + step(k), 16, 1024), id,
                                 (j > 0 || k > 0) ? 1u : 0u);
-                    if (kTwo) mma_ts_warp(tm + 256u + 128u * g, tm + 128u * g + 64u + 8u * k, smem_desc(va + step(k), 16, 1024), id, 1u);
+                    if (kTwo) mma_ts_warp(tm + 256u + 128u * g, tm + 128u * from + 64u + 8u * k, smem_desc(va + step(k), 16, 1024), id, 1u);
                 }
             };
             bool ok = wait(kBarQ, 0) && (ng < 2 || wait(kBarQ + 1, 0)) && wait(kBarKFull, 0);
             if (ok) {
                 tc_fence_after();
-                for (int g = 0; g < ng; ++g) issue_s(g, 0);
+                for (int g = 0; g < ng; ++g) issue_s(g, g, 0);
                 mma_commit_warp(BAR(kBarKEmpty));
             }
             for (int j = 0; ok && j < nkt; ++j) {
                 const int s = j & 1;
                 const bool next = j + 1 < nkt;
-                ok = wait(kBarVFull + s, (uint32_t)(j >> 1)) && (!next || wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)));
+                ok = (ng == 1 || wait(kBarVFull + s, (uint32_t)(j >> 1))) && (!next || wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)));
+                if (ng == 1) {
+                    // one row block: the next tile's S while this one's softmax runs
+                    if (!ok) break;
+                    if (next) {
+                        tc_fence_after();
+                        issue_s(0, s ^ 1, j + 1);
+                        mma_commit_warp(BAR(kBarKEmpty + (s ^ 1)));
+                    }
+                    if (!(ok = wait(kBarP, (uint32_t)j) && wait(kBarVFull + s, (uint32_t)(j >> 1)))) break;
+                    tc_fence_after();
+                    issue_pv(0, s, j);
+                    mma_commit_warp(BAR(next ? kBarPv : kBarO));
+                    mma_commit_warp(BAR(kBarVEmpty + s));
+                    continue;
+                }
                 for (int g = 0; g < ng && ok; ++g) {
                     ok = wait(kBarP + g, (uint32_t)j);
                     if (!ok) break;
                     tc_fence_after();
-                    issue_pv(g, j);
+                    issue_pv(g, g, j);
                     if (next) {
-                        issue_s(g, j + 1);
+                        issue_s(g, g, j + 1);
                     } else {
                         mma_commit_warp(BAR(kBarO + g));
                     }
@@ -409,37 +421,43 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             mma_commit_warp(BAR(kBarDrain));
             mbar_wait(BAR(kBarDrain), 0, abort_flag, p.status, false);
         } else if (warp >= kDqWarp0) {
-            // ---- decoding: piece u = 16 j + (0..7 keys, 8..15 values of group u mod 8 of tile j)
+            // ---- decoding: piece u = 16 j + (0..7 keys, 8..15 values of group u mod 8 of
+            // tile j), every kDqWarps-th a warp, the next kRing of them on their way
+            const int w = warp - kDqWarp0;
             const int n_groups = (n + kGroup - 1) / kGroup, first = j0 * kTileGroups;
             const int count = max(0, min(kTileGroups * nkt, n_groups - first));  // groups of the CTA's tiles
             const Place at(lane);
-            auto fetch = [&](int x) {
-                const int st = x % kSlots, full = kBarFull + 2 * st + (x / kSlots & 1);
-                const uint8_t* src = p.map.group(b, h, first + x);
-                if (!src) {
-                    if (p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
-                    src = p.map.base;  // (some group of the pool: the output is unspecified)
+            const uint32_t ring = sbase + kOffStage + w * (kRing * kPieceBytes);
+            auto fetch = [&](int u, int st) {
+                const int x = kTileGroups * (u >> 4) + (u & 7);
+                if (x < count) {
+                    const uint8_t* src = p.map.group(b, h, first + x);
+                    if (!src) {
+                        if (lane == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
+                        src = p.map.base;  // (some group of the pool: the output is unspecified)
+                    }
+                    src += 16 * lane;
+                    const uint32_t dst = ring + st * kPieceBytes + 16 * lane;
+                    const uint8_t* codes = src + (u & 8 ? kGroupV : 0);
+                    copy16(dst, codes);
+                    copy16(dst + 512, codes + 512);
+                    if (lane < 8) copy16(dst + kPieceScales, src + (u & 8 ? kGroupVs : kGroupKs));
                 }
-                s_issued[st] = x / kSlots + 1;
-                mbar_expect_tx(BAR(full), kGroupBytes);
-                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                                 sbase + kOffStage + st * kGroupBytes),
-                             "l"(src), "r"((uint32_t)kGroupBytes), "r"(BAR(full))
-                             : "memory");
+                asm volatile("cp.async.commit_group;" ::: "memory");
             };
             auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
                 return __all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag, p.status));
             };
-            if (warp == kDqWarp0 && lane == 0)
-                for (int x = 0; x < min(count, kSlots); ++x) fetch(x);
-            for (int u = warp - kDqWarp0; u < 16 * nkt; u += kDqWarps) {
+            for (int i = 0; i < kRing; ++i) fetch(w + i * kDqWarps, i);
+            int st = 0;
+            for (int u = w; u < 16 * nkt; u += kDqWarps) {
                 const int j = u >> 4, gr = u & 7, s = j & 1, x = kTileGroups * j + gr;
-                const uint32_t slot = (uint32_t)(x % kSlots), round = (uint32_t)(x / kSlots);
-                const uint32_t img = sbase + kOffStage + slot * kGroupBytes;
+                const uint32_t img = ring + st * kPieceBytes;
                 const bool keys = !(u & 8);
-                // the tile's buffer is free, the group has landed
+                // the tile's buffer is free, the piece has landed
                 if (j >= 2 && !wait(BAR((keys ? kBarKEmpty : kBarVEmpty) + s), (uint32_t)((j >> 1) - 1))) break;
-                if (x < count && !wait(BAR(kBarFull + 2 * slot + (round & 1u)), round >> 1)) break;
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+                __syncwarp();
                 if (keys) {
                     if (x < count) decode_keys(at, img, sbase + kOffK + s * kTile, gr);
                 } else if (x < count) {
@@ -449,16 +467,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                 }
                 fence_to_async();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(BAR((keys ? kBarKFull : kBarVFull) + s));
-                    if (keys) {
-                        if (x < count) mbar_arrive(BAR(kBarKeys + slot));
-                    } else if (x + kSlots < count && mbar_wait(BAR(kBarKeys + slot), round & 1u, abort_flag, p.status)) {
-                        fetch(x + kSlots);  // the slot's next group
-                    }
-                }
-                __syncwarp();
+                if (lane == 0) mbar_arrive(BAR((keys ? kBarKFull : kBarVFull) + s));
+                fetch(u + kRing * kDqWarps, st);
+                if (++st == kRing) st = 0;
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
         __syncwarp();
     } else {
@@ -473,12 +486,14 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             if (lane == 0) mbar_arrive(BAR(kBarQ + g));
             const int lim_min = __reduce_min_sync(0xffffffffu, r < rows ? lim : n - 1);
             const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-            const uint32_t tS = tmem + lanes + 128u * g, tO = tmem + lanes + 256u + 128u * g;
+            const uint32_t tO = tmem + lanes + 256u + 128u * g;
             const float c = p.scale_log2;
             float m = kLow, l = 0.0f;
             bool ok = true;
             for (int j = 0; j < nkt; ++j) {
-                if (!__all_sync(0xffffffffu, mbar_wait(BAR(kBarS + g), j & 1, abort_flag, p.status))) {
+                const int at = ng == 1 ? j & 1 : g;  // its S
+                const uint32_t tS = tmem + lanes + 128u * at;
+                if (!__all_sync(0xffffffffu, mbar_wait(BAR(kBarS + at), (ng == 1 ? j >> 1 : j) & 1, abort_flag, p.status))) {
                     ok = false;
                     break;
                 }
@@ -511,7 +526,12 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                 }
                 if (j > 0 && __any_sync(0xffffffffu, raise)) {
                     // the row's O so far is in tensor memory; PV of tile j - 1 has
-                    // completed (S of tile j was issued after it)
+                    // completed (two blocks: S of tile j was issued after it)
+                    if (ng == 1 && !__all_sync(0xffffffffu, mbar_wait(BAR(kBarPv), (j - 1) & 1, abort_flag, p.status))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
 #pragma unroll 1
                     for (int q = 0; q < kD / 32; ++q) {
                         float o[32];
@@ -592,11 +612,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
     }
     tc_fence_before();
     __syncthreads();
-    // (after a wait that gave up: every copy issued lands, or times out once more, before the CTA ends)
-    if (s_abort && tid < kSlots && s_issued[tid]) {
-        const uint32_t round = (uint32_t)(s_issued[tid] - 1);
-        mbar_wait(BAR(kBarFull + 2 * tid + (round & 1u)), (round >> 1) & 1u, abort_flag, p.status, false);
-    }
 #undef BAR
     if (warp == 8) {
         tc_fence_after();
