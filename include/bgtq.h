@@ -30,8 +30,10 @@
  *     pos_start BEFORE that wait, so these must not be written by a kernel
  *     that triggers its dependents early (ordinary kernels and copies are
  *     fine; of this library's kernels only bgtq_evict's write lengths, and
- *     they let no kernel after the call start early).  bgtq_evict reads
- *     everything after the wait.
+ *     they let no kernel after the call start early).  bgtq_evict,
+ *     bgtq_rope_rows, bgtq_fp4_append and bgtq_fp4_attn, which launch the
+ *     same way, read everything after the wait; bgtq_rope_append is an
+ *     append.
  *   - head_dim must be 128.  Inputs must be finite: NaN/Inf inputs give
  *     unspecified codes, never a fault.
  *   - Errors discovered on the device (positions beyond the cache capacity,
@@ -724,8 +726,8 @@ int bgtq_fp4_attn_workspace(int n_kv_heads, int group, int batch, int t, int64_t
  * (two fp16 parts) for a float one; their sum is taken before.
  * Positions from n on, and their bytes, do not matter.
  * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (more than 65535 sequences,
- * batch * H > 65535, batch * H * max_len >=
- * 2^34, sizes past 2^31 rows), CUDA.
+ * batch * H > 65535,
+ * batch * H * max_len >= 2^34, sizes past 2^31 rows), CUDA.
  */
 int bgtq_fp4_attn(void* stream, const bgtq_rope* rope, const int32_t* pos, const bgtq_rows* q, int group, int batch,
                   int t, const bgtq_fp4_cache* cache, const int32_t* seq_lens, int64_t max_len, void* out,

@@ -12,6 +12,8 @@
 //                the other kernel 5.9)
 //   many         a warp a group, its rows' loads all on their way at once
 // Floor: 512 bytes in and 144 out for a token and head, 512 of tables a token.
+// 131043 tokens of 2 heads, rotated: 51 us, 69 % of the copy bandwidth; bound by
+// 1880 warp-instructions a group at 16 warps a SM.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -350,7 +352,7 @@ cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsVie
     // groups that t_new positions can touch (more than the capacity: no sequence takes
     // them, and the kernels' first blocks say so)
     const int64_t groups = (std::min<int64_t>(t_new, c.capacity) + 14) / kGroup + 1;
-    // Up to two waves of blocks (8 x 152): the block-a-group kernel's short chain of
+    // Up to 16 groups a SM (two waves of blocks): the block-a-group kernel's short chain of
     // waits; beyond, the work counts (131043 tokens x 2 heads: 64 us with a block
     // a group, whose six warps each pay for the set-up).
     const bool bulk = groups * c.n_heads * batch > 16 * 152;

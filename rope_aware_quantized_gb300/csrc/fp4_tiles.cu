@@ -10,17 +10,27 @@
 //   warp 8          issues the MMAs (one elected lane)
 //   warps 9-15      decode the tiles (a value is exact in fp16).  A tile is 16
 //                   pieces of work, the keys of its eight groups of 16
-//                   positions, then their values, 1152 bytes each, that the
-//                   warps take in turn
+//                   positions, then their values, 1152 bytes each (kPer = 2:
+//                   eight of twice the size), that the warps take in turn;
+//                   each brings its own pieces (cp.async, four halves of a
+//                   group ahead)
 // Decoded tiles are K-major operands with the 128-byte swizzle.  Values are
 // stored transposed, [dim][position]: two neighbouring positions share a byte,
 // so the conversion of a byte gives a pair that lies side by side there, and
 // the stores of a warp fall on 32 distinct banks.  A tile is decoded once for
-// 256 rows; its 2000 warp-instructions run beside the softmax's 6700 in what
-// issue slots those leave, which is why seven warps share them (four took 2.1 us a
-// tile, longer than the softmax and the products).
+// 256 rows.
+// What bounds it: 2048 rows x 8 heads a KV head, two of them, onto 34815
+// positions take 457 us, 3500 clocks a tile of 256 rows, 2100 of them products
+// (the rest of the time they wait for decoded tiles).  The products' operands
+// (192 KB a tile) and the decoded stores (64 KB) share shared memory's 128
+// bytes a clock, and a piece takes its warp about 1080 clocks whether or not its
+// conversions, its loads or the softmax's exponentials are there.  Copies
+// started by one lane with a barrier each took 400 clocks a piece more (497 us),
+// pieces loaded a step ahead into registers and a fifth buffer as long (459 us).
 // Tensor memory: S_g at columns 128 g (P_g, fp16, over its first 64), O_g at
-// 256 + 128 g.  MMA order of tile j: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1).
+// 256 + 128 g.  MMA order of tile j: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1); with one
+// row block S of the tiles in turn in both places and S(j+1) before PV(j), so that
+// a tile's softmax follows the one before without a pause (40 rows of 131072: 39 -> 34 us).
 // fp16 outputs: probabilities are rounded to fp16 before they meet the values
 // (an output is off by 2.6e-4 of itself, 2-norm, 2.1e-4 of them the rounding of
 // the output); fp32 outputs: two fp16 parts (22 bits), half as many products
@@ -44,14 +54,14 @@ constexpr int kRows = 128;                      // rows of a block
 constexpr int kKeys = 128;                      // positions of a tile
 constexpr int kTileGroups = kKeys / kGroup;
 constexpr int kTileThreads = 512;
-constexpr int kDqWarp0 = 9, kDqWarps = 7, kRing = 4;  // decoding warps; pieces of a warp in shared memory
-constexpr uint32_t kPieceScales = kGroupV, kPieceBytes = kPieceScales + kGroup * kD / 16;  // codes, then scales
-// (a decoding warp has a piece of every tile's keys and values, so it sees every phase of their buffers)
-static_assert(kDqWarps <= kTileGroups, "");
+constexpr int kDqWarp0 = 9, kDqWarps = 7;        // decoding warps
+constexpr uint32_t kHalfBytes = kGroupBytes / 2;  // a group's keys or values: codes, then scales
+constexpr int kRingHalves = 4;                    // of them of a decoding warp in shared memory
+static_assert(kDqWarps < kTileGroups, "a decoding warp has a piece among any eight: its waits' phases are not mistaken");
 constexpr uint32_t kTile = kRows * kD * 2;      // one 128 x 128 fp16 tile
 constexpr uint32_t kBox = kTile / 2;            // 64 columns of it (128 rows x 128 B)
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffStage = 6 * kTile;
-constexpr uint32_t kTilesSmem = kOffStage + kDqWarps * kRing * kPieceBytes + 1024;
+constexpr uint32_t kTilesSmem = kOffStage + kDqWarps * kRingHalves * kHalfBytes + 1024;
 constexpr uint32_t kTmemCols = 512;
 // a row's reference stays kLift below its largest logit when set and moves when
 // a logit passes it by kLift + kHeadroom: P up to 2^15, its small ones above
@@ -123,9 +133,6 @@ __device__ __forceinline__ uint32_t tile_at(int row, int col) {
 __device__ __forceinline__ void st_shared_v4(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-__device__ __forceinline__ void st_shared(uint32_t a, uint32_t x) {
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
-}
 __device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
@@ -150,11 +157,11 @@ struct Place {
         const int i = lane >> 2, c = lane & 3;
         const int pos = i < 4 ? (i << 1) + (i & 1) : ((i - 4) << 1) + 1 - (i & 1);  // 0 3 4 7 1 2 5 6
         k_in = 64 * pos + 16 * c;
-        ks_in = kPieceScales + 8 * pos;
+        ks_in = 8 * pos;
 #pragma unroll
         for (int j = 0; j < 4; ++j) k_out[j] = 128u * pos + 8u * (c & 1) + 16u * ((uint32_t)(2 * j + (c >> 1)) ^ (uint32_t)pos);
         v_in = 16 * lane;
-        vs_in = kPieceScales + 32 * c;
+        vs_in = 32 * c;
         v_out = 128u * i + 4u * c;
         g16 = 16u * i;
     }
@@ -169,7 +176,7 @@ __device__ __forceinline__ void store1(uint32_t a, uint32_t x) {
     asm volatile("st.shared.b32 [%0 + %2], %1;" ::"r"(a), "r"(x), "n"(kAt) : "memory");
 }
 
-// Blocks 2 kJJ and 2 kJJ + 1 of a position's keys (row 8 kIt + .. of the group's rows).
+// Blocks 2 kJJ and 2 kJJ + 1 of a position's keys (row 8 kIt + .. of the piece's rows).
 template <int kIt, int kJJ>
 __device__ __forceinline__ void key_blocks(uint32_t w, uint32_t sw, const uint32_t (&out)[4]) {
     const __half2 s = fp4_scales<(kJJ & 1) * 2>(sw), s0 = __low2half2(s), s1 = __high2half2(s);
@@ -180,26 +187,36 @@ __device__ __forceinline__ void key_blocks(uint32_t w, uint32_t sw, const uint32
     store2<kAt>(out[(2 * kJJ + 1) & 3], u32(__hmul2(x[2], s1)), u32(__hmul2(x[3], s1)));
 }
 
-// Keys of group gr (0..7) of a tile.
-__device__ __forceinline__ void decode_keys(const Place& at, uint32_t img, uint32_t tile, int gr) {
-    uint4 w[2];
-    uint32_t s[2][2];
+template <int kIt>
+__device__ __forceinline__ void key_row(const uint4& w, const uint32_t (&s)[2], const uint32_t (&out)[4]) {
+    key_blocks<kIt, 0>(w.x, s[0], out);
+    key_blocks<kIt, 1>(w.y, s[0], out);
+    key_blocks<kIt, 2>(w.z, s[1], out);
+    key_blocks<kIt, 3>(w.w, s[1], out);
+}
+
+// Keys of groups kPer pr .. of a tile.
+template <int kPer>
+__device__ __forceinline__ void decode_keys(const Place& at, uint32_t img, uint32_t tile, int pr) {
+    uint4 w[2 * kPer];
+    uint32_t s[2 * kPer][2];
 #pragma unroll
-    for (int it = 0; it < 2; ++it) {
+    for (int it = 0; it < 2 * kPer; ++it) {
         w[it] = ld_shared_v4(img + at.k_in + 512 * it);
-        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(s[it][0]), "=r"(s[it][1]) : "r"(img + at.ks_in + 64 * it) : "memory");
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                     : "=r"(s[it][0]), "=r"(s[it][1])
+                     : "r"(img + kPer * kGroupV + at.ks_in + 64 * it)
+                     : "memory");
     }
     uint32_t out[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) out[j] = tile + 2048u * gr + at.k_out[j];
-    key_blocks<0, 0>(w[0].x, s[0][0], out);
-    key_blocks<0, 1>(w[0].y, s[0][0], out);
-    key_blocks<0, 2>(w[0].z, s[0][1], out);
-    key_blocks<0, 3>(w[0].w, s[0][1], out);
-    key_blocks<1, 0>(w[1].x, s[1][0], out);
-    key_blocks<1, 1>(w[1].y, s[1][0], out);
-    key_blocks<1, 2>(w[1].z, s[1][1], out);
-    key_blocks<1, 3>(w[1].w, s[1][1], out);
+    for (int j = 0; j < 4; ++j) out[j] = tile + 2048u * kPer * pr + at.k_out[j];
+    key_row<0>(w[0], s[0], out);
+    key_row<1>(w[1], s[1], out);
+    if constexpr (kPer == 2) {
+        key_row<2>(w[2], s[2], out);
+        key_row<3>(w[3], s[3], out);
+    }
 }
 
 // Block kJ (dims 16 kJ ..) of the values of four positions.
@@ -214,37 +231,41 @@ __device__ __forceinline__ void value_block(uint32_t w, uint32_t sw, uint32_t a0
     store1<2048 * kJ + 1024>(a1, u32(__hmul2(x[3], f1)));
 }
 
-// Values of group gr, transposed; `live`: positions of the group that exist (the others become zeros).
-__device__ __forceinline__ void decode_values(const Place& at, uint32_t img, uint32_t tile, int gr, int live, int lane) {
-    const uint4 w0 = ld_shared_v4(img + at.v_in), w1 = ld_shared_v4(img + at.v_in + 512);
-    uint4 s0 = ld_shared_v4(img + at.vs_in), s1 = ld_shared_v4(img + at.vs_in + 16);
-    if (live < kGroup) {
-        uint32_t keep = 0xffffffffu;
+// Values of groups kPer pr .., transposed; `live`: positions from the first
+// group's on that exist (the others become zeros, whatever their bytes).
+template <int kPer>
+__device__ __forceinline__ void decode_values(const Place& at, uint32_t img, uint32_t tile, int pr, int live, int lane) {
+    uint4 w[2 * kPer], s[2 * kPer];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (2 * (lane & 3) + (e & 1) + 8 * (e >> 1) >= live) keep &= ~(0xffu << (8 * e));
-        s0.x &= keep, s0.y &= keep, s0.z &= keep, s0.w &= keep;
-        s1.x &= keep, s1.y &= keep, s1.z &= keep, s1.w &= keep;
+    for (int i = 0; i < 2 * kPer; ++i) {
+        w[i] = ld_shared_v4(img + at.v_in + 512 * i);
+        s[i] = ld_shared_v4(img + kPer * kGroupV + at.vs_in + 128 * (i >> 1) + 16 * (i & 1));
     }
-    // positions 16 gr + 2 c (+ 1) and + 8: columns of the transposed tile
-    const uint32_t box = tile + (uint32_t)(gr >> 2) * kBox + at.v_out;
-    const uint32_t a0 = box + ((uint32_t)(32 * (gr & 3)) ^ at.g16), a1 = box + ((uint32_t)(32 * (gr & 3) + 16) ^ at.g16);
-    value_block<0>(w0.x, s0.x, a0, a1);
-    value_block<1>(w0.y, s0.y, a0, a1);
-    value_block<2>(w0.z, s0.z, a0, a1);
-    value_block<3>(w0.w, s0.w, a0, a1);
-    value_block<4>(w1.x, s1.x, a0, a1);
-    value_block<5>(w1.y, s1.y, a0, a1);
-    value_block<6>(w1.z, s1.z, a0, a1);
-    value_block<7>(w1.w, s1.w, a0, a1);
-}
-__device__ __forceinline__ void zero_values(uint32_t tile, int gr, int lane) {
-    const int g = lane >> 2, c = lane & 3;
-    const uint32_t box = tile + (uint32_t)(gr >> 2) * kBox + 4u * c;
-    const uint32_t p0 = ((uint32_t)(2 * (gr & 3)) ^ (uint32_t)g) * 16u, p1 = ((uint32_t)(2 * (gr & 3) + 1) ^ (uint32_t)g) * 16u;
-    for (int d = 0; d < kD; d += 8) {
-        st_shared(box + (uint32_t)(d + g) * 128u + p0, 0u);
-        st_shared(box + (uint32_t)(d + g) * 128u + p1, 0u);
+    if (live < kPer * kGroup) {
+#pragma unroll
+        for (int i = 0; i < 2 * kPer; ++i) {
+            uint32_t keep = 0xffffffffu;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (kGroup * (i >> 1) + 2 * (lane & 3) + (e & 1) + 8 * (e >> 1) >= live) keep &= ~(0xffu << (8 * e));
+            s[i].x &= keep, s[i].y &= keep, s[i].z &= keep, s[i].w &= keep;
+        }
+    }
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+        // positions 16 gr + 2 c (+ 1) and + 8: columns of the transposed tile
+        const int gr = kPer * pr + x;
+        const uint32_t box = tile + (uint32_t)(gr >> 2) * kBox + at.v_out;
+        const uint32_t a0 = box + ((uint32_t)(32 * (gr & 3)) ^ at.g16), a1 = box + ((uint32_t)(32 * (gr & 3) + 16) ^ at.g16);
+        const uint4 &w0 = w[2 * x], &w1 = w[2 * x + 1], &s0 = s[2 * x], &s1 = s[2 * x + 1];
+        value_block<0>(w0.x, s0.x, a0, a1);
+        value_block<1>(w0.y, s0.y, a0, a1);
+        value_block<2>(w0.z, s0.z, a0, a1);
+        value_block<3>(w0.w, s0.w, a0, a1);
+        value_block<4>(w1.x, s1.x, a0, a1);
+        value_block<5>(w1.y, s1.y, a0, a1);
+        value_block<6>(w1.z, s1.z, a0, a1);
+        value_block<7>(w1.w, s1.w, a0, a1);
     }
 }
 
@@ -301,7 +322,7 @@ __device__ __forceinline__ int bring_query(const TileParams& p, uint32_t tile, i
     return lim;
 }
 
-template <bool kTwo>
+template <bool kTwo, int kPer>
 __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid_constant__ TileParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t s_bar[kNumBars];
@@ -337,7 +358,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
     if (tid == 0) {
         s_abort = 0;
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(BAR(i), i < kBarKFull ? 4 : i < kBarKEmpty ? kTileGroups : (i == kBarP || i == kBarP + 1) ? kRows : 1);
+            mbar_init(BAR(i), i < kBarKFull ? 4 : i < kBarKEmpty ? kTileGroups / kPer : (i == kBarP || i == kBarP + 1) ? kRows : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) {
@@ -421,27 +442,39 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             mma_commit_warp(BAR(kBarDrain));
             mbar_wait(BAR(kBarDrain), 0, abort_flag, p.status, false);
         } else if (warp >= kDqWarp0) {
-            // ---- decoding: piece u = 16 j + (0..7 keys, 8..15 values of group u mod 8 of
-            // tile j), every kDqWarps-th a warp, the next kRing of them on their way
+            // ---- decoding: a tile's pieces are the keys, then the values of kPer groups
+            // each; a warp takes every kDqWarps-th, the next kRing of them on their way
+            constexpr int kPieces = kTileGroups / kPer, kRing = kRingHalves / kPer;
+            constexpr uint32_t kPieceScales = kPer * kGroupV, kPieceBytes = kPer * kHalfBytes;
             const int w = warp - kDqWarp0;
             const int n_groups = (n + kGroup - 1) / kGroup, first = j0 * kTileGroups;
             const int count = max(0, min(kTileGroups * nkt, n_groups - first));  // groups of the CTA's tiles
             const Place at(lane);
             const uint32_t ring = sbase + kOffStage + w * (kRing * kPieceBytes);
+            const bool paged = p.map.page_table != nullptr;
+            const uint8_t* flat = paged ? nullptr : p.map.group(b, h, first);
+            auto group = [&](int x) -> const uint8_t* {
+                if (!paged) return flat + (int64_t)x * kGroupBytes;
+                const uint8_t* src = p.map.group(b, h, first + x);
+                if (src) return src;
+                if (lane == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
+                return p.map.base;  // (some group of the pool: the output is unspecified)
+            };
             auto fetch = [&](int u, int st) {
-                const int x = kTileGroups * (u >> 4) + (u & 7);
+                const int x = u / (2 * kPieces) * kTileGroups + kPer * (u % kPieces);
                 if (x < count) {
-                    const uint8_t* src = p.map.group(b, h, first + x);
-                    if (!src) {
-                        if (lane == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_PAGE_RANGE);
-                        src = p.map.base;  // (some group of the pool: the output is unspecified)
+                    const bool two = kPer == 2 && x + 1 < count, values = u & kPieces;
+                    const uint8_t* src = group(x);
+                    const uint8_t* next = !two ? src : !paged || p.map.lg > 0 ? src + kGroupBytes : group(x + 1);
+                    const uint32_t dst = ring + st * kPieceBytes + 16 * lane, codes = 16 * lane + (values ? kGroupV : 0);
+                    copy16(dst, src + codes);
+                    copy16(dst + 512, src + codes + 512);
+                    if (two) {
+                        copy16(dst + 1024, next + codes);
+                        copy16(dst + 1536, next + codes + 512);
                     }
-                    src += 16 * lane;
-                    const uint32_t dst = ring + st * kPieceBytes + 16 * lane;
-                    const uint8_t* codes = src + (u & 8 ? kGroupV : 0);
-                    copy16(dst, codes);
-                    copy16(dst + 512, codes + 512);
-                    if (lane < 8) copy16(dst + kPieceScales, src + (u & 8 ? kGroupVs : kGroupKs));
+                    if (lane < 8 * kPer)
+                        copy16(dst + kPieceScales, (lane < 8 ? src : next) + (values ? kGroupVs : kGroupKs) + 16 * (lane & 7));
                 }
                 asm volatile("cp.async.commit_group;" ::: "memory");
             };
@@ -450,21 +483,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             };
             for (int i = 0; i < kRing; ++i) fetch(w + i * kDqWarps, i);
             int st = 0;
-            for (int u = w; u < 16 * nkt; u += kDqWarps) {
-                const int j = u >> 4, gr = u & 7, s = j & 1, x = kTileGroups * j + gr;
+            for (int u = w; u < 2 * kPieces * nkt; u += kDqWarps) {
+                const int j = u / (2 * kPieces), pr = u % kPieces, s = j & 1, x = kTileGroups * j + kPer * pr;
                 const uint32_t img = ring + st * kPieceBytes;
-                const bool keys = !(u & 8);
-                // the tile's buffer is free, the piece has landed
+                const bool keys = !(u & kPieces);
+                // the tile's buffer is free, the piece has landed.  (Seven pieces ago this warp
+                // waited for a product issued after those of tile j - 4, whose phase this wait
+                // could be mistaken for.)
                 if (j >= 2 && !wait(BAR((keys ? kBarKEmpty : kBarVEmpty) + s), (uint32_t)((j >> 1) - 1))) break;
                 asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
                 __syncwarp();
-                if (keys) {
-                    if (x < count) decode_keys(at, img, sbase + kOffK + s * kTile, gr);
-                } else if (x < count) {
-                    decode_values(at, img, sbase + kOffV + s * kTile, gr, n - (first + x) * kGroup, lane);
-                } else {
-                    zero_values(sbase + kOffV + s * kTile, gr, lane);
-                }
+                if (keys)
+                    decode_keys<kPer>(at, img, sbase + kOffK + s * kTile, pr);
+                else
+                    decode_values<kPer>(at, img, sbase + kOffV + s * kTile, pr, n - (first + x) * kGroup, lane);
                 fence_to_async();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(BAR((keys ? kBarKFull : kBarVFull) + s));
@@ -757,7 +789,7 @@ cudaError_t launch_fp4_tiles(cudaStream_t s, const Fp4Attn& a, void* ws) {
     {
         std::lock_guard<std::mutex> lock(mu);
         if (!done[dev]) {
-            for (auto kernel : {fp4_tiles_kernel<false>, fp4_tiles_kernel<true>}) {
+            for (auto kernel : {fp4_tiles_kernel<false, 1>, fp4_tiles_kernel<false, 2>, fp4_tiles_kernel<true, 1>}) {
                 cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTilesSmem);
                 cudaFuncAttributes fa;
                 if (e == cudaSuccess) e = cudaFuncGetAttributes(&fa, kernel);
@@ -801,7 +833,14 @@ cudaError_t launch_fp4_tiles(cudaStream_t s, const Fp4Attn& a, void* ws) {
     cfg.stream = s;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, a.out_dtype ? fp4_tiles_kernel<true> : fp4_tiles_kernel<false>, p);
+    // one row block, one part of P: pieces of two groups (32 x 8 heads of 8192, 64 rows a
+    // head: 173 us, of one 199); else their bursts hold up the softmax (256 rows of 131072
+    // in fp32 64 us, of one 53)
+    cudaError_t e = cudaLaunchKernelEx(&cfg,
+                                       a.out_dtype     ? fp4_tiles_kernel<true, 1>
+                                       : rows <= kRows ? fp4_tiles_kernel<false, 2>
+                                                       : fp4_tiles_kernel<false, 1>,
+                                       p);
     if (e != cudaSuccess || sp.n_split == 0) return e;
     // a block a row while the rows alone do not fill the GPU (256 rows of 16 parts:
     // 12.7 us in all against 14.7; 2048 rows of 8: 27 against 20)
