@@ -19,14 +19,15 @@
 // so the conversion of a byte gives a pair that lies side by side there, and
 // the stores of a warp fall on 32 distinct banks.  A tile is decoded once for
 // 256 rows.
-// What bounds it: 2048 rows x 8 heads a KV head, two of them, onto 34815
-// positions take 457 us, 3500 clocks a tile of 256 rows, 2100 of them products
-// (the rest of the time they wait for decoded tiles).  The products' operands
-// (192 KB a tile) and the decoded stores (64 KB) share shared memory's 128
-// bytes a clock, and a piece takes its warp about 1080 clocks whether or not its
-// conversions, its loads or the softmax's exponentials are there.  Copies
-// started by one lane with a barrier each took 400 clocks a piece more (497 us),
-// pieces loaded a step ahead into registers and a fifth buffer as long (459 us).
+// What bounds it: 2048 rows of 8 query heads onto 34815 positions of two KV heads
+// take 430 us, 3300 clocks a tile of 256 rows, 2100 of them products (tensor pipe
+// 57 %; the rest of the time the products wait for decoded tiles and for P).  Their
+// operands (192 KB a tile) and the decoded stores (64 KB) share shared memory's 128
+// bytes a clock, and a piece takes its warp about 1080 clocks, with or without its
+// conversions, its loads or the softmax's exponentials.  Copies started by one
+// lane, a barrier each, took 400 clocks a piece more (497 us); pieces loaded a step
+// ahead into registers and a fifth buffer, before the values' buffers were given back
+// early, 459 us for 457.
 // Tensor memory: S_g at columns 128 g (P_g, fp16, over its first 64), O_g at
 // 256 + 128 g.  MMA order of tile j: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1); with one
 // row block S of the tiles in turn in both places and S(j+1) before PV(j), so that
@@ -407,11 +408,11 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             for (int j = 0; ok && j < nkt; ++j) {
                 const int s = j & 1;
                 const bool next = j + 1 < nkt;
-                ok = (ng == 1 || wait(kBarVFull + s, (uint32_t)(j >> 1))) && (!next || wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)));
+                auto next_keys = [&]() { return wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)); };
                 if (ng == 1) {
                     // one row block: the next tile's S while this one's softmax runs
-                    if (!ok) break;
                     if (next) {
+                        if (!(ok = next_keys())) break;
                         tc_fence_after();
                         issue_s(0, s ^ 1, j + 1);
                         mma_commit_warp(BAR(kBarKEmpty + (s ^ 1)));
@@ -423,20 +424,22 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                     mma_commit_warp(BAR(kBarVEmpty + s));
                     continue;
                 }
-                for (int g = 0; g < ng && ok; ++g) {
-                    ok = wait(kBarP + g, (uint32_t)j);
-                    if (!ok) break;
+                // (both before the first product: with the keys' wait in front of S_0 alone the
+                // row blocks lose their turns, 461 us for 428)
+                ok = wait(kBarVFull + s, (uint32_t)(j >> 1)) && (!next || next_keys());
+                for (int g = 0; g < 2 && ok; ++g) {
+                    if (!(ok = wait(kBarP + g, (uint32_t)j))) break;
                     tc_fence_after();
                     issue_pv(g, g, j);
+                    // (a commit covers what was issued before it: the values' before S_1, 457 -> 430 us)
+                    if (g == 1) mma_commit_warp(BAR(kBarVEmpty + s));
                     if (next) {
                         issue_s(g, g, j + 1);
                     } else {
                         mma_commit_warp(BAR(kBarO + g));
                     }
                 }
-                if (!ok) break;
-                mma_commit_warp(BAR(kBarVEmpty + s));
-                if (next) mma_commit_warp(BAR(kBarKEmpty + (s ^ 1)));
+                if (ok && next) mma_commit_warp(BAR(kBarKEmpty + (s ^ 1)));
             }
             // every MMA issued has completed before the CTA ends
             mma_commit_warp(BAR(kBarDrain));
