@@ -358,8 +358,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
 
     if (tid == 0) {
         s_abort = 0;
+        auto lanes_of = [&](int g) { return max(1, min(kRows, (rows - r0 - kRows * g + 31) & ~31)); };  // of warps with a row
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(BAR(i), i < kBarKFull ? 4 : i < kBarKEmpty ? kTileGroups / kPer : (i == kBarP || i == kBarP + 1) ? kRows : 1);
+            mbar_init(BAR(i), i < kBarKFull ? 4 : i < kBarKEmpty ? kTileGroups / kPer : (i == kBarP || i == kBarP + 1) ? lanes_of(i - kBarP) : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) {
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             };
             auto issue_pv = [&](int g, int from, int j) {
                 const uint32_t va = sbase + kOffV + (j & 1) * kTile;
-#pragma unroll
+#pragma unroll(kTwo ? 4 : 8)  // (all 16 products in line cost the warp registers that it has not)
                 for (int k = 0; k < kKeys / 16; ++k) {
                     mma_ts_warp(tm + 256u + 128u * g, tm + 128u * from + 8u * k, smem_desc(va + step(k), 16, 1024), id,
                                 (j > 0 || k > 0) ? 1u : 0u);
@@ -408,11 +409,13 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             for (int j = 0; ok && j < nkt; ++j) {
                 const int s = j & 1;
                 const bool next = j + 1 < nkt;
-                auto next_keys = [&]() { return wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)); };
+                // (two blocks: both waits before the first product; with the keys' in front of
+                // S_0 alone the blocks lose their turns, 461 us for 428)
+                ok = (ng == 1 || wait(kBarVFull + s, (uint32_t)(j >> 1))) && (!next || wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)));
+                if (!ok) break;
                 if (ng == 1) {
                     // one row block: the next tile's S while this one's softmax runs
                     if (next) {
-                        if (!(ok = next_keys())) break;
                         tc_fence_after();
                         issue_s(0, s ^ 1, j + 1);
                         mma_commit_warp(BAR(kBarKEmpty + (s ^ 1)));
@@ -424,9 +427,6 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                     mma_commit_warp(BAR(kBarVEmpty + s));
                     continue;
                 }
-                // (both before the first product: with the keys' wait in front of S_0 alone the
-                // row blocks lose their turns, 461 us for 428)
-                ok = wait(kBarVFull + s, (uint32_t)(j >> 1)) && (!next || next_keys());
                 for (int g = 0; g < 2 && ok; ++g) {
                     if (!(ok = wait(kBarP + g, (uint32_t)j))) break;
                     tc_fence_after();
@@ -525,7 +525,9 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
             const float c = p.scale_log2;
             float m = kLow, l = 0.0f;
             bool ok = true;
-            for (int j = 0; j < nkt; ++j) {
+            // (a warp without a row leaves its lanes' P and O as they are)
+            const int n_soft = __shfl_sync(0xffffffffu, r < rows ? nkt : 0, 0);
+            for (int j = 0; j < n_soft; ++j) {
                 const int at = ng == 1 ? j & 1 : g;  // its S
                 const uint32_t tS = tmem + lanes + 128u * at;
                 if (!__all_sync(0xffffffffu, mbar_wait(BAR(kBarS + at), (ng == 1 ? j >> 1 : j) & 1, abort_flag, p.status))) {
