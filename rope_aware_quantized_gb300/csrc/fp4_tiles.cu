@@ -58,7 +58,7 @@ constexpr int kTileThreads = 512;
 constexpr int kDqWarp0 = 9, kDqWarps = 7;        // decoding warps
 constexpr uint32_t kHalfBytes = kGroupBytes / 2;  // a group's keys or values: codes, then scales
 constexpr int kRingHalves = 4;                    // of them of a decoding warp in shared memory
-static_assert(kDqWarps < kTileGroups, "a decoding warp has a piece among any eight: its waits' phases are not mistaken");
+static_assert(kDqWarps <= kTileGroups, "a decoding warp has a piece in every tile (of eight or sixteen)");
 constexpr uint32_t kTile = kRows * kD * 2;      // one 128 x 128 fp16 tile
 constexpr uint32_t kBox = kTile / 2;            // 64 columns of it (128 rows x 128 B)
 constexpr uint32_t kOffQ = 0, kOffK = 2 * kTile, kOffV = 4 * kTile, kOffStage = 6 * kTile;
@@ -82,7 +82,6 @@ enum {
     kBarP = 12,
     kBarO = 14,
     kBarDrain = 16,
-    kBarPv = 17,                  // (one row block) PV of a tile has completed
     kNumBars
 };
 
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
     const int b = head / p.H, h = head - b * p.H;
     const int rows = p.t * p.group;
     const int r0 = pb * 2 * kRows;
-    const int ng = r0 + kRows < rows ? 2 : 1;
+    const int ng = kPer == 1 && r0 + kRows < rows ? 2 : 1;  // (kPer = 2: up to kRows rows)
     const uint32_t bar0 = smem_u32(&s_bar[0]);
     volatile int* abort_flag = &s_abort;
 #define BAR(i) (bar0 + 8u * (uint32_t)(i))
@@ -360,7 +359,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
         s_abort = 0;
         auto lanes_of = [&](int g) { return max(1, min(kRows, (rows - r0 - kRows * g + 31) & ~31)); };  // of warps with a row
         for (int i = 0; i < kNumBars; ++i)
-            mbar_init(BAR(i), i < kBarKFull ? 4 : i < kBarKEmpty ? kTileGroups / kPer : (i == kBarP || i == kBarP + 1) ? lanes_of(i - kBarP) : 1);
+            mbar_init(BAR(i), i < kBarKFull ? 4 : i < kBarKEmpty ? kTileGroups / kPer : (i == kBarP || i == kBarP + 1) ? lanes_of(ng == 1 ? 0 : i - kBarP) : 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 8) {
@@ -414,17 +413,20 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                 ok = (ng == 1 || wait(kBarVFull + s, (uint32_t)(j >> 1))) && (!next || wait(kBarKFull + (s ^ 1), (uint32_t)((j + 1) >> 1)));
                 if (!ok) break;
                 if (ng == 1) {
-                    // one row block: the next tile's S while this one's softmax runs
+                    // one row block: the next tile's S while this one's softmax runs.  Buffers are
+                    // given back in order, each after the ones before it have arrived: a wait for
+                    // one is then never told from its barrier's phase before by time alone.
                     if (next) {
                         tc_fence_after();
                         issue_s(0, s ^ 1, j + 1);
+                        if (!(ok = (j == 0 || wait(kBarVEmpty + (s ^ 1), (uint32_t)((j - 1) >> 1))) && wait(kBarKEmpty + s, (uint32_t)(j >> 1)))) break;
                         mma_commit_warp(BAR(kBarKEmpty + (s ^ 1)));
                     }
-                    if (!(ok = wait(kBarP, (uint32_t)j) && wait(kBarVFull + s, (uint32_t)(j >> 1)))) break;
+                    if (!(ok = wait(kBarP + s, (uint32_t)(j >> 1)) && wait(kBarVFull + s, (uint32_t)(j >> 1)))) break;
                     tc_fence_after();
                     issue_pv(0, s, j);
-                    mma_commit_warp(BAR(next ? kBarPv : kBarO));
                     mma_commit_warp(BAR(kBarVEmpty + s));
+                    if (!next) mma_commit_warp(BAR(kBarO));
                     continue;
                 }
                 for (int g = 0; g < 2 && ok; ++g) {
@@ -490,9 +492,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                 const int j = u / (2 * kPieces), pr = u % kPieces, s = j & 1, x = kTileGroups * j + kPer * pr;
                 const uint32_t img = ring + st * kPieceBytes;
                 const bool keys = !(u & kPieces);
-                // the tile's buffer is free, the piece has landed.  (Seven pieces ago this warp
-                // waited for a product issued after those of tile j - 4, whose phase this wait
-                // could be mistaken for.)
+                // the tile's buffer is free, the piece has landed.  (The wait could be mistaken for
+                // that of tile j - 4 while its buffer is out.  With pieces of one group this warp
+                // waited for it itself, tile by tile; with two it may have had none of this kind,
+                // but waited for one that was given back after it, see the MMA warp.)
                 if (j >= 2 && !wait(BAR((keys ? kBarKEmpty : kBarVEmpty) + s), (uint32_t)((j >> 1) - 1))) break;
                 asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
                 __syncwarp();
@@ -563,8 +566,8 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                 }
                 if (j > 0 && __any_sync(0xffffffffu, raise)) {
                     // the row's O so far is in tensor memory; PV of tile j - 1 has
-                    // completed (two blocks: S of tile j was issued after it)
-                    if (ng == 1 && !__all_sync(0xffffffffu, mbar_wait(BAR(kBarPv), (j - 1) & 1, abort_flag, p.status))) {
+                    // completed (two blocks: S of tile j was issued after it; one: its values are given back)
+                    if (ng == 1 && !__all_sync(0xffffffffu, mbar_wait(BAR(kBarVEmpty + ((j - 1) & 1)), ((j - 1) >> 1) & 1, abort_flag, p.status))) {
                         ok = false;
                         break;
                     }
@@ -617,7 +620,7 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
                 l += (a.x + a.y) + (b2.x + b2.y);
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(BAR(kBarP + g));
+                mbar_arrive(BAR(kBarP + at));
             }
             if (nkt > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(BAR(kBarO + g), 0, abort_flag, p.status));
             if (ok) {
