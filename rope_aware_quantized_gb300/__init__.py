@@ -832,10 +832,11 @@ def bgtq_fp4_attn(q, cache: Fp4Cache, seq_lens, max_len: int, out, workspace, ro
 def bgtq_fp4_dequant(cache: Fp4Cache, b: int, head: int, t0: int, t1: int, k_out=None, v_out=None, stream=None):
     """Positions [t0, t1) of (sequence b, head) back to float32 rows [t1 - t0][128], for inspection."""
     import torch
-    dev = cache.groups.get_device()
+    dev = _device(cache.groups)
+    _on_fp4(cache, 0, None, dev)
     for x, name in ((k_out, "k_out"), (v_out, "v_out")):
         if x is not None:
-            _need(x, name, torch.float32, (t1 - t0, HEAD_DIM), _device(x))
+            _need(x, name, torch.float32, (t1 - t0, HEAD_DIM), dev)
     _check(lib().bgtq_fp4_dequant(_stream(stream, dev), C.byref(cache.desc), cache.batch, b, head, t0, t1, _ptr(k_out),
                                   _ptr(v_out)))
 
