@@ -725,9 +725,8 @@ int bgtq_fp4_attn_workspace(int n_kv_heads, int group, int batch, int t, int64_t
  * rounded to fp16 for a half output, as in bgtq_prefill_attn, and in 22 bits
  * (two fp16 parts) for a float one; their sum is taken before.
  * Positions from n on, and their bytes, do not matter.
- * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (more than 65535 sequences,
- * batch * H > 65535,
- * batch * H * max_len >= 2^34, sizes past 2^31 rows), CUDA.
+ * Errors: INVALID_ARG, WORKSPACE, UNSUPPORTED (batch * H > 65535,
+ * batch * H * (max_len / 16 + 1) >= 2^30, batch * H * group * t + 256 >= 2^31), CUDA.
  */
 int bgtq_fp4_attn(void* stream, const bgtq_rope* rope, const int32_t* pos, const bgtq_rows* q, int group, int batch,
                   int t, const bgtq_fp4_cache* cache, const int32_t* seq_lens, int64_t max_len, void* out,

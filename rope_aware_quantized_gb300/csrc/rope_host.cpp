@@ -225,9 +225,8 @@ int bgtq_fp4_attn(void* stream, const bgtq_rope* rope, const int32_t* pos, const
     if (reinterpret_cast<uintptr_t>(out) & 15) return set_error(BGTQ_ERR_INVALID_ARG, "out must be 16-byte aligned");
     if (reinterpret_cast<uintptr_t>(ws) & 255) return set_error(BGTQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     max_len = std::min(max_len, c->capacity);
-    if ((uint64_t)batch * c->n_heads * group * (uint64_t)t + 256 >= (1ull << 31) ||
-        ((int64_t)t * group > kFp4RowsLeast && (uint64_t)batch * c->n_heads * (uint64_t)(max_len + 256) >= (1ull << 31)))
-        return set_error(BGTQ_ERR_UNSUPPORTED, "batch * query heads * t and batch * heads * max_len must stay below 2^31");
+    if ((uint64_t)batch * c->n_heads * group * (uint64_t)t + 256 >= (1ull << 31))
+        return set_error(BGTQ_ERR_UNSUPPORTED, "batch * query heads * t + 256 must stay below 2^31");
     if ((uint64_t)batch * c->n_heads * (uint64_t)(max_len / kGroup + 1) >= (1ull << 30))
         return set_error(BGTQ_ERR_UNSUPPORTED, "batch * heads * max_len must stay below 2^34");
     const size_t need = fp4_attn_workspace_bytes(c->n_heads, group, batch, t, max_len);

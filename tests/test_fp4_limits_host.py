@@ -1,0 +1,24 @@
+"""Host checks of the 4-bit cache's limits (no GPU: every call below is refused, or its refusal is the next check's)."""
+
+import ctypes as C
+
+import pytest
+
+import rope_aware_quantized_gb300 as bg
+from tests.test_rope_fp4_host import call_attn, fp4
+
+
+def virtual(capacity, heads):
+    """A paged cache with few pages of a large virtual capacity."""
+    return fp4(capacity=capacity, heads=heads, page=256, n_pages=8)
+
+
+@pytest.mark.parametrize("t", [1, 2, 3, 40])
+def test_rows_do_not_change_the_limit_on_lengths(t):
+    """2048 (sequence, head)s of up to 2^20 positions: as many rows as wanted (past the limits, a workspace too small is what is refused)."""
+    c = virtual(1 << 20, 8)
+    rc, msg = call_attn(group=8, batch=256, t=t, c=c, max_len=1 << 20, ws_bytes=0)
+    assert rc == -4 and "workspace" in msg
+    # 2^34 positions in all are one step too many
+    rc, msg = call_attn(group=8, batch=256, t=t, c=virtual(1 << 23, 8), max_len=1 << 23, ws_bytes=0)
+    assert rc == -2 and "2^34" in msg
