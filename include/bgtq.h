@@ -691,7 +691,8 @@ int bgtq_fp4_cache_bytes(int n_kv_heads, int batch, int64_t capacity, size_t* by
  * ordered by the caller).  An unmapped page: those tokens are skipped
  * (BGTQ_STATUS_PAGE_RANGE).  Inputs are finite: one that is not gives
  * unspecified codes of its own block.
- * Errors: INVALID_ARG, UNSUPPORTED (more than 65535 sequences), CUDA.
+ * Errors: INVALID_ARG, UNSUPPORTED (more than 65535 sequences, t_new / 64 * H
+ * >= 2^31), CUDA.
  */
 int bgtq_fp4_append(void* stream, const bgtq_rope* rope, const int32_t* pos, const bgtq_rows* k, const bgtq_rows* v,
                     int batch, int t_new, const int32_t* pos_start, const bgtq_fp4_cache* cache, int32_t* dev_status);

@@ -74,6 +74,12 @@ cudaError_t launch_fp4_attn(cudaStream_t s, const Fp4Attn& a);
 // The tiles' part (fp4_tiles.cu); ws behind the counters of the one-pass kernel.
 size_t fp4_tiles_workspace_bytes(int64_t heads, int64_t rows, int64_t max_len);
 cudaError_t launch_fp4_tiles(cudaStream_t s, const Fp4Attn& a, void* ws);
+// Groups of a sequence that t_new positions can touch (more than the capacity:
+// no sequence takes them, and the kernels' first blocks say so), and the blocks
+// of the warp-a-group append of all heads.
+constexpr int kFp4AppendWarps = 4;
+inline int64_t fp4_append_groups(int64_t t_new, int64_t capacity) { return ((t_new < capacity ? t_new : capacity) + kGroup - 2) / kGroup + 1; }
+inline int64_t fp4_append_blocks(int64_t groups, int heads) { return (groups + kFp4AppendWarps - 1) / kFp4AppendWarps * heads; }
 cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsView& k, const RowsView& v, int batch, int t_new,
                               const int32_t* pos_start, const bgtq_fp4_cache& c, int32_t* status);
 cudaError_t launch_fp4_dequant(cudaStream_t s, const bgtq_fp4_cache& c, int b, int head, int64_t t0, int64_t t1, float* k_out,

@@ -16,8 +16,6 @@
 // 1880 warp-instructions a group at 16 warps a SM.
 #include <cuda_fp16.h>
 
-#include <algorithm>
-
 #include "fp4.cuh"
 
 namespace bgtq {
@@ -190,7 +188,7 @@ __global__ void __launch_bounds__(kApThreads, 7) fp4_append_kernel(const __grid_
         reinterpret_cast<uint4*>(g)[tid] = reinterpret_cast<const uint4*>(img)[tid];
 }
 
-constexpr int kBulkWarps = 4;
+constexpr int kBulkWarps = kFp4AppendWarps;
 
 template <bool kRope, bool kHalves>  // kHalves: both dims of a rotary block are 64 apart (layout 0), or there is none
 __global__ void __launch_bounds__(32 * kBulkWarps) fp4_append_bulk_kernel(const __grid_constant__ Fp4AppendParams p) {
@@ -349,14 +347,12 @@ cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsVie
     p.cap = c.capacity;
     p.pos_start = pos_start;
     p.status = status;
-    // groups that t_new positions can touch (more than the capacity: no sequence takes
-    // them, and the kernels' first blocks say so)
-    const int64_t groups = (std::min<int64_t>(t_new, c.capacity) + 14) / kGroup + 1;
+    const int64_t groups = fp4_append_groups(t_new, c.capacity);
     // Up to 16 groups a SM (two waves of blocks): the block-a-group kernel's short chain of
     // waits; beyond, the work counts (131043 tokens x 2 heads: 64 us with a block
     // a group, whose six warps each pay for the set-up).
     const bool bulk = groups * c.n_heads * batch > 16 * 152;
-    const int64_t blocks = (bulk ? (groups + kBulkWarps - 1) / kBulkWarps : groups) * c.n_heads;
+    const int64_t blocks = bulk ? fp4_append_blocks(groups, c.n_heads) : groups * c.n_heads;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;

@@ -188,6 +188,8 @@ int bgtq_fp4_append(void* stream, const bgtq_rope* rope, const int32_t* pos, con
     if (batch > 65535) return set_error(BGTQ_ERR_UNSUPPORTED, "at most 65535 sequences per call");
     if (batch == 0 || t_new == 0) return BGTQ_OK;
     if ((rc = check_new(rope, pos, k, v, batch, c->n_heads, t_new, pos_start))) return rc;
+    if (fp4_append_blocks(fp4_append_groups(t_new, c->capacity), c->n_heads) > INT32_MAX)
+        return set_error(BGTQ_ERR_UNSUPPORTED, "t_new / 64 * heads must stay below 2^31");
     const cudaError_t e = launch_fp4_append((cudaStream_t)stream, make_rope(rope, pos, (int64_t)batch * t_new), make_rows(*k),
                                             make_rows(*v), batch, t_new, pos_start, *c, status);
     if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "fp4_append launch: %s", cudaGetErrorString(e));

@@ -5,7 +5,7 @@ import ctypes as C
 import pytest
 
 import rope_aware_quantized_gb300 as bg
-from tests.test_rope_fp4_host import call_attn, fp4
+from tests.test_rope_fp4_host import call_append, call_attn, fp4, rows
 
 
 def virtual(capacity, heads):
@@ -22,3 +22,11 @@ def test_rows_do_not_change_the_limit_on_lengths(t):
     # 2^34 positions in all are one step too many
     rc, msg = call_attn(group=8, batch=256, t=t, c=virtual(1 << 23, 8), max_len=1 << 23, ws_bytes=0)
     assert rc == -2 and "2^34" in msg
+
+
+def test_an_append_of_more_blocks_than_a_launch_has_is_refused():
+    """One row broadcast to 2^30 positions of 4096 heads in a paged cache of as large a virtual capacity."""
+    c = virtual(1 << 30, 4096)
+    for heads, t, code in ((4096, 1 << 30, -2), (4096, 1 << 25, -2)):
+        rc, msg = call_append(c=virtual(1 << 30, heads), t=t, k=rows(sb=0, sh=0, st=0), v=rows(sb=0, sh=0, st=0))
+        assert rc == code and "2^31" in msg
