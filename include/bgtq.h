@@ -675,7 +675,8 @@ typedef struct {
 } bgtq_fp4_cache;
 
 /* Bytes of the groups of `batch` sequences of `capacity` positions (a multiple
- * of 16); for a paged cache batch = n_pages, capacity = page_tokens.  Host only. */
+ * of 16); for a paged cache batch = n_pages, capacity = page_tokens.  Host only.
+ * Errors: INVALID_ARG, UNSUPPORTED (2^63 bytes or more). */
 int bgtq_fp4_cache_bytes(int n_kv_heads, int batch, int64_t capacity, size_t* bytes);
 
 /*

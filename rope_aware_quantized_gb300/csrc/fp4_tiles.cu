@@ -782,7 +782,8 @@ int64_t pair_blocks(int64_t rows) { return (rows + 2 * kRows - 1) / (2 * kRows);
 // parts and kSms smaller ones, none of less than kLeastTiles but the last.
 size_t fp4_tiles_workspace_bytes(int64_t heads, int64_t rows, int64_t max_len) {
     const int64_t tiles = std::max<int64_t>(1, (max_len + kKeys - 1) / kKeys);
-    const int64_t slots = std::min<int64_t>(2 * kSms, heads * pair_blocks(rows) * ((tiles + kLeastTiles - 1) / kLeastTiles));
+    auto most = [](int64_t n) { return std::min<int64_t>(n, 2 * kSms); };  // (the product of the largest shapes passes 64 bits)
+    const int64_t slots = most(most(heads) * most(pair_blocks(rows)) * most((tiles + kLeastTiles - 1) / kLeastTiles));
     return (size_t)slots * 2 * kRows * (8 + 4 * kD);
 }
 

@@ -176,6 +176,8 @@ int bgtq_fp4_cache_bytes(int H, int batch, int64_t capacity, size_t* bytes) {
     if (!bytes) return set_error(BGTQ_ERR_INVALID_ARG, "NULL pointer");
     if (H < 1 || H > 4096 || batch < 0 || capacity < 0 || capacity % kGroup || capacity > (1 << 30))
         return set_error(BGTQ_ERR_INVALID_ARG, "bad head count, batch or capacity (a multiple of 16, at most 2^30)");
+    if (capacity && (uint64_t)batch * H > (uint64_t)INT64_MAX / kGroupBytes / (uint64_t)(capacity / kGroup))
+        return set_error(BGTQ_ERR_UNSUPPORTED, "the groups' bytes do not fit 64 bits");
     *bytes = (size_t)batch * H * (size_t)(capacity / kGroup) * kGroupBytes;
     return BGTQ_OK;
 }

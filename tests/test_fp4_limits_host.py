@@ -30,3 +30,15 @@ def test_an_append_of_more_blocks_than_a_launch_has_is_refused():
     for heads, t, code in ((4096, 1 << 30, -2), (4096, 1 << 25, -2)):
         rc, msg = call_append(c=virtual(1 << 30, heads), t=t, k=rows(sb=0, sh=0, st=0), v=rows(sb=0, sh=0, st=0))
         assert rc == code and "2^31" in msg
+
+
+def test_sizes_past_64_bits_are_refused_or_right():
+    big = (1 << 31) - 1
+    for args in ((4096, big, 1 << 30), (4096, 1 << 30, 1 << 30)):  # 2^69 and 2^68 groups
+        with pytest.raises(bg.BgtqError, match="64 bits"):
+            bg.bgtq_fp4_cache_bytes(*args)
+    assert bg.bgtq_fp4_cache_bytes(4096, 1 << 12, 1 << 30) == 2304 << 50  # fits
+    # no shape needs more than 304 slots of 256 rows of a workspace: the largest shapes as any large one
+    need = bg.bgtq_fp4_attn_workspace(8, 8, 300, 2048, 1 << 20)
+    for args in ((4096, 8, big, big, 1 << 30), (4096, 8, 1 << 30, 1 << 30, 1 << 30), (4096, 8, 1 << 29, 1 << 20, 1 << 30), (1, 8, big, big, 1 << 30)):
+        assert bg.bgtq_fp4_attn_workspace(*args) == need
