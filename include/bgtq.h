@@ -721,6 +721,7 @@ int bgtq_fp4_attn_workspace(int n_kv_heads, int group, int batch, int t, int64_t
  *              (BGTQ_STATUS_SEQLEN_CAPACITY; its rows are then the cut one's last)
  *   out        device, [batch][H*group][t][128], half (out_dtype 0) or float
  *              (1), 16-byte aligned
+ *   softmax_scale  in (0, 2^40]
  *   workspace  device, 256-byte aligned, bgtq_fp4_attn_workspace bytes; two
  *              calls that may overlap on the GPU need two
  * Logits are fp16 products summed in fp32.  Probabilities meet the values

@@ -215,7 +215,8 @@ int bgtq_fp4_attn(void* stream, const bgtq_rope* rope, const int32_t* pos, const
     if (batch < 0 || t < 0 || max_len < 0) return set_error(BGTQ_ERR_INVALID_ARG, "batch, t and max_len must be >= 0");
     if (group < 1 || group > 8) return set_error(BGTQ_ERR_INVALID_ARG, "group must be in 1..8");
     if (out_dtype != 0 && out_dtype != 1) return set_error(BGTQ_ERR_INVALID_ARG, "out_dtype must be 0 (half) or 1 (float)");
-    if (!(scale > 0.0f) || !std::isfinite(scale)) return set_error(BGTQ_ERR_INVALID_ARG, "softmax_scale must be finite and > 0");
+    // (a larger one could take logits past the kernels' first reference, -1e30: |q.k| < 2^39)
+    if (!(scale > 0.0f) || !(scale <= 1099511627776.0f)) return set_error(BGTQ_ERR_INVALID_ARG, "softmax_scale must be in (0, 2^40]");
     if (batch > 65535 || (int64_t)batch * c->n_heads > 65535)
         return set_error(BGTQ_ERR_UNSUPPORTED, "at most 65535 sequences x KV heads per call");
     if (batch == 0 || t == 0) return BGTQ_OK;

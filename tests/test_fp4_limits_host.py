@@ -42,3 +42,12 @@ def test_sizes_past_64_bits_are_refused_or_right():
     need = bg.bgtq_fp4_attn_workspace(8, 8, 300, 2048, 1 << 20)
     for args in ((4096, 8, big, big, 1 << 30), (4096, 8, 1 << 30, 1 << 30, 1 << 30), (4096, 8, 1 << 29, 1 << 20, 1 << 30), (1, 8, big, big, 1 << 30)):
         assert bg.bgtq_fp4_attn_workspace(*args) == need
+
+
+def test_a_scale_whose_logits_pass_the_references_range_is_refused():
+    """A row's first reference is -1e30: logits below it would get no weight.  |q.k| < 128 * 65504 * 61440 < 2^39, so a scale of 2^40 is safe."""
+    for scale in (2.0 ** 40 * (1 + 2.0 ** -23), 1e19, 1e30, 3e38):
+        rc, msg = call_attn(scale=scale)
+        assert rc == -1 and "softmax_scale" in msg
+    rc, msg = call_attn(scale=2.0 ** 40, ws_bytes=0)
+    assert rc == -4
