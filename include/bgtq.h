@@ -618,8 +618,11 @@ int bgtq_rope_table(void* stream, const double* inv_freq, int64_t n_pos, double 
  *   in_dtype, out_dtype  BGTQ_F16, BGTQ_F32 or BGTQ_BF16, of q and k alike
  *   inverse      1: rotate back (sin negated), which is also the gradient of
  *                the rotation
- * Output rows must not overlap one another, nor inputs unless in place (the
- * former and each output against its own input are checked).
+ * Output rows must not overlap one another, nor inputs unless in place: they
+ * may lie between an input's rows (other heads of one tensor).  Checked are the
+ * rows of an output, q_out against k_out where their strides agree, and each
+ * output against its own input, where rows of other strides than the input's
+ * must lie before or behind all of it.
  * Errors: INVALID_ARG, UNSUPPORTED (batch * t >= 2^31), CUDA.
  */
 int bgtq_rope_rows(void* stream, const bgtq_rope* rope, const int32_t* pos, int batch, int t, const bgtq_rows* q,

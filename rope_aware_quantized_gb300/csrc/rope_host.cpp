@@ -57,15 +57,57 @@ int64_t extent(const bgtq_rows& r, int batch, int heads, int64_t t, int elem) {
     return (r.stride_b * (batch - 1) + r.stride_h * (heads - 1) + r.stride_t * (t - 1) + kD) * elem;
 }
 
+// Rows of two tensors with the same steps in memory: whether one row of each
+// meets, i.e. some lo < delta + c0 s0 + c1 s1 + c2 s2 < hi with
+// least[k] <= c[k] <= most[k] (s falling, steps of 0 left out).  A step is no
+// shorter than the smaller ones' whole reach (outputs are checked for that), so
+// few c fit in each.
+struct Steps {
+    int n = 0;
+    int64_t s[3], least[3], most[3];
+};
+bool some_meet(const Steps& x, int k, int64_t delta, int64_t lo, int64_t hi) {
+    if (k == x.n) return lo < delta && delta < hi;
+    int64_t below = 0, above = 0;  // what the smaller steps can add
+    for (int i = k + 1; i < x.n; ++i) {
+        below += x.s[i] * -x.least[i];
+        above += x.s[i] * x.most[i];
+    }
+    auto floor_div = [](int64_t a, int64_t b) { return a / b - (a % b < 0); };
+    const int64_t first = std::max(x.least[k], floor_div(lo - above - delta, x.s[k]));
+    const int64_t last = std::min(x.most[k], floor_div(hi + below - delta, x.s[k]) + 1);
+    for (int64_t c = first; c <= last; ++c)
+        if (some_meet(x, k + 1, delta + c * x.s[k], lo, hi)) return true;
+    return false;
+}
+
+enum class Meet { kApart, kSame, kSome, kUnknown };
+// Rows a (na heads) and b (nb): apart, the very same ones, some of them in one
+// another, or (steps that differ within one another's extent) not told.
+Meet rows_meet(const bgtq_rows& a, int na, int ea, const bgtq_rows& b, int nb, int eb, int batch, int64_t t) {
+    const char *pa = static_cast<const char*>(a.data), *pb = static_cast<const char*>(b.data);
+    if (pa + extent(a, batch, na, t, ea) <= pb || pb + extent(b, batch, nb, t, eb) <= pa) return Meet::kApart;
+    const int64_t n[2][3] = {{batch, na, t}, {batch, nb, t}};
+    const int64_t s[2][3] = {{a.stride_b * ea, a.stride_h * ea, a.stride_t * ea}, {b.stride_b * eb, b.stride_h * eb, b.stride_t * eb}};
+    Steps x;
+    for (int i = 0; i < 3; ++i) {
+        if (n[0][i] == 1 && n[1][i] == 1) continue;
+        if (n[0][i] > 1 && n[1][i] > 1 && s[0][i] != s[1][i]) return Meet::kUnknown;
+        const int64_t step = n[1][i] > 1 ? s[1][i] : s[0][i];
+        if (step == 0) return Meet::kUnknown;
+        int k = x.n++;
+        for (; k > 0 && x.s[k - 1] < step; --k) x.s[k] = x.s[k - 1], x.least[k] = x.least[k - 1], x.most[k] = x.most[k - 1];
+        x.s[k] = step, x.least[k] = 1 - n[0][i], x.most[k] = n[1][i] - 1;
+    }
+    if (pa == pb && na == nb && ea == eb) return Meet::kSame;
+    return some_meet(x, 0, pb - pa, (int64_t)-kD * eb, (int64_t)kD * ea) ? Meet::kSome : Meet::kApart;
+}
+
 // An output and its input: the same rows, or apart.
 int check_in_place(const bgtq_rows& in, const bgtq_rows& out, const char* name, int batch, int heads, int64_t t, int di, int dt) {
-    const int ei = dtype_size(di), eo = dtype_size(dt);
-    const char *a = static_cast<const char*>(in.data), *b = static_cast<const char*>(out.data);
-    if (a + extent(in, batch, heads, t, ei) <= b || b + extent(out, batch, heads, t, eo) <= a) return BGTQ_OK;
-    const bool same = a == b && di == dt && (batch == 1 || in.stride_b == out.stride_b) && (heads == 1 || in.stride_h == out.stride_h) &&
-                      (t == 1 || in.stride_t == out.stride_t);
-    if (!same) return set_error(BGTQ_ERR_INVALID_ARG, "%s_out overlaps %s without being it", name, name);
-    return BGTQ_OK;
+    const Meet m = rows_meet(in, heads, dtype_size(di), out, heads, dtype_size(dt), batch, t);
+    if (m == Meet::kApart || (m == Meet::kSame && di == dt)) return BGTQ_OK;
+    return set_error(BGTQ_ERR_INVALID_ARG, "%s_out overlaps %s without being it", name, name);
 }
 
 int check_fp4(const bgtq_fp4_cache* c) {
@@ -136,17 +178,19 @@ int bgtq_rope_rows(void* stream, const bgtq_rope* rope, const int32_t* pos, int 
     const int ei = dtype_size(in_dtype), eo = dtype_size(out_dtype);
     RowsView none = {nullptr, 0, 0, 0}, qi = none, qo = none, ki = none, ko = none;
     if (n_q) {
-        if ((rc = check_rows(q, "q", batch, n_q, t, ei, false)) || (rc = check_rows(q_out, "q_out", batch, n_q, t, eo, true)) ||
-            (rc = check_in_place(*q, *q_out, "q", batch, n_q, t, in_dtype, out_dtype)))
-            return rc;
+        if ((rc = check_rows(q, "q", batch, n_q, t, ei, false)) || (rc = check_rows(q_out, "q_out", batch, n_q, t, eo, true))) return rc;
         qi = make_rows(*q), qo = make_rows(*q_out);
     }
     if (n_k) {
-        if ((rc = check_rows(k, "k", batch, n_k, t, ei, false)) || (rc = check_rows(k_out, "k_out", batch, n_k, t, eo, true)) ||
-            (rc = check_in_place(*k, *k_out, "k", batch, n_k, t, in_dtype, out_dtype)))
-            return rc;
+        if ((rc = check_rows(k, "k", batch, n_k, t, ei, false)) || (rc = check_rows(k_out, "k_out", batch, n_k, t, eo, true))) return rc;
         ki = make_rows(*k), ko = make_rows(*k_out);
     }
+    if (n_q && n_k) {
+        const Meet m = rows_meet(*q_out, n_q, eo, *k_out, n_k, eo, batch, t);
+        if (m == Meet::kSome || m == Meet::kSame) return set_error(BGTQ_ERR_INVALID_ARG, "q_out and k_out overlap");
+    }
+    if (n_q && (rc = check_in_place(*q, *q_out, "q", batch, n_q, t, in_dtype, out_dtype))) return rc;
+    if (n_k && (rc = check_in_place(*k, *k_out, "k", batch, n_k, t, in_dtype, out_dtype))) return rc;
     const cudaError_t e = launch_rope_rows((cudaStream_t)stream, make_rope(rope, pos, (int64_t)batch * t), batch, t, qi, qo, n_q,
                                            ki, ko, n_k, in_dtype, out_dtype, inverse, status);
     if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "rope_rows launch: %s", cudaGetErrorString(e));
