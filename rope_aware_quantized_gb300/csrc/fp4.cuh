@@ -27,18 +27,25 @@ struct Fp4Map {
     int64_t cap_groups;         // groups of a sequence
     int64_t max_pages, n_pages;
     int H, lg;                  // lg = log2(P / 16)
+    int batch;                  // sequences of the launch
+    int32_t* status;            // where a failed range check is reported
 #ifdef __CUDACC__
-    // nullptr when the page_table entry is outside [0, n_pages)
+    // nullptr when the page_table entry is outside [0, n_pages) (and, in the
+    // BGTQ_DEBUG_BOUNDS build, when b, h or gi is out of range)
     __device__ __forceinline__ uint8_t* group(int b, int h, int64_t gi) const {
+        if (!debug_in_range(b >= 0 && b < batch && h >= 0 && h < H && gi >= 0 && gi < cap_groups, status)) return nullptr;
         if (!page_table) return base + (((int64_t)b * H + h) * cap_groups + gi) * kGroupBytes;
         const int32_t pg = page_table[(int64_t)b * max_pages + (gi >> lg)];
-        if (pg < 0 || (int64_t)pg >= n_pages) return nullptr;
+        if (pg < 0 || (int64_t)pg >= n_pages) {
+            debug_in_range(false, status);
+            return nullptr;
+        }
         return base + ((((int64_t)pg * H + h) << lg) + (gi & (((int64_t)1 << lg) - 1))) * kGroupBytes;
     }
 #endif
 };
 
-inline Fp4Map make_fp4_map(const bgtq_fp4_cache& c) {
+inline Fp4Map make_fp4_map(const bgtq_fp4_cache& c, int batch, int32_t* status) {
     Fp4Map m;
     m.base = static_cast<uint8_t*>(c.groups);
     m.page_table = c.page_table;
@@ -49,6 +56,8 @@ inline Fp4Map make_fp4_map(const bgtq_fp4_cache& c) {
     m.lg = 0;
     if (c.page_table)
         while (((int64_t)kGroup << m.lg) < c.page_tokens) ++m.lg;
+    m.batch = batch;
+    m.status = status;
     return m;
 }
 
@@ -82,7 +91,7 @@ inline int64_t fp4_append_groups(int64_t t_new, int64_t capacity) { return ((t_n
 inline int64_t fp4_append_blocks(int64_t groups, int heads) { return (groups + kFp4AppendWarps - 1) / kFp4AppendWarps * heads; }
 cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsView& k, const RowsView& v, int batch, int t_new,
                               const int32_t* pos_start, const bgtq_fp4_cache& c, int32_t* status);
-cudaError_t launch_fp4_dequant(cudaStream_t s, const bgtq_fp4_cache& c, int b, int head, int64_t t0, int64_t t1, float* k_out,
+cudaError_t launch_fp4_dequant(cudaStream_t s, const bgtq_fp4_cache& c, int batch, int b, int head, int64_t t0, int64_t t1, float* k_out,
                                float* v_out);
 
 #ifdef __CUDACC__

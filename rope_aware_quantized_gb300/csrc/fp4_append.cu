@@ -107,7 +107,10 @@ __global__ void __launch_bounds__(kApThreads, 7) fp4_append_kernel(const __grid_
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int ps = p.pos_start[b];
     if (ps < 0 || (int64_t)ps + p.t_new > p.cap) {
-        if (blockIdx.x == 0 && tid == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_APPEND_CAPACITY);
+        if (blockIdx.x == 0 && tid == 0 && p.status) {
+            atomicOr(p.status, BGTQ_STATUS_APPEND_CAPACITY);
+            debug_in_range(false, p.status);  // positions past the capacity
+        }
         return;
     }
     const int64_t end = (int64_t)ps + p.t_new;
@@ -199,7 +202,10 @@ __global__ void __launch_bounds__(32 * kBulkWarps) fp4_append_bulk_kernel(const 
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int ps = p.pos_start[b];
     if (ps < 0 || (int64_t)ps + p.t_new > p.cap) {
-        if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) atomicOr(p.status, BGTQ_STATUS_APPEND_CAPACITY);
+        if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) {
+            atomicOr(p.status, BGTQ_STATUS_APPEND_CAPACITY);
+            debug_in_range(false, p.status);  // positions past the capacity
+        }
         return;
     }
     const int64_t end = (int64_t)ps + p.t_new;
@@ -342,7 +348,7 @@ cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsVie
     p.rope = r;
     p.k = k;
     p.v = v;
-    p.map = make_fp4_map(c);
+    p.map = make_fp4_map(c, batch, status);
     p.t_new = t_new;
     p.cap = c.capacity;
     p.pos_start = pos_start;
@@ -368,9 +374,9 @@ cudaError_t launch_fp4_append(cudaStream_t s, const RopeParams& r, const RowsVie
                          : cudaLaunchKernelEx(&cfg, fp4_append_bulk_kernel<true, false>, p);
 }
 
-cudaError_t launch_fp4_dequant(cudaStream_t s, const bgtq_fp4_cache& c, int b, int head, int64_t t0, int64_t t1, float* k_out,
+cudaError_t launch_fp4_dequant(cudaStream_t s, const bgtq_fp4_cache& c, int batch, int b, int head, int64_t t0, int64_t t1, float* k_out,
                                float* v_out) {
-    fp4_dequant_kernel<<<(unsigned)(t1 - t0), kD, 0, s>>>(make_fp4_map(c), b, head, t0, t1, k_out, v_out);
+    fp4_dequant_kernel<<<(unsigned)(t1 - t0), kD, 0, s>>>(make_fp4_map(c, batch, nullptr), b, head, t0, t1, k_out, v_out);
     return cudaGetLastError();
 }
 

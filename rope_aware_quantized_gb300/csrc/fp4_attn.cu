@@ -459,8 +459,10 @@ __global__ void __launch_bounds__(kThreads, NQ <= kTwoCtas ? 2 : 1) fp4_attn_ker
             // (one stage a warp before the query's cos and sin, the others after: those
             // small loads would queue behind all the warps' copies)
             if (lane == 0) fetch_first(0, 1);
-            if (tid == 0 && rank == 0 && h == 0 && g0 == 0 && p.status && n != p.seq_lens[b])
+            if (tid == 0 && rank == 0 && h == 0 && g0 == 0 && p.status && n != p.seq_lens[b]) {
                 atomicOr(p.status, BGTQ_STATUS_SEQLEN_CAPACITY);
+                debug_in_range(false, p.status);  // groups past the bound
+            }
 #pragma unroll
             for (int i = 0; i < NQ; ++i) {
                 const int r = warp + kWarps * i;

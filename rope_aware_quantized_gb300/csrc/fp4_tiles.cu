@@ -348,7 +348,10 @@ __global__ void __launch_bounds__(kTileThreads, 1) fp4_tiles_kernel(const __grid
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int n = clamp_len(p, b);
-    if (tid == 0 && part == 0 && pb == 0 && h == 0 && p.status && n != p.seq_lens[b]) atomicOr(p.status, BGTQ_STATUS_SEQLEN_CAPACITY);
+    if (tid == 0 && part == 0 && pb == 0 && h == 0 && p.status && n != p.seq_lens[b]) {
+        atomicOr(p.status, BGTQ_STATUS_SEQLEN_CAPACITY);
+        debug_in_range(false, p.status);  // groups past the bound
+    }
     const int tiles = block_tiles(p, pb, n);
     const int j0 = part * p.part_tiles, j1 = cut ? min(tiles, j0 + p.part_tiles) : tiles;
     if (part > 0 && j0 >= tiles) return;

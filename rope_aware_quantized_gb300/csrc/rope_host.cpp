@@ -283,7 +283,7 @@ int bgtq_fp4_attn(void* stream, const bgtq_rope* rope, const int32_t* pos, const
     Fp4Attn a;
     a.rope = make_rope(rope, pos, (int64_t)batch * t);
     a.q = make_rows(*q);
-    a.map = make_fp4_map(*c);
+    a.map = make_fp4_map(*c, batch, status);
     a.seq_lens = seq_lens;
     a.cap = c->capacity;
     a.max_len = max_len;
@@ -307,7 +307,7 @@ int bgtq_fp4_dequant(void* stream, const bgtq_fp4_cache* c, int batch, int b, in
     if (b < 0 || b >= batch || head < 0 || head >= c->n_heads) return set_error(BGTQ_ERR_INVALID_ARG, "sequence or head out of range");
     if (t0 < 0 || t1 < t0 || t1 > c->capacity) return set_error(BGTQ_ERR_INVALID_ARG, "positions out of range");
     if (t0 == t1 || (!k_out && !v_out)) return BGTQ_OK;
-    const cudaError_t e = launch_fp4_dequant((cudaStream_t)stream, *c, b, head, t0, t1, k_out, v_out);
+    const cudaError_t e = launch_fp4_dequant((cudaStream_t)stream, *c, batch, b, head, t0, t1, k_out, v_out);
     if (e != cudaSuccess) return set_error(BGTQ_ERR_CUDA, "fp4_dequant launch: %s", cudaGetErrorString(e));
     return BGTQ_OK;
 }
