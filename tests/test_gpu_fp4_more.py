@@ -18,18 +18,15 @@ def seeded():
     torch.manual_seed(23)
 
 
-def sampled(c, half, rng, some, **kw):
-    """Runs a case and checks `some` of its (sequence, query head)s, each as a case of its own."""
-    out = c.run(half, **kw)
-    B, hq = c.q.shape[:2]
-    for b, a in {(int(b), int(a)) for b, a in zip(rng.integers(0, B, some), rng.integers(0, hq, some))}:
+def check(c, out, half, units):
+    """Checks those (sequence, query head)s of a case, each as a case of its own."""
+    for b, a in units:
         one = Case.__new__(Case)
         one.H, one.G, one.t, one.lens, n = 1, 1, c.t, [c.lens[b]], -(-c.lens[b] // 16)
         rows = torch.from_numpy(group_rows(c.cache, b, a // c.G)[:n]).cuda()
         one.cache = types.SimpleNamespace(groups=c.cache.groups.view(-1, F.GROUP_BYTES)[rows].flatten(), capacity=16 * n, page_tokens=0, n_kv_heads=1)
         one.q = c.q[b:b + 1, a:a + 1]
         one.check(out[b:b + 1, a:a + 1], half)
-    return out
 
 
 def filled(B, H, G, t, lens, cap, page, seed, n_pages=0, spread=1.0):
@@ -56,5 +53,45 @@ def test_many_rows_under_a_large_virtual_length(t):
     lens[0] = 300
     c = filled(256, 8, 8, t, lens, 1 << 20, 256, t, n_pages=600)
     st = status()
-    sampled(c, True, rng, 25, max_len=1 << 20, status=st)
+    out = c.run(True, max_len=1 << 20, status=st)
+    check(c, out, True, {(int(b), int(a)) for b, a in zip(rng.integers(0, 256, 25), rng.integers(0, 64, 25))})
     assert st.item() == 0
+
+
+# (sequences, KV heads, bound): where the tiles are split unevenly, the parts of a head in tiles
+UNEVEN = [(10, 8, 8192, (43, 21)), (15, 4, 16384, (52, 52, 24))]
+
+
+@pytest.mark.parametrize("B,H,top,parts", UNEVEN)
+@pytest.mark.parametrize("t,half", [(20, True), (20, False), (33, True), (40, False)])  # 80, 132 and 160 rows
+def test_uneven_parts_of_a_head(B, H, top, parts, t, half):
+    """Heads whose tiles are cut into equal parts and a smaller one, with lengths that end before, at and behind each border."""
+    assert sum(parts) == top // 128
+    ends = [128 * sum(parts[:i + 1]) for i in range(len(parts) - 1)]
+    rng = np.random.default_rng(top + t)
+    lens = [top, top - 1] + [e + d for e in ends for d in (-1, 0, 1, t, 200)] + [1, t]
+    lens = (lens + rng.integers(1, top, B).tolist())[:B]
+    c = filled(B, H, 4, t, lens, top, 0, seed=t)
+    out = c.run(half, max_len=top)
+    check(c, out, half, {(b, (5 * b + 1) % (4 * H)) for b in range(B)} | {(0, 0), (0, 4 * H - 1)})
+    assert torch.equal(out, c.run(half, max_len=top))
+
+
+@pytest.mark.parametrize("t", [1, 5, 40])  # 8, 40 and 320 rows a head
+@pytest.mark.parametrize("page", [16, 32])
+@pytest.mark.parametrize("half", [False, True])
+def test_an_unmapped_page_is_reported_and_touches_no_other_sequence(t, page, half):
+    c = Case(2, 8, t, [320, 500], 512, page, seed=page + t)
+    st = status()
+    good = c.run(half, status=st)
+    assert st.item() == 0
+    for entry in (-1, c.cache.n_pages, 1 << 30):
+        c.cache.page_table[0, 1] = entry
+        out = c.run(half, status=st.zero_())
+        assert st.item() == bg.STATUS_PAGE_RANGE
+        assert torch.equal(out[1], good[1])
+    # pages behind the last position are not looked at
+    c.cache.page_table[1, -(-500 // page):] = -1
+    c.lens, c.seq = [16, 500], i32([16, 500])
+    out = c.run(half, status=st.zero_())
+    assert st.item() == 0 and torch.equal(out[1], good[1])
