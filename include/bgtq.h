@@ -570,8 +570,10 @@ int bgtq_evict(const bgtq_plan* plan, void* stream, const bgtq_cache* cache, con
 /*
  * ---- Rotary positions.  The paper's keys are cached after their rotation
  * ("under RoPE a key's contribution to a logit is a sum over 2-D frequency
- * blocks", English abstract); these calls apply it, so that a model's
- * projections go to the cache, and its queries to attention, as they are.
+ * blocks", English abstract); these calls apply it, so that an fp16 model's
+ * projections go to the cache, and its queries to attention, as they are
+ * (bgtq_rope_rows takes other types too and gives fp16; values of other types
+ * are the caller's to convert).
  * Block i of 64 is the pair of dims (i, i + 64) of layout 0 or (2i, 2i + 1) of
  * layout 1, rotated by the angle of position p = pos[axis[i]]:
  *   lo' = lo cos[p][i] - hi sin[p][i],  hi' = hi cos[p][i] + lo sin[p][i]

@@ -12,8 +12,9 @@
 //                the other kernel 5.9)
 //   many         a warp a group, its rows' loads all on their way at once
 // Floor: 512 bytes in and 144 out for a token and head, 512 of tables a token.
-// 131043 tokens of 2 heads, rotated: 51 us, 69 % of the copy bandwidth; bound by
-// 1880 warp-instructions a group at 16 warps a SM.
+// 131043 tokens of 2 heads, rotated: 51.5 us, 68 % of the copy bandwidth.  Bound by
+// the bytes in flight: 128 registers leave 16 warps a SM, which spend 39 % of their
+// time waiting for loads (issue slots 45 % busy).
 #include <cuda_fp16.h>
 
 #include "fp4.cuh"

@@ -22,6 +22,12 @@
 // to pass through shared memory once more, decoded (4.5 -> 16 bits a value).
 // Two groups at a time: their chains of products and exponentials run side by
 // side, and the wait, the reference's check and the loop are paid once.
+// What bounds it: 32 x 8 heads of up to 16384 take 69 us, 67 % of HBM's copy rate.
+// No unit is full (issue slots 60 % of the active clocks, tensor pipe 20 %): of a
+// warp's time a fifth is the fixed latencies of its chain of conversions, products
+// and exponentials, 16 % other warps' turns, 13 % the arithmetic pipes, 11 %
+// barriers, 5 % loads.  Two heads of 131072 take 20 us, of which 5 pass before the
+// first data and 7 in the joins.
 // The reference m of a row's exponentials stays kLift below the largest logit
 // when set and moves only when a logit passes it by kRange, so that the parts
 // keep their bits well above fp16's smallest numbers.

@@ -20,8 +20,8 @@
 // the stores of a warp fall on 32 distinct banks.  A tile is decoded once for
 // 256 rows.
 // What bounds it: 2048 rows of 8 query heads onto 34815 positions of two KV heads
-// take 430 us, 3300 clocks a tile of 256 rows, 2100 of them products (tensor pipe
-// 57 %; the rest of the time the products wait for decoded tiles and for P).  Their
+// take 428 us, 3300 clocks a tile of 256 rows, 2100 of them products (tensor pipe
+// 56 %; the rest of the time the products wait for decoded tiles and for P).  Their
 // operands (192 KB a tile) and the decoded stores (64 KB) share shared memory's 128
 // bytes a clock, and a piece takes its warp about 1080 clocks, with or without its
 // conversions, its loads or the softmax's exponentials.  Copies started by one
@@ -31,11 +31,12 @@
 // Tensor memory: S_g at columns 128 g (P_g, fp16, over its first 64), O_g at
 // 256 + 128 g.  MMA order of tile j: PV_0(j), S_0(j+1), PV_1(j), S_1(j+1); with one
 // row block S of the tiles in turn in both places and S(j+1) before PV(j), so that
-// a tile's softmax follows the one before without a pause (40 rows of 131072: 39 -> 34 us).
+// a tile's softmax follows the one before without a pause (40 rows of 131072: 39 -> 34 us
+// when it was built, 30 now).
 // fp16 outputs: probabilities are rounded to fp16 before they meet the values
 // (an output is off by 2.6e-4 of itself, 2-norm, 2.1e-4 of them the rounding of
 // the output); fp32 outputs: two fp16 parts (22 bits), half as many products
-// again.  Their sum is taken before the rounding, in fp32.
+// again (613 us for 428).  Their sum is taken before the rounding, in fp32.
 // The key tiles of pair blocks that do not fill the GPU are split over CTAs
 // (tile_split), whose unnormalised rows with their maximum and sum are joined
 // by a second kernel.

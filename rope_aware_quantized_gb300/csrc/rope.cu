@@ -24,7 +24,9 @@ struct FreqTable {
 };
 
 // Angles and functions in float64: a float32 product of a far position and a
-// frequency is off by whole radians' fractions (2^-24 of 10^6 rad).
+// frequency is off by whole radians' fractions (2^-24 of 10^6 rad).  Bound by the
+// 64-bit functions: 131072 positions take 478 us (their bytes 10), 4096 16 us; a
+// model's tables are made once.
 __global__ void __launch_bounds__(256) rope_table_kernel(FreqTable f, int64_t n_pos, double scale, float* cs, float* sn) {
     const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (at >= n_pos * kNB) return;
