@@ -95,3 +95,60 @@ def test_an_unmapped_page_is_reported_and_touches_no_other_sequence(t, page, hal
     c.lens, c.seq = [16, 500], i32([16, 500])
     out = c.run(half, status=st.zero_())
     assert st.item() == 0 and torch.equal(out[1], good[1])
+
+
+@pytest.mark.parametrize("t", [5, 40])  # 40 and 320 rows a head, whose tiles are split and joined
+@pytest.mark.parametrize("half", [False, True])
+def test_a_captured_call_with_parts_replayed(t, half):
+    """Lengths, queries and positions changed on the device between replays, eager calls with the same workspace between them."""
+    top = 6000
+    c = filled(3, 2, 8, t, [top, 1, 2000], 6016, 64, seed=t)
+    rope = bg.Rope(*bg.bgtq_rope_table(1e6 ** (-np.arange(64) / 64), 7000))
+    pos = torch.zeros((3, t), dtype=torch.int32, device="cuda")
+    ws = torch.zeros(bg.bgtq_fp4_attn_workspace(2, 8, 3, t, top), dtype=torch.uint8, device="cuda")
+    dtype = torch.float16 if half else torch.float32
+    out, two = (torch.empty((3, 16, t, 128), dtype=dtype, device="cuda") for _ in range(2))
+    st = status()
+
+    def call(o, **kw):
+        bg.bgtq_fp4_attn(c.q, c.cache, c.seq, top, o, ws, rope=rope, pos=pos, status=st, **kw)
+
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        call(out)
+        call(two, softmax_scale=0.01)
+    rng = np.random.default_rng(t)
+    for i in range(12):
+        lens = rng.integers(0, top + 1, 3)
+        lens[i % 3] = (0, 1, top, t, 128, 129)[i % 6]
+        c.seq.copy_(i32(lens))
+        pos.copy_(i32(rng.integers(0, 7000, (3, t))))
+        c.q.normal_()
+        graph.replay()
+        want, want2 = torch.empty_like(out), torch.empty_like(out)
+        call(want)
+        call(want2, softmax_scale=0.01)
+        assert torch.equal(out, want) and torch.equal(two, want2)
+        c.lens = lens.tolist()
+        if i % 4 == 2:
+            turned = torch.empty_like(c.q)
+            bg.bgtq_rope_rows(rope, pos, c.q, turned)
+            c.q.copy_(turned)
+            check(c, out, half, {(b, 5 * b + i % 5) for b in range(3) if lens[b]})
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("t", [1, 3, 20])
+def test_sequences_that_share_pages(t):
+    """Two sequences over the same pages of a prefix, and their own from there: the outputs of sequences with copies."""
+    c = Case(2, 4, t, [700, 700, 700], 704, 64, seed=t)
+    apart = c.cache.groups.clone()
+    P, table = c.cache.page_tokens // 16, c.cache.page_table
+    g = c.cache.groups.view(-1, 2 * P * F.GROUP_BYTES)  # a pool page a row
+    for i in range(8):
+        g[table[1, i].long()] = g[table[0, i].long()]
+    want = c.run(False)
+    c.cache.groups.copy_(apart)
+    table[1, :8] = table[0, :8]
+    assert torch.equal(c.run(False), want)
